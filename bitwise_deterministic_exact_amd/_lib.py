@@ -16,6 +16,12 @@ DET_PATH_AUTO, DET_PATH_ACCUMULATOR, DET_PATH_SLICES, DET_PATH_AUTO_HOST = 0, 1,
 NUM_DIGITS = 18
 LSB_EXPONENT = -298
 K_MAX = 1 << 19
+ROWS_MAX = 1 << 22
+HEAD_V_MAX = 1 << 24
+NORM_C_MAX = 32768
+NORM_SHARD_ROWS = 32
+TOP_MAX = 64
+ENTRIES_MAX = 1024
 
 _lib = None
 
@@ -55,6 +61,19 @@ def load() -> ctypes.CDLL:
         "det_check_finite": ([c_int, vp, i64, i64, i64, i64, vp, vp], c_int),
         "det_dot_partial": ([c_int, vp, i64, vp, i64, i64, vp, c_int, vp], c_int),
         "det_sqdiff_partial": ([c_int, vp, i64, vp, i64, i64, vp, c_int, vp], c_int),
+        "det_layer_norm": ([c_int, vp, i64, c_int, vp, vp, i64, i64, ctypes.c_double, c_int, vp, vp, vp, vp], c_int),
+        "det_layer_norm_grad_workspace_bytes": ([i64, i64], i64),
+        "det_layer_norm_grad": ([c_int, vp, i64, c_int, vp, i64, c_int, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp,
+                                 ctypes.c_size_t, vp], c_int),
+        "det_head_workspace_bytes": ([i64, i64, c_int], i64),
+        "det_token_logprobs": ([c_int, vp, i64, i64, i64, ctypes.c_double, vp, i64, i64, c_int, vp, vp, vp, vp, vp,
+                                vp, ctypes.c_size_t, vp], c_int),
+        "det_token_logprobs_grad": ([c_int, vp, i64, i64, i64, ctypes.c_double, vp, i64, i64, c_int, vp, vp, vp, i64,
+                                     vp, i64, vp, i64, i64, vp, i64, vp], c_int),
+        "det_distill": ([c_int, vp, i64, i64, i64, ctypes.c_double, c_int, vp, i64, vp, i64, i64, vp, vp, vp, vp,
+                         ctypes.c_size_t, vp], c_int),
+        "det_distill_grad": ([c_int, vp, i64, i64, i64, ctypes.c_double, vp, i64, i64, vp, vp, vp, i64, vp, i64, vp],
+                             c_int),
         "det_set_gemm_path": ([c_int, c_int], c_int),
         "det_set_kernel_events": ([vp, vp], None),
         "det_device_status": ([vp, c_int, ctypes.POINTER(c_int)], c_int),

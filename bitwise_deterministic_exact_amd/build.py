@@ -7,7 +7,7 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", "detgemm.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("detgemm.hip", "head.hip", "norm.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdetgemm.so")
 # the benchmark's LDS-atomic peak probe: its own library, never loaded by the package
@@ -29,7 +29,7 @@ def hipcc() -> str:
 
 
 def _hipcc(sources, out: str, verbose: bool) -> str:
-    cmd = [hipcc(), *HIPCC_FLAGS, "-o", out + ".tmp", *sources]
+    cmd = [hipcc(), *HIPCC_FLAGS, f"-parallel-jobs={min(len(sources), 4)}", "-o", out + ".tmp", *sources]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -49,11 +49,11 @@ def build(verbose: bool = False) -> str:
     return _hipcc(SOURCES, LIB, verbose)
 
 
-def device_asm(out_path: str) -> str:
-    """Write the gfx950 assembly of the kernels (for inspection)."""
+def device_asm(out_path: str, source: str = SOURCES[0]) -> str:
+    """Write the gfx950 assembly of one source's kernels (for inspection)."""
     cmd = [hipcc(), "-O3", "-std=c++17", f"--offload-arch={ARCH}", "--cuda-device-only", "-S",
            "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", f"-I{INCLUDE}",
-           "-o", out_path, *SOURCES]
+           "-o", out_path, source]
     subprocess.run(cmd, check=True, capture_output=True)
     return out_path
 

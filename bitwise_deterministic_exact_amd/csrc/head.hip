@@ -1,0 +1,758 @@
+// The losses and scores of a language model's head for MI355X (gfx950): log
+// probabilities of given tokens with entropy and top alternatives, and the
+// distillation loss against a teacher's top logits, each with its gradient.
+//
+// For a row z of V logits and a scale s > 0 (1 / temperature):
+//   l_j = s z_j - ln sum_i exp(s z_i),   p_j = exp(l_j)
+//   logprob = l_t,   entropy H = -sum_j p_j l_j
+//   loss = T^2 sum_k q_k (ln q_k - l_{i_k}),  q = softmax(teacher / T), s = 1/T
+// and the gradients
+//   dz_j = s (sum of the incoming gradients of j's own log probabilities
+//             - p_j (G + gH (H + l_j))),  G = all of those gradients' sum
+//   dz_j = g T (p_j - sum_{k: i_k = j} q_k)
+//
+// Everything is one pass over the logits: a wave takes a chunk of 2048
+// consecutive logits into registers, finds its maximum m, and forms
+// S = sum 2^(c (z - m)) and U = sum c (z - m) 2^(c (z - m)), c = s log2 e.
+// The chunks' (m, S, U) are joined in 64 bits in chunk order.  The chunks are
+// cut by V alone, so a row's bits are a function of that row: not of the
+// batch, of how many workgroups share a row, or of the alignment.
+#include <algorithm>
+
+#include "rowops.h"
+
+namespace {
+
+using namespace rowops;
+
+constexpr int CHUNK = 2048;               // logits per wave and step
+constexpr int LANE_ELEMS = CHUNK / 64;    // 32 in registers per lane
+constexpr int WAVES = 4;                  // per workgroup
+constexpr int TOP_MAX = 64;               // alternatives per row: one per lane
+constexpr int ENTRIES_MAX = 1024;         // teacher entries per row
+constexpr int LDS_PARTS = 512;            // chunks of a row whose (m, S, U) fit one workgroup's LDS
+constexpr double LOG2E = 1.4426950408889634074, LN2 = 0.69314718055994530942;
+
+constexpr int MODE_SCORE = 0, MODE_DISTILL = 1;
+
+struct ScoreArgs {
+  const void* z; int64_t s_row;
+  int64_t N, V;
+  float c;                                // s log2 e
+  double scale;                           // s
+  int dt, mode;
+  int nchunk;                             // ceil(V / CHUNK)
+  int wpr;                                // waves of a workgroup that share a row (1, 2, 4)
+  int nblk;                               // workgroups that share a row (> 1 only with wpr = 4)
+  int top, cap;                           // alternatives; candidates a wave's pool holds
+  // workspace of a row shared by several workgroups
+  float* parts;                           // [N][nchunk][3]
+  uint64_t* lists;                        // [N][nblk][top]
+  // score
+  const int64_t* target; int64_t s_target;
+  int64_t ignore;
+  float* logprob; float* entropy;
+  int64_t* top_index; float* top_value;
+  // distill
+  const void* teacher; int64_t s_teacher; int tdt;
+  const int64_t* entry; int64_t s_entry;
+  int K;
+  float* q;                               // [N][K]
+  float* loss;
+  float4* stat;                           // [N]: m, 1/S, log2 S, H
+  int32_t* status;
+};
+
+// ---------------------------------------------------------------- order keys
+//
+// (value, index) as one integer whose order is "larger value first, then lower
+// index": the float's bits mapped to an order-preserving integer (-0 as +0)
+// above the complement of the index.  Keys of a row are distinct, so the top
+// k are one set whatever the order in which candidates are found.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) {
+  return (static_cast<uint64_t>(order) << 32) | (0xFFFFFFFFu - index);
+}
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v)), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v >> 32)), lane);
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+// The largest `want` of the n keys in LDS at pool[0..n), sorted, into out (not
+// overlapping the pool), by `lanes` threads numbered `t` (all of a wave, or of a workgroup): each key's
+// rank is the number of larger keys.  n^2 / lanes broadcast reads: n is close
+// to `want` except for rows built against it.
+__device__ __forceinline__ void rank_keys(const uint64_t* pool, int n, uint64_t* out, int want, int t, int lanes) {
+  for (int e = t; e < n; e += lanes) {
+    const uint64_t mine = pool[e];
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) rank += pool[i] > mine ? 1 : 0;
+    if (rank < want) out[rank] = mine;
+  }
+}
+
+// ---------------------------------------------------------------- one chunk
+
+template <int DT>
+__device__ __forceinline__ void load_chunk(const void* row, int64_t base, int64_t V, int lane,
+                                           float (&v)[LANE_ELEMS]) {
+  constexpr int VE = Elem<DT>::VE, NV = LANE_ELEMS / VE;
+  if (base + CHUNK <= V) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      load_vec<DT, VE>(row, base + (i * 64 + lane) * VE, reinterpret_cast<float (&)[VE]>(v[i * VE]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t at = base + (i * 64 + lane) * VE;
+      if (at + VE <= V) {
+        load_vec<DT, VE>(row, at, reinterpret_cast<float (&)[VE]>(v[i * VE]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[i * VE + j] = at + j < V ? load_elem<DT>(row, at + j) : -INFINITY;
+      }
+    }
+  }
+}
+
+// A wave's running list of its row's largest keys, in its part of the LDS:
+// `list` (top keys, sorted, L of them) and `pool` (list + candidates).
+//
+// A chunk's candidates are the elements above the list's last value (later
+// indices lose ties).  While the list is short, or when a chunk has more
+// candidates than the pool holds, the bar is raised first: each lane's largest
+// (value, vector) is a lower bound for one distinct element, so the top-th
+// largest of the 64 lane bests is a bar that at least `top` elements reach,
+// and all that reach it lie in `top` lanes, 32 elements each: the pool's size.
+template <int DT>
+struct TopList {
+  static constexpr int VE = Elem<DT>::VE, NV = LANE_ELEMS / VE;
+  uint64_t* pool;
+  uint64_t* list;
+  int top, cap, L;
+  float bar;                             // the list's last value once it is full
+
+  __device__ __forceinline__ int append(const float (&v)[LANE_ELEMS], const float (&vmax)[NV], int64_t base,
+                                        int64_t V, int lane, bool full, uint64_t floor_key) {
+    const uint32_t fo = static_cast<uint32_t>(floor_key >> 32);
+    const float fv = floor_key == 0 ? -INFINITY : order_value(fo);
+    const uint32_t fvec = 0xFFFFFFFFu - static_cast<uint32_t>(floor_key);
+    int n = L;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t vec = i * 64 + lane;
+      // at the floor's value only vectors up to the floor's count
+      const bool some = (!full || vmax[i] > bar) && (vmax[i] > fv || (vmax[i] == fv && vec <= fvec));
+      if (__ballot(some) == 0) continue;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float x = v[i * VE + j];
+        const int64_t at = base + static_cast<int64_t>(vec) * VE + j;
+        const bool in = at < V && (!full || x > bar) && (x > fv || (x == fv && vec <= fvec));
+        const uint64_t b = __ballot(in);
+        if (b == 0) continue;
+        const int pos = n + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32),
+                                                      __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), 0));
+        if (in && pos < cap) pool[pos] = key_of(order_bits(x), static_cast<uint32_t>(at));
+        n += __popcll(b);
+      }
+    }
+    return n;
+  }
+
+  __device__ __forceinline__ uint64_t raise(const float (&vmax)[NV], float lane_max, int64_t base, int64_t V,
+                                            int lane) const {
+    uint32_t first = 0;
+#pragma unroll
+    for (int i = NV - 1; i >= 0; --i)
+      if (vmax[i] == lane_max) first = i * 64 + lane;
+    const uint64_t mine = base + static_cast<int64_t>(lane) * VE < V ? key_of(order_bits(lane_max), first) : 0;
+    if (__popcll(__ballot(mine != 0)) < top) return 0;
+    int rank = 0;
+#pragma unroll 4
+    for (int l = 0; l < 64; ++l) rank += lane_u64(mine, l) > mine ? 1 : 0;
+    const uint64_t hit = __ballot(mine != 0 && rank == top - 1);
+    return lane_u64(mine, __builtin_ctzll(hit));
+  }
+
+  __device__ __forceinline__ void add(const float (&v)[LANE_ELEMS], const float (&vmax)[NV], float lane_max,
+                                      int64_t base, int64_t V, int lane) {
+    const bool full = L == top;
+    if (full && __ballot(lane_max > bar) == 0) return;
+    int n = cap + 1;
+    if (full) n = append(v, vmax, base, V, lane, true, 0);
+    if (n > cap) n = append(v, vmax, base, V, lane, full, raise(vmax, lane_max, base, V, lane));
+    if (n > cap) n = cap;                // cannot be: the raised bar leaves at most 32 top candidates
+    wave_sync();
+    rank_keys(pool, n, list, top, lane, 64);
+    wave_sync();
+    L = n < top ? n : top;
+    for (int e = lane; e < L; e += 64) pool[e] = list[e];
+    wave_sync();
+    if (L == top) bar = order_value(static_cast<uint32_t>(list[top - 1] >> 32));
+  }
+};
+
+// ---------------------------------------------------------------- a row's end
+//
+// One wave joins a row's chunk sums in 64 bits and writes the row's results.
+// Conventions: a row of nothing but -inf has log probabilities -inf, entropy
+// 0 and probabilities 0; a NaN or +inf makes S NaN and with it every result.
+struct RowSums {
+  float m;                               // the maximum (0 for an empty row)
+  double log2s;                          // log2 S (0 for an empty row)
+  bool empty, bad;
+};
+
+__device__ __forceinline__ RowSums join(const ScoreArgs& a, const float* parts, int64_t row, int lane) {
+  float m = -INFINITY;
+  bool nan = false;
+  for (int i = lane; i < a.nchunk; i += 64) {
+    m = fmaxf(m, parts[3 * i]);
+    nan |= parts[3 * i + 1] != parts[3 * i + 1];
+  }
+  m = wave_max(m);
+  RowSums r;
+  r.bad = __ballot(nan) != 0;
+  r.empty = m == -INFINITY && !r.bad;
+  r.m = m == -INFINITY ? 0.0f : m;
+  double S = 0.0, U = 0.0;
+  const double c = a.scale * LOG2E;
+  for (int i = lane; i < a.nchunk; i += 64) {
+    const float mi = parts[3 * i];
+    if (mi == -INFINITY) continue;
+    const double d = (static_cast<double>(mi) - static_cast<double>(r.m)) * c;
+    const double f = exp2(d), s = parts[3 * i + 1];
+    if (f > 0.0) {
+      S += s * f;
+      U += f * (parts[3 * i + 2] + d * s);
+    }
+  }
+  S = wave_sum(S);
+  U = wave_sum(U);
+  r.log2s = r.empty ? 0.0 : log2(S);
+  double H = r.empty ? 0.0 : LN2 * (r.log2s - U / S);
+  if (H < 0.0) H = 0.0;                  // rounding of the 32-bit chunk sums
+  if (r.bad) { r.log2s = NAN; H = NAN; }
+  if (lane == 0) {
+    a.stat[row] = make_float4(r.m, r.empty ? 0.0f : (r.bad ? NAN : static_cast<float>(1.0 / S)),
+                              static_cast<float>(r.log2s), static_cast<float>(H));
+    if (a.entropy != nullptr) a.entropy[row] = static_cast<float>(H);
+    if (r.bad) a.status[0] = 1;
+  }
+  return r;
+}
+
+__device__ __forceinline__ double log_prob(const ScoreArgs& a, const RowSums& r, float z) {
+  return (static_cast<double>(z) - static_cast<double>(r.m)) * a.scale - LN2 * r.log2s;
+}
+
+// the row's alternatives from its sorted keys (fewer than `top` only in a bad row)
+__device__ __forceinline__ void write_top(const ScoreArgs& a, const RowSums& r, int64_t row, const uint64_t* list,
+                                          int t) {
+  if (t >= a.top) return;
+  const uint64_t key = list[t];
+  a.top_index[row * a.top + t] = r.bad ? -1 : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+  a.top_value[row * a.top + t] =
+      r.bad ? NAN : static_cast<float>(log_prob(a, r, order_value(static_cast<uint32_t>(key >> 32))));
+}
+
+__device__ __forceinline__ void finish_score(const ScoreArgs& a, const RowSums& r, int64_t row, int lane) {
+  if (lane != 0 || a.target == nullptr) return;
+  const int64_t t = a.target[row * a.s_target];
+  float lp;
+  if (t == a.ignore) lp = 0.0f;
+  else if (t < 0 || t >= a.V || r.bad) lp = NAN;
+  else lp = static_cast<float>(log_prob(a, r, load_elem(a.dt, a.z, row * a.s_row + t)));
+  a.logprob[row] = lp;
+}
+
+__device__ __forceinline__ void finish_distill(const ScoreArgs& a, const RowSums& r, int64_t row, int lane) {
+  // q in 64 bits: K is small beside V
+  const int64_t t0 = row * a.s_teacher, e0 = row * a.s_entry;
+  float m = -INFINITY;
+  bool nan = false;
+  for (int k = lane; k < a.K; k += 64) {
+    const float t = load_elem(a.tdt, a.teacher, t0 + k);
+    nan |= !(t < INFINITY);              // NaN or +inf
+    m = fmaxf(m, t);
+  }
+  m = wave_max(m);
+  const bool bad = __ballot(nan) != 0;
+  const bool none = m == -INFINITY;      // no entry at all: loss and gradient 0
+  double sum = 0.0;
+  for (int k = lane; k < a.K; k += 64) {
+    const float t = load_elem(a.tdt, a.teacher, t0 + k);
+    if (t > -INFINITY) sum += exp((static_cast<double>(t) - m) * a.scale);
+  }
+  sum = wave_sum(sum);
+  const double lsum = none ? 0.0 : log(sum), inv = none ? 0.0 : 1.0 / sum;
+  double loss = 0.0;
+  for (int k = lane; k < a.K; k += 64) {
+    const float t = load_elem(a.tdt, a.teacher, t0 + k);
+    float qk = 0.0f;
+    if (t > -INFINITY) {
+      const double d = (static_cast<double>(t) - m) * a.scale;
+      const double q = exp(d) * inv;
+      qk = static_cast<float>(q);
+      if (q > 0.0) {
+        const int64_t i = a.entry[e0 + k];
+        if (i < 0 || i >= a.V) loss = NAN;
+        else loss += q * (d - lsum - log_prob(a, r, load_elem(a.dt, a.z, row * a.s_row + i)));
+      }
+    }
+    a.q[row * a.K + k] = bad ? NAN : qk;
+  }
+  loss = wave_sum(loss);
+  if (lane == 0) {
+    a.loss[row] = (bad || r.bad) ? NAN : static_cast<float>(loss / (a.scale * a.scale));
+    if (bad) a.status[0] = 1;
+  }
+}
+
+// ---------------------------------------------------------------- the pass
+//
+// Wave w of a row (of nblk * wpr) takes chunks w, w + nblk * wpr, ...  With
+// one workgroup per row (nblk = 1) its first wave also finishes the row; rows
+// of at most one or two chunks share a workgroup (wpr = 1, 2).
+template <int DT, bool TOP>
+__global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
+  constexpr int VE = Elem<DT>::VE, NV = LANE_ELEMS / VE;
+  extern __shared__ __align__(16) uint64_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rpb = WAVES / a.wpr;                              // rows per workgroup
+  const int64_t blk = blockIdx.x;
+  const int64_t row = a.nblk > 1 ? blk / a.nblk : blk * rpb + wave / a.wpr;
+  const int part = a.nblk > 1 ? static_cast<int>(blk % a.nblk) : 0;
+  const int rw = wave % a.wpr;                                // this wave within the row and workgroup
+  const bool live = row < a.N;
+  const bool whole = a.nblk == 1;
+  // LDS: per wave a pool (cap) and a list (top); then the rows' chunk sums
+  const int per_wave = a.cap + a.top;
+  uint64_t* const pool = lds + wave * per_wave;
+  uint64_t* const list = pool + a.cap;
+  float* const lparts = reinterpret_cast<float*>(lds + WAVES * per_wave);
+  float* const parts = whole ? lparts + (wave / a.wpr) * a.nchunk * 3 : a.parts + row * a.nchunk * 3;
+
+  TopList<DT> tl{pool, list, a.top, a.cap, 0, 0.0f};
+  if (live) {
+    const void* const zr = static_cast<const char*>(a.z) + row * a.s_row * Elem<DT>::BYTES;
+    for (int ch = part * a.wpr + rw; ch < a.nchunk; ch += a.nblk * a.wpr) {
+      const int64_t base = static_cast<int64_t>(ch) * CHUNK;
+      float v[LANE_ELEMS];
+      load_chunk<DT>(zr, base, a.V, lane, v);
+      float vmax[NV], lane_max = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        vmax[i] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) vmax[i] = fmaxf(vmax[i], v[i * VE + j]);
+        lane_max = fmaxf(lane_max, vmax[i]);
+      }
+      const float m = wave_max(lane_max);
+      const float ref = m == -INFINITY ? 0.0f : m;
+      float s = 0.0f, u = 0.0f;
+#pragma unroll
+      for (int j = 0; j < LANE_ELEMS; ++j) {
+        const float d = (v[j] - ref) * a.c;
+        const float e = __builtin_amdgcn_exp2f(d);
+        s += e;
+        u += e * d;
+      }
+      if (u != u && s == s) {            // 0 * -inf: masked logits add nothing
+        u = 0.0f;
+#pragma unroll
+        for (int j = 0; j < LANE_ELEMS; ++j) {
+          const float d = (v[j] - ref) * a.c;
+          u += __builtin_amdgcn_exp2f(d) * fmaxf(d, -2000.0f);
+        }
+      }
+      s = wave_sum(s);
+      u = wave_sum(u);
+      if (lane == 0) {
+        parts[3 * ch] = m;
+        parts[3 * ch + 1] = s;
+        parts[3 * ch + 2] = u;
+      }
+      if constexpr (TOP) tl.add(v, vmax, lane_max, base, a.V, lane);
+    }
+    if constexpr (TOP)
+      for (int e = tl.L + lane; e < a.top; e += 64) list[e] = 0;     // a wave with few elements
+  }
+  __syncthreads();
+  if (!live) return;
+  if (TOP && a.wpr > 1 && rw == 0) {
+    // the row's wave lists, gathered into this wave's pool (cap >= wpr * top), joined
+    for (int w = 0; w < a.wpr; ++w)
+      if (lane < a.top) pool[w * a.top + lane] = lds[(wave + w) * per_wave + a.cap + lane];
+    wave_sync();
+    if (lane < a.top) list[lane] = 0;    // a workgroup may hold fewer than `top` elements
+    wave_sync();
+    rank_keys(pool, a.wpr * a.top, list, a.top, lane, 64);
+    wave_sync();
+  }
+  if (rw != 0) return;
+  if (!whole) {
+    if (TOP && lane < a.top) a.lists[(row * a.nblk + part) * a.top + lane] = list[lane];
+    return;
+  }
+  const RowSums r = join(a, parts, row, lane);
+  if (a.mode == MODE_DISTILL) finish_distill(a, r, row, lane);
+  else finish_score(a, r, row, lane);
+  if constexpr (TOP) write_top(a, r, row, list, lane);
+}
+
+// The end of rows that several workgroups shared: one workgroup per row.
+__global__ __launch_bounds__(256) void k_score_join(ScoreArgs a) {
+  extern __shared__ __align__(16) uint64_t lds[];
+  const int64_t row = blockIdx.x;
+  const int n = a.nblk * a.top;
+  if (a.top > 0) {
+    for (int e = threadIdx.x; e < n; e += 256) lds[e] = a.lists[row * n + e];
+    __syncthreads();
+    rank_keys(lds, n, lds + n, a.top, threadIdx.x, 256);
+    __syncthreads();
+  }
+  if (threadIdx.x >= 64) return;
+  const int lane = threadIdx.x;
+  const RowSums r = join(a, a.parts + row * a.nchunk * 3, row, lane);
+  if (a.mode == MODE_DISTILL) finish_distill(a, r, row, lane);
+  else finish_score(a, r, row, lane);
+  if (a.top > 0) write_top(a, r, row, lds + n, lane);
+}
+
+// ---------------------------------------------------------------- gradients
+//
+// Reads the logits once and writes their gradient once; p_j = 2^(c (z_j - m))
+// / S from the saved (m, 1/S).  The few elements with a gradient of their own
+// (the target, the alternatives, the teacher's entries) are written again
+// after a barrier, each by one thread, with equal indices added in list order.
+struct GradArgs {
+  const void* z; int64_t s_row;
+  int64_t N, V;
+  float c, scale;
+  int dt, mode;
+  int nchunk, nblk;
+  const float4* stat;
+  void* dz; int64_t s_dz;
+  // score: gradients of logprob, entropy (or null) and alternatives (or null)
+  const int64_t* target; int64_t s_target; int64_t ignore;
+  const float* glp; int64_t s_glp;
+  const float* gent; int64_t s_gent;
+  const float* gtop; int64_t s_gtop, s_gtop_k;
+  const int64_t* top_index; int top;
+  // distill: gradient of the loss
+  const float* g; int64_t s_g;
+  const float* q;
+  const int64_t* entry; int64_t s_entry; int K;
+};
+
+struct GradRow {
+  float c, m, inv, l2s;                  // p = 2^(c (z - m)) inv, ln p = ln2 (c (z - m) - l2s)
+  float A, B;                            // dz = p (A + B log2 p)
+};
+
+template <bool ENT>
+__device__ __forceinline__ float grad_elem(const GradRow& r, float z) {
+  const float t = (z - r.m) * r.c;
+  const float p = __builtin_amdgcn_exp2f(t) * r.inv;
+  if constexpr (ENT) return p * fmaf(r.B, fmaxf(t - r.l2s, -2000.0f), r.A);
+  else return p * r.A;
+}
+
+template <int DT, bool ENT>
+__global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
+  constexpr int VE = Elem<DT>::VE, NV = LANE_ELEMS / VE;
+  extern __shared__ __align__(16) int32_t lds_i[];            // entry indices, then their gradients
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = blockIdx.x / a.nblk;
+  const int part = static_cast<int>(blockIdx.x % a.nblk);
+  const int n = a.mode == MODE_DISTILL ? a.K : 1 + a.top;
+  float* const lds_w = reinterpret_cast<float*>(lds_i + n);
+
+  // the row's entries; an index outside [0, V) adds nothing
+  const float4 st = a.stat[row];
+  float G = 0.0f;
+  for (int e = threadIdx.x; e < n; e += 64 * WAVES) {
+    int64_t i;
+    float w;
+    if (a.mode == MODE_DISTILL) {
+      i = a.entry[row * a.s_entry + e];
+      w = a.q[row * a.K + e];
+      w = w > 0.0f || w != w ? -w * a.g[row * a.s_g] / a.scale : 0.0f;
+    } else if (e == 0) {
+      i = a.target != nullptr ? a.target[row * a.s_target] : -1;
+      w = i == a.ignore || a.glp == nullptr ? 0.0f : a.glp[row * a.s_glp];
+      if (i == a.ignore) i = -1;
+    } else {
+      i = a.top_index[row * a.top + e - 1];
+      w = a.gtop != nullptr ? a.gtop[row * a.s_gtop + (e - 1) * a.s_gtop_k] : 0.0f;
+    }
+    const bool in = i >= 0 && i < a.V;
+    lds_i[e] = in ? static_cast<int32_t>(i) : -1;
+    lds_w[e] = in ? w : 0.0f;
+  }
+  __syncthreads();
+  GradRow r;
+  r.c = a.c;
+  r.m = st.x; r.inv = st.y; r.l2s = st.z;
+  if (a.mode == MODE_DISTILL) {
+    // sum q = 1, or 0 for a row without entries
+    float some = 0.0f;
+    for (int e = 0; e < n; ++e) some += lds_w[e] != 0.0f ? 1.0f : 0.0f;
+    r.A = some > 0.0f ? a.g[row * a.s_g] / a.scale : 0.0f;
+    r.B = 0.0f;
+  } else {
+    for (int e = 0; e < n; ++e) G += lds_w[e];
+    const float gent = a.gent != nullptr ? a.gent[row * a.s_gent] : 0.0f;
+    r.A = -a.scale * (G + gent * st.w);
+    r.B = -a.scale * gent * static_cast<float>(LN2);
+  }
+
+  const void* const zr = static_cast<const char*>(a.z) + row * a.s_row * Elem<DT>::BYTES;
+  void* const dr = static_cast<char*>(a.dz) + row * a.s_dz * Elem<DT>::BYTES;
+  for (int ch = part * WAVES + wave; ch < a.nchunk; ch += a.nblk * WAVES) {
+    const int64_t base = static_cast<int64_t>(ch) * CHUNK;
+    float v[LANE_ELEMS];
+    load_chunk<DT>(zr, base, a.V, lane, v);
+#pragma unroll
+    for (int j = 0; j < LANE_ELEMS; ++j) v[j] = grad_elem<ENT>(r, v[j]);
+    const bool full = base + CHUNK <= a.V;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t at = base + (i * 64 + lane) * VE;
+      if (full || at + VE <= a.V) {
+        store_vec<DT, VE>(dr, at, reinterpret_cast<const float (&)[VE]>(v[i * VE]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          if (at + j < a.V) store_elem<DT>(dr, at + j, v[i * VE + j]);
+      }
+    }
+  }
+  __syncthreads();                        // the chunks' stores before the entries'
+  if (st.y == 0.0f) return;               // an empty row has no gradient at all
+  const float ws = a.mode == MODE_DISTILL ? 1.0f : a.scale;
+  for (int e = threadIdx.x; e < n; e += 64 * WAVES) {
+    const int i = lds_i[e];
+    if (i < 0 || (i / CHUNK / WAVES) % a.nblk != part) continue;
+    float w = 0.0f;
+    bool first = true;
+    for (int k = 0; k < n; ++k) {
+      if (lds_i[k] != i) continue;
+      if (k < e) first = false;
+      w += lds_w[k];
+    }
+    if (first) store_elem<DT>(dr, i, grad_elem<ENT>(r, load_elem<DT>(zr, i)) + w * ws);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+// Workgroups per row: one when the rows alone give every CU four workgroups
+// (then the row is finished in the same launch), else enough to do so, or as many
+// as the row has groups of four chunks.
+int blocks_per_row(int64_t N, int64_t nchunk) {
+  int64_t b = 1;
+  if (N < 1024) b = std::min(ceil_div(nchunk, WAVES), ceil_div(1024, N > 0 ? N : 1));
+  if (nchunk > LDS_PARTS && b == 1) b = 2;                    // the sums go through the workspace
+  return static_cast<int>(b);
+}
+
+int64_t score_ws_bytes(int64_t N, int64_t V, int top) {
+  const int64_t nchunk = ceil_div(V, CHUNK);
+  const int nblk = blocks_per_row(N, nchunk);
+  if (nblk == 1) return 0;
+  return N * (nblk * static_cast<int64_t>(top) * 8 + nchunk * 12);
+}
+
+det_status check_logits(int dt, const void* z, int64_t N, int64_t V, int64_t s_row, double scale) {
+  if (!known_dtype(dt)) return fail(DET_EDTYPE, "unknown dtype %d", dt);
+  if (N < 0 || V < 1 || s_row < 0) return fail(DET_EINVAL, "bad size or stride: N=%lld V=%lld stride=%lld",
+                                              (long long)N, (long long)V, (long long)s_row);
+  if (V > DET_HEAD_V_MAX) return fail(DET_EINVAL, "V = %lld exceeds the limit 2^24", (long long)V);
+  if (N > DET_ROWS_MAX) return fail(DET_EINVAL, "N = %lld exceeds the limit 2^22 rows per call", (long long)N);
+  if (!(scale > 0.0) || !(scale < 1e6) || scale < 1e-6) return fail(DET_EINVAL, "the scale must lie in [1e-6, 1e6)");
+  if (N == 0) return DET_OK;
+  if (z == nullptr) return fail(DET_EINVAL, "null logits");
+  if (!aligned_for(z, dt)) return fail(DET_EINVAL, "logits must be aligned to their element size");
+  return DET_OK;
+}
+
+det_status launch_score(ScoreArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
+  a.nchunk = static_cast<int>(ceil_div(a.V, CHUNK));
+  a.nblk = blocks_per_row(a.N, a.nchunk);
+  a.wpr = a.nchunk >= WAVES ? WAVES : a.nchunk;
+  if (a.wpr == 3) a.wpr = 4;
+  a.cap = a.top > 0 ? (LANE_ELEMS + 1) * a.top : 0;
+  a.status = det_device_status_word();
+  if (a.status == nullptr) return DET_EHIP;
+  if (a.nblk > 1) {
+    a.wpr = WAVES;
+    const int64_t need = score_ws_bytes(a.N, a.V, a.top);
+    if (ws == nullptr || !aligned8(ws) || ws_bytes < static_cast<size_t>(need))
+      return fail(DET_EINVAL, "workspace: %lld bytes, 8-byte aligned, are needed", (long long)need);
+    a.lists = static_cast<uint64_t*>(ws);
+    a.parts = reinterpret_cast<float*>(a.lists + a.N * a.nblk * a.top);
+  }
+  const int rpb = WAVES / a.wpr;
+  const int64_t blocks = a.nblk > 1 ? a.N * a.nblk : ceil_div(a.N, rpb);
+  const size_t lds = static_cast<size_t>(WAVES) * (a.cap + a.top) * 8 +
+                     (a.nblk > 1 ? 0 : static_cast<size_t>(rpb) * a.nchunk * 12);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * WAVES);
+  if (a.dt == DET_F32) {
+    if (a.top > 0) hipLaunchKernelGGL((k_score<DET_F32, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_score<DET_F32, false>), grid, block, lds, s, a);
+  } else {
+    if (a.top > 0) hipLaunchKernelGGL((k_score<DET_BF16, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_score<DET_BF16, false>), grid, block, lds, s, a);
+  }
+  det_status st = hip_check(hipGetLastError(), "score launch");
+  if (st != DET_OK || a.nblk == 1) return st;
+  const size_t jl = static_cast<size_t>(a.nblk + 1) * a.top * 8;
+  hipLaunchKernelGGL(k_score_join, dim3(static_cast<unsigned>(a.N)), dim3(256), jl, s, a);
+  return hip_check(hipGetLastError(), "score join launch");
+}
+
+det_status launch_grad(GradArgs a, hipStream_t s) {
+  a.nchunk = static_cast<int>(ceil_div(a.V, CHUNK));
+  a.nblk = blocks_per_row(a.N, a.nchunk);
+  const int n = a.mode == MODE_DISTILL ? a.K : 1 + a.top;
+  const dim3 grid(static_cast<unsigned>(a.N * a.nblk)), block(64 * WAVES);
+  const size_t lds = static_cast<size_t>(n) * 8;
+  const bool ent = a.gent != nullptr;
+  if (a.dt == DET_F32) {
+    if (ent) hipLaunchKernelGGL((k_score_grad<DET_F32, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_score_grad<DET_F32, false>), grid, block, lds, s, a);
+  } else {
+    if (ent) hipLaunchKernelGGL((k_score_grad<DET_BF16, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_score_grad<DET_BF16, false>), grid, block, lds, s, a);
+  }
+  return hip_check(hipGetLastError(), "gradient launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t det_head_workspace_bytes(int64_t N, int64_t V, int top) {
+  if (N <= 0 || V <= 0 || top < 0 || N > DET_ROWS_MAX || V > DET_HEAD_V_MAX || top > TOP_MAX) return 0;
+  return score_ws_bytes(N, V, top);
+}
+
+det_status det_token_logprobs(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double scale,
+                              const int64_t* target, int64_t s_target, int64_t ignore, int top, float* logprob,
+                              float* entropy, float* stat, int64_t* top_index, float* top_logprob, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  det_status st = check_logits(dt, z, N, V, s_row, scale);
+  if (st != DET_OK) return st;
+  if (top < 0 || top > TOP_MAX || top > V)
+    return fail(DET_EINVAL, "top = %d must lie in 0..min(%d, V)", top, TOP_MAX);
+  if (s_target < 0) return fail(DET_EINVAL, "negative target stride");
+  if (N == 0) return DET_OK;
+  if (stat == nullptr || (target != nullptr && logprob == nullptr) ||
+      (top > 0 && (top_index == nullptr || top_logprob == nullptr)))
+    return fail(DET_EINVAL, "null output");
+  if (!aligned8(target) || !aligned8(top_index) || (reinterpret_cast<uintptr_t>(stat) & 15u) ||
+      ((reinterpret_cast<uintptr_t>(logprob) | reinterpret_cast<uintptr_t>(entropy) |
+        reinterpret_cast<uintptr_t>(top_logprob)) & 3u))
+    return fail(DET_EINVAL, "misaligned target or output");
+  ScoreArgs a{};
+  a.z = z; a.s_row = s_row; a.N = N; a.V = V; a.dt = dt; a.mode = MODE_SCORE;
+  a.scale = scale; a.c = static_cast<float>(scale * LOG2E);
+  a.top = top;
+  a.target = target; a.s_target = s_target; a.ignore = ignore;
+  a.logprob = logprob; a.entropy = entropy; a.stat = reinterpret_cast<float4*>(stat);
+  a.top_index = top_index; a.top_value = top_logprob;
+  return launch_score(a, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+det_status det_token_logprobs_grad(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double scale,
+                                   const int64_t* target, int64_t s_target, int64_t ignore, int top,
+                                   const int64_t* top_index, const float* stat, const float* g_logprob,
+                                   int64_t s_g_logprob, const float* g_entropy, int64_t s_g_entropy,
+                                   const float* g_top, int64_t s_g_top, int64_t s_g_top_k, void* dz, int64_t s_dz,
+                                   void* stream) {
+  det_status st = check_logits(dt, z, N, V, s_row, scale);
+  if (st != DET_OK) return st;
+  if (top < 0 || top > TOP_MAX || top > V)
+    return fail(DET_EINVAL, "top = %d must lie in 0..min(%d, V)", top, TOP_MAX);
+  if (s_target < 0 || s_g_logprob < 0 || s_g_entropy < 0 || s_g_top < 0 || s_g_top_k < 0 || s_dz < V)
+    return fail(DET_EINVAL, "negative stride, or gradient rows that overlap");
+  if (N == 0) return DET_OK;
+  if (stat == nullptr || dz == nullptr || (g_logprob != nullptr && target == nullptr) ||
+      (top > 0 && top_index == nullptr))
+    return fail(DET_EINVAL, "null pointer");
+  if (!aligned_for(dz, dt) || !aligned8(target) || !aligned8(top_index) || (reinterpret_cast<uintptr_t>(stat) & 15u) ||
+      ((reinterpret_cast<uintptr_t>(g_logprob) | reinterpret_cast<uintptr_t>(g_entropy) |
+        reinterpret_cast<uintptr_t>(g_top)) & 3u))
+    return fail(DET_EINVAL, "misaligned pointer");
+  GradArgs a{};
+  a.z = z; a.s_row = s_row; a.N = N; a.V = V; a.dt = dt; a.mode = MODE_SCORE;
+  a.scale = static_cast<float>(scale); a.c = static_cast<float>(scale * LOG2E);
+  a.stat = reinterpret_cast<const float4*>(stat); a.dz = dz; a.s_dz = s_dz;
+  a.target = target; a.s_target = s_target; a.ignore = ignore;
+  a.glp = g_logprob; a.s_glp = s_g_logprob;
+  a.gent = g_entropy; a.s_gent = s_g_entropy;
+  a.gtop = g_top; a.s_gtop = s_g_top; a.s_gtop_k = s_g_top_k;
+  a.top_index = top_index; a.top = g_top != nullptr ? top : 0;
+  return launch_grad(a, static_cast<hipStream_t>(stream));
+}
+
+det_status det_distill(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double temperature,
+                       det_dtype teacher_dt, const void* teacher, int64_t s_teacher, const int64_t* entry,
+                       int64_t s_entry, int64_t K, float* loss, float* stat, float* q, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!(temperature > 0.0)) return fail(DET_EINVAL, "the temperature must be positive");
+  det_status st = check_logits(dt, z, N, V, s_row, 1.0 / temperature);
+  if (st != DET_OK) return st;
+  if (!known_dtype(teacher_dt)) return fail(DET_EDTYPE, "unknown teacher dtype %d", static_cast<int>(teacher_dt));
+  if (K < 1 || K > ENTRIES_MAX) return fail(DET_EINVAL, "K = %lld must lie in 1..%d", (long long)K, ENTRIES_MAX);
+  if (s_teacher < 0 || s_entry < 0) return fail(DET_EINVAL, "negative stride");
+  if (N == 0) return DET_OK;
+  if (teacher == nullptr || entry == nullptr || loss == nullptr || stat == nullptr || q == nullptr)
+    return fail(DET_EINVAL, "null pointer");
+  if (!aligned_for(teacher, teacher_dt) || !aligned8(entry) || (reinterpret_cast<uintptr_t>(stat) & 15u) ||
+      ((reinterpret_cast<uintptr_t>(loss) | reinterpret_cast<uintptr_t>(q)) & 3u))
+    return fail(DET_EINVAL, "misaligned pointer");
+  ScoreArgs a{};
+  a.z = z; a.s_row = s_row; a.N = N; a.V = V; a.dt = dt; a.mode = MODE_DISTILL;
+  a.scale = 1.0 / temperature; a.c = static_cast<float>(a.scale * LOG2E);
+  a.teacher = teacher; a.s_teacher = s_teacher; a.tdt = teacher_dt;
+  a.entry = entry; a.s_entry = s_entry; a.K = static_cast<int>(K);
+  a.loss = loss; a.stat = reinterpret_cast<float4*>(stat); a.q = q;
+  return launch_score(a, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+det_status det_distill_grad(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double temperature,
+                            const int64_t* entry, int64_t s_entry, int64_t K, const float* stat, const float* q,
+                            const float* g, int64_t s_g, void* dz, int64_t s_dz, void* stream) {
+  if (!(temperature > 0.0)) return fail(DET_EINVAL, "the temperature must be positive");
+  det_status st = check_logits(dt, z, N, V, s_row, 1.0 / temperature);
+  if (st != DET_OK) return st;
+  if (K < 1 || K > ENTRIES_MAX) return fail(DET_EINVAL, "K = %lld must lie in 1..%d", (long long)K, ENTRIES_MAX);
+  if (s_entry < 0 || s_g < 0 || s_dz < V) return fail(DET_EINVAL, "negative stride, or gradient rows that overlap");
+  if (N == 0) return DET_OK;
+  if (entry == nullptr || stat == nullptr || q == nullptr || g == nullptr || dz == nullptr)
+    return fail(DET_EINVAL, "null pointer");
+  if (!aligned_for(dz, dt) || !aligned8(entry) || (reinterpret_cast<uintptr_t>(stat) & 15u) ||
+      ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(g)) & 3u))
+    return fail(DET_EINVAL, "misaligned pointer");
+  GradArgs a{};
+  a.z = z; a.s_row = s_row; a.N = N; a.V = V; a.dt = dt; a.mode = MODE_DISTILL;
+  a.scale = static_cast<float>(1.0 / temperature); a.c = static_cast<float>(LOG2E / temperature);
+  a.stat = reinterpret_cast<const float4*>(stat); a.dz = dz; a.s_dz = s_dz;
+  a.entry = entry; a.s_entry = s_entry; a.K = static_cast<int>(K); a.q = q;
+  a.g = g; a.s_g = s_g;
+  return launch_grad(a, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

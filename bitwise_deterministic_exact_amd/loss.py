@@ -28,7 +28,7 @@ from typing import Optional
 
 import torch
 
-from .api import det_finalize, exact_sqdiff_digits, mse_grad
+from .api import det_finalize, exact_dot_digits, exact_sqdiff_digits, mse_grad
 
 
 class _ExactMSE(torch.autograd.Function):
@@ -62,3 +62,31 @@ def exact_mse_loss(y: torch.Tensor, target: Optional[torch.Tensor] = None) -> to
     if y.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("exact_mse_loss takes float32 or bfloat16 tensors")
     return _ExactMSE.apply(y, target)
+
+
+class _ExactMean(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, t: torch.Tensor) -> torch.Tensor:
+        ctx.shape, ctx.dtype = t.shape, t.dtype
+        ones = torch.ones((), dtype=t.dtype, device=t.device).expand(t.numel())
+        s = det_finalize(exact_dot_digits(t.reshape(-1), ones, check_finite=False)).reshape(())
+        return s / torch.full((), float(max(t.numel(), 1)), dtype=torch.float32, device=t.device)
+
+    @staticmethod
+    def backward(ctx, g: torch.Tensor):
+        n = 1
+        for d in ctx.shape:
+            n *= d
+        return (g / torch.full((), float(max(n, 1)), dtype=torch.float32, device=g.device)).to(ctx.dtype).expand(
+            ctx.shape)
+
+
+def exact_mean(t: torch.Tensor) -> torch.Tensor:
+    """RNE32(sum_i t_i) / n with the sum formed exactly (the products t_i * 1
+    in one long accumulator); a 0-d float32 tensor whose bits do not depend on
+    the order or the split of the elements.  For per-token losses such as
+    distill_loss's.  t: finite float32 or bfloat16 GPU tensor of at most 2^30
+    elements.  Its gradient is the one value g / n, broadcast."""
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("exact_mean takes float32 or bfloat16 tensors")
+    return _ExactMean.apply(t)

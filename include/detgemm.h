@@ -396,6 +396,143 @@ det_status det_device_status(void* stream, int clear, int* flags);
 
 int32_t* det_device_status_word(void);
 
+/*
+ * ------------------------------------------------------------------------
+ * The head of a language model around the exact linear layers: layer norm,
+ * the log probabilities of given tokens, and distillation, with their
+ * gradients.  They are not exact sums of products (they hold exponentials,
+ * logarithms and square roots, rounded once each), but they keep what the
+ * exact GEMM promises about order: every result is a fixed function of its
+ * inputs.  A row's results depend on that row (and its width) alone, never on
+ * the number of rows, the strides, the alignment or how a launch splits the
+ * work; repetition gives the same bits; no floating-point atomics are used.
+ *
+ * Rows may start at any multiple of the element size (`s_row` elements
+ * apart, >= 0); the elements of a row are adjacent.
+ */
+#define DET_ROWS_MAX ((int64_t)1 << 22)
+#define DET_HEAD_V_MAX ((int64_t)1 << 24)
+#define DET_NORM_C_MAX ((int64_t)32768)
+#define DET_NORM_SHARD_ROWS 32
+
+/*
+ * det_layer_norm -- y = (x - mean) rstd w + b over each row of C elements,
+ *   mean = sum x / C, rstd = 1 / sqrt(sum (x - mean)^2 / C + eps)
+ *   x_dt, w_dt, y_dt  element types of x, of w and b, and of y
+ *   x                 [N] rows of C, s_x apart
+ *   w, b              C elements each; null for 1 and 0
+ *   y                 [N][C] contiguous, rounded once (nearest-even)
+ *   mean, rstd        [N] fp32, for the gradient; either null: not written
+ * N <= 2^22, 1 <= C <= 32768.  Sums are fp32 in one fixed order per C; the
+ * mean is corrected by the sum of the differences from it, so an offset that
+ * is large beside the spread costs no precision.
+ * Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
+ */
+det_status det_layer_norm(det_dtype x_dt, const void* x, int64_t s_x, det_dtype w_dt, const void* w, const void* b,
+                          int64_t N, int64_t C, double eps, det_dtype y_dt, void* y, float* mean, float* rstd,
+                          void* stream);
+
+/*
+ * det_layer_norm_grad -- the gradients of det_layer_norm.  With h = (x - mean)
+ * rstd and g = dy w:
+ *   dx = rstd (g - sum g / C - h sum (g h) / C)
+ *   dw = sum over rows of dy h,   db = sum over rows of dy
+ *   x, mean, rstd     as det_layer_norm read and wrote them
+ *   dy                [N] rows of C of type y_dt, s_dy apart
+ *   dx                [N][C] contiguous, type x_dt; null: not needed
+ *   dw, db            C elements each, type w_dt; null: not needed
+ *   digits            null, or int64 [2][C][18]: the raw digits of dw and db
+ *   workspace         det_layer_norm_grad_workspace_bytes(N, C), 16-byte
+ *                     aligned; null when dw, db and digits all are
+ * dw and db are summed in fp32 over chunks of consecutive rows in one fixed
+ * order (DET_NORM_SHARD_ROWS = 32 rows, 16 for C <= 2048) and the chunks are
+ * added exactly in the long accumulator and rounded once.  So the digits of
+ * row shards cut at multiples of 32 rows add up (det_combine) to the digits
+ * of all rows, and det_finalize of the sum gives the same bits as one call
+ * over all rows, for any number of shards and any order of adding them.
+ * An Inf or NaN chunk is noted in the device status; those sums are then NaN
+ * (their digits unspecified).
+ * Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
+ */
+int64_t det_layer_norm_grad_workspace_bytes(int64_t N, int64_t C);
+
+det_status det_layer_norm_grad(det_dtype x_dt, const void* x, int64_t s_x, det_dtype y_dt, const void* dy,
+                               int64_t s_dy, det_dtype w_dt, const void* w, const float* mean, const float* rstd,
+                               int64_t N, int64_t C, void* dx, void* dw, void* db, int64_t* digits,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * det_token_logprobs -- for each row z of V logits and l_j = scale z_j -
+ * ln sum_i exp(scale z_i): the target's l_t, the entropy -sum exp(l_j) l_j,
+ * and the `top` largest l_j with their indices.
+ *   z                 [N] rows of V logits of type dt, s_row apart; -inf masks
+ *   scale             1 / temperature, in [1e-6, 1e6)
+ *   target            [N], s_target apart (null: no logprob); `ignore` gives
+ *                     the log probability 0, any other value outside [0, V) NaN
+ *   top               0..64, at most V; ordered by value, ties by lower index
+ *   logprob, entropy  [N] fp32; entropy may be null, logprob without targets
+ *   stat              [N][4] fp32, 16-byte aligned: the maximum, 1 / S, log2 S
+ *                     (S = sum 2^(scale log2e (z - max))) and the entropy
+ *   top_index, top_logprob   [N][top]
+ *   workspace         det_head_workspace_bytes(N, V, top), 8-byte aligned
+ * A row of nothing but -inf has log probabilities -inf and entropy 0.  A row
+ * with a NaN or +inf has NaN results and indices -1, and is noted in the
+ * device status ("non-finite").  1 <= V <= 2^24, N <= 2^22.
+ * Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
+ */
+int64_t det_head_workspace_bytes(int64_t N, int64_t V, int top);
+
+det_status det_token_logprobs(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double scale,
+                              const int64_t* target, int64_t s_target, int64_t ignore, int top, float* logprob,
+                              float* entropy, float* stat, int64_t* top_index, float* top_logprob, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * det_token_logprobs_grad -- dz_j = scale ([j's own incoming gradients] -
+ * p_j (G + g_entropy (H + l_j))), G the sum of the row's incoming gradients of
+ * log probabilities.  stat and top_index are det_token_logprobs' outputs.
+ *   g_logprob, g_entropy   [N] fp32 with strides (0 repeats one value); null: none
+ *   g_top             [N][top] fp32 with strides s_g_top, s_g_top_k; null: none
+ *   dz                [N] rows of V of type dt, s_dz >= V apart; must not
+ *                     overlap z
+ * A row of nothing but -inf gets zeros.  Errors as for det_token_logprobs.
+ */
+det_status det_token_logprobs_grad(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double scale,
+                                   const int64_t* target, int64_t s_target, int64_t ignore, int top,
+                                   const int64_t* top_index, const float* stat, const float* g_logprob,
+                                   int64_t s_g_logprob, const float* g_entropy, int64_t s_g_entropy,
+                                   const float* g_top, int64_t s_g_top, int64_t s_g_top_k, void* dz, int64_t s_dz,
+                                   void* stream);
+
+/*
+ * det_distill -- per row T^2 sum_k q_k (ln q_k - l_{entry_k}), with q the
+ * softmax of the teacher's K logits at temperature T and l the student's log
+ * probabilities over all V at T.
+ *   z                 student logits, as for det_token_logprobs
+ *   teacher           [N] rows of K, s_teacher apart; -inf: no entry
+ *   entry             [N] rows of K indices, s_entry apart; those of entries
+ *                     without probability are not read as indices; any other
+ *                     outside [0, V) makes the row's loss NaN
+ *   K                 1..1024; an index may occur more than once
+ *   loss              [N] fp32;  stat: [N][4] as above;  q: [N][K] fp32
+ *   workspace         det_head_workspace_bytes(N, V, 0)
+ * A row without any entry has the loss 0 and no gradient; a student row of
+ * nothing but -inf the loss +inf and no gradient.
+ */
+det_status det_distill(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double temperature,
+                       det_dtype teacher_dt, const void* teacher, int64_t s_teacher, const int64_t* entry,
+                       int64_t s_entry, int64_t K, float* loss, float* stat, float* q, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * det_distill_grad -- dz_j = g T (p_j - sum over entries k of index j of q_k)
+ * with g = the row's incoming gradient (stride s_g, 0 repeats one value); the
+ * other arguments as for det_distill and det_token_logprobs_grad.
+ */
+det_status det_distill_grad(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double temperature,
+                            const int64_t* entry, int64_t s_entry, int64_t K, const float* stat, const float* q,
+                            const float* g, int64_t s_g, void* dz, int64_t s_dz, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
