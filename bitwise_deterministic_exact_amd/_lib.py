@@ -24,6 +24,7 @@ TOP_MAX = 64
 ENTRIES_MAX = 1024
 
 _lib = None
+_ops = None
 
 
 class DetGemmError(RuntimeError):
@@ -90,6 +91,22 @@ def load() -> ctypes.CDLL:
         raise ImportError("libdetgemm.so layout constants do not match the binding")
     _lib = lib
     return lib
+
+
+def ops():
+    """The torch extension module of the head operators (csrc/head_ops.cpp)."""
+    global _ops
+    if _ops is not None:
+        return _ops
+    load()
+    try:
+        from . import _ops as mod
+    except ImportError as e:
+        raise ImportError(
+            f"{os.path.join(os.path.dirname(LIB_PATH), '_ops.so')} is not built or does not load; run "
+            "`python -c 'import __graft_entry__ as g; g.build()'`.  There is no fallback implementation.") from e
+    _ops = mod
+    return _ops
 
 
 def last_error() -> str:

@@ -145,6 +145,10 @@ def test_optional_weights_and_needs(C):
                                           need_dbias=needs[2])
             for g, f, n in zip(got, full, needs):
                 assert (g is None) if not n else torch.equal(g, f)
+        # through autograd, with the absent weights' places empty
+        leaves = [t.clone().requires_grad_(True) if t is not None else None for t in (x, ww, bb)]
+        grads = torch.autograd.grad(det.layer_norm(*leaves), [t for t in leaves if t is not None], dy)
+        assert all(torch.equal(p, f) for p, f in zip(grads, [f for f, t in zip(full, leaves) if t is not None]))
 
 
 def test_leading_shapes_strides_and_broadcast_gradients():
@@ -312,6 +316,15 @@ def test_streams_repetition_and_graph_replay():
         ey, em, er = det.layer_norm_forward(nx, w, b)
         eg = det.layer_norm_backward(dy * (k + 1), nx, w, em, er)
         assert torch.equal(gy, ey) and all(torch.equal(p, q) for p, q in zip(gg, eg)), k
+
+
+def test_second_derivatives_are_refused():
+    x = torch.randn(3, 20, device="cuda", requires_grad=True)
+    dy = torch.randn(3, 20, device="cuda", requires_grad=True)
+    g, = torch.autograd.grad(det.layer_norm(x), x, dy, create_graph=True)
+    assert torch.equal(g.detach(), torch.autograd.grad(det.layer_norm(x), x, dy)[0])
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        g.sum().backward()
 
 
 def test_module_trains():
