@@ -19,7 +19,7 @@ K_MAX = 1 << 19
 ROWS_MAX = 1 << 22
 HEAD_V_MAX = 1 << 24
 NORM_C_MAX = 32768
-NORM_SHARD_ROWS = 32
+NORM_SHARD_ROWS = 64
 TOP_MAX = 64
 ENTRIES_MAX = 1024
 

@@ -47,7 +47,7 @@ struct ScoreArgs {
   int top, cap;                           // alternatives; candidates a wave's pool holds
   // workspace of a row shared by several workgroups
   float* parts;                           // [N][nchunk][3]
-  uint64_t* lists;                        // [N][nblk][top]
+  uint64_t* lists;                        // [N][nblk * WAVES][top]: the waves' lists, sorted, 0 at the end
   // score
   const int64_t* target; int64_t s_target;
   int64_t ignore;
@@ -86,17 +86,38 @@ __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
 }
 
 // The largest `want` of the n keys in LDS at pool[0..n), sorted, into out (not
-// overlapping the pool), by `lanes` threads numbered `t` (all of a wave, or of a workgroup): each key's
-// rank is the number of larger keys.  n^2 / lanes broadcast reads: n is close
-// to `want` except for rows built against it.
+// overlapping the pool), by `lanes` threads numbered `t` (all of a wave, or of
+// a workgroup): each key's rank is the number of larger keys, read two to an
+// access and 16 in flight.  n^2 / lanes comparisons: n is close to `want`
+// except for rows built against it.  pool is 16-byte aligned; the keys behind
+// n up to a multiple of 16 are read and must be readable, their values unused.
 __device__ __forceinline__ void rank_keys(const uint64_t* pool, int n, uint64_t* out, int want, int t, int lanes) {
+  const ulonglong2* const two = reinterpret_cast<const ulonglong2*>(pool);
   for (int e = t; e < n; e += lanes) {
     const uint64_t mine = pool[e];
     int rank = 0;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) rank += pool[i] > mine ? 1 : 0;
+    for (int i = 0; i < n; i += 16) {
+      ulonglong2 k[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) k[j] = two[(i >> 1) + j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        rank += i + 2 * j < n && k[j].x > mine ? 1 : 0;
+        rank += i + 2 * j + 1 < n && k[j].y > mine ? 1 : 0;
+      }
+    }
     if (rank < want) out[rank] = mine;
   }
+}
+
+// the key of rank r (0 = largest) among the lanes' distinct nonzero keys, or
+// 0 when there are not that many
+__device__ __forceinline__ uint64_t lane_key_of_rank(uint64_t mine, int r) {
+  if (__popcll(__ballot(mine != 0)) <= r) return 0;
+  int rank = 0;
+#pragma unroll 8
+  for (int l = 0; l < 64; ++l) rank += lane_u64(mine, l) > mine ? 1 : 0;
+  return lane_u64(mine, __builtin_ctzll(__ballot(mine != 0 && rank == r)));
 }
 
 // ---------------------------------------------------------------- one chunk
@@ -175,12 +196,7 @@ struct TopList {
     for (int i = NV - 1; i >= 0; --i)
       if (vmax[i] == lane_max) first = i * 64 + lane;
     const uint64_t mine = base + static_cast<int64_t>(lane) * VE < V ? key_of(order_bits(lane_max), first) : 0;
-    if (__popcll(__ballot(mine != 0)) < top) return 0;
-    int rank = 0;
-#pragma unroll 4
-    for (int l = 0; l < 64; ++l) rank += lane_u64(mine, l) > mine ? 1 : 0;
-    const uint64_t hit = __ballot(mine != 0 && rank == top - 1);
-    return lane_u64(mine, __builtin_ctzll(hit));
+    return lane_key_of_rank(mine, top - 1);
   }
 
   __device__ __forceinline__ void add(const float (&v)[LANE_ELEMS], const float (&vmax)[NV], float lane_max,
@@ -336,7 +352,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
   const bool live = row < a.N;
   const bool whole = a.nblk == 1;
   // LDS: per wave a pool (cap) and a list (top); then the rows' chunk sums
-  const int per_wave = a.cap + a.top;
+  const int per_wave = a.cap + (a.top + 1) / 2 * 2;           // even: the pools stay 16-byte aligned
   uint64_t* const pool = lds + wave * per_wave;
   uint64_t* const list = pool + a.cap;
   float* const lparts = reinterpret_cast<float*>(lds + WAVES * per_wave);
@@ -386,10 +402,16 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
     }
     if constexpr (TOP)
       for (int e = tl.L + lane; e < a.top; e += 64) list[e] = 0;     // a wave with few elements
+    wave_sync();
   }
-  __syncthreads();
+  if (whole) __syncthreads();            // uniform: the other waves' sums and lists
   if (!live) return;
-  if (TOP && a.wpr > 1 && rw == 0) {
+  if (!whole) {                          // k_score_join does the rest
+    if (TOP && lane < a.top) a.lists[((row * a.nblk + part) * WAVES + wave) * a.top + lane] = list[lane];
+    return;
+  }
+  if (rw != 0) return;
+  if (TOP && a.wpr > 1) {
     // the row's wave lists, gathered into this wave's pool (cap >= wpr * top), joined
     for (int w = 0; w < a.wpr; ++w)
       if (lane < a.top) pool[w * a.top + lane] = lds[(wave + w) * per_wave + a.cap + lane];
@@ -399,34 +421,50 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
     rank_keys(pool, a.wpr * a.top, list, a.top, lane, 64);
     wave_sync();
   }
-  if (rw != 0) return;
-  if (!whole) {
-    if (TOP && lane < a.top) a.lists[(row * a.nblk + part) * a.top + lane] = list[lane];
-    return;
-  }
   const RowSums r = join(a, parts, row, lane);
   if (a.mode == MODE_DISTILL) finish_distill(a, r, row, lane);
   else finish_score(a, r, row, lane);
   if constexpr (TOP) write_top(a, r, row, list, lane);
 }
 
-// The end of rows that several workgroups shared: one workgroup per row.
+// The end of rows that several workgroups shared: one workgroup per row.  Of
+// the n lists' keys only those can be among the top that reach a bar: with j =
+// ceil(top / n), the ceil(top / j)-th largest of the lists' j-th keys, which
+// at least `top` keys reach.  On unordered rows that leaves about 1.5 top keys
+// of n top to be ranked.
 __global__ __launch_bounds__(256) void k_score_join(ScoreArgs a) {
   extern __shared__ __align__(16) uint64_t lds[];
+  __shared__ int count;
+  __shared__ uint64_t bar;
   const int64_t row = blockIdx.x;
-  const int n = a.nblk * a.top;
+  const int lane = threadIdx.x & 63;
+  const int lists = a.nblk * WAVES, n = lists * a.top;
+  uint64_t* const best = lds;                                 // [top]
+  uint64_t* const pool = lds + TOP_MAX;                       // [n + 16]: the keys that reach the bar
   if (a.top > 0) {
-    for (int e = threadIdx.x; e < n; e += 256) lds[e] = a.lists[row * n + e];
+    const uint64_t* const src = a.lists + row * n;
+    if (threadIdx.x < 64) {
+      const int j = (a.top + lists - 1) / lists;
+      const uint64_t b = lane_key_of_rank(lane < lists ? src[lane * a.top + j - 1] : 0, (a.top + j - 1) / j - 1);
+      if (lane == 0) {
+        bar = b > 0 ? b : 1;
+        count = 0;
+      }
+    }
     __syncthreads();
-    rank_keys(lds, n, lds + n, a.top, threadIdx.x, 256);
+    for (int e = threadIdx.x; e < n; e += 256) {
+      const uint64_t key = src[e];
+      if (key >= bar) pool[atomicAdd(&count, 1)] = key;
+    }
+    __syncthreads();
+    rank_keys(pool, count, best, a.top, threadIdx.x, 256);
     __syncthreads();
   }
   if (threadIdx.x >= 64) return;
-  const int lane = threadIdx.x;
   const RowSums r = join(a, a.parts + row * a.nchunk * 3, row, lane);
   if (a.mode == MODE_DISTILL) finish_distill(a, r, row, lane);
   else finish_score(a, r, row, lane);
-  if (a.top > 0) write_top(a, r, row, lds + n, lane);
+  if (a.top > 0) write_top(a, r, row, best, lane);
 }
 
 // ---------------------------------------------------------------- gradients
@@ -473,7 +511,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
   constexpr int VE = Elem<DT>::VE, NV = LANE_ELEMS / VE;
   extern __shared__ __align__(16) int32_t lds_i[];            // entry indices, then their gradients
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = blockIdx.x / a.nblk;
+  // the last rows first: they are what the forward pass left in the memory-side cache
+  const int64_t row = a.N - 1 - blockIdx.x / a.nblk;
   const int part = static_cast<int>(blockIdx.x % a.nblk);
   const int n = a.mode == MODE_DISTILL ? a.K : 1 + a.top;
   float* const lds_w = reinterpret_cast<float*>(lds_i + n);
@@ -557,21 +596,24 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
 
 // ---------------------------------------------------------------- host side
 
-// Workgroups per row: one when the rows alone give every CU four workgroups
-// (then the row is finished in the same launch), else enough to do so, or as many
-// as the row has groups of four chunks.
-int blocks_per_row(int64_t N, int64_t nchunk) {
+// Workgroups per row: one when the rows alone give every CU about three (then
+// the row is finished in the same launch), else enough for four, or as many as
+// the row has groups of four chunks, and with alternatives at most 16 (64
+// lists to join).
+constexpr int SHARED_MAX = 16;
+int blocks_per_row(int64_t N, int64_t nchunk, int top) {
   int64_t b = 1;
-  if (N < 1024) b = std::min(ceil_div(nchunk, WAVES), ceil_div(1024, N > 0 ? N : 1));
+  if (N < 768) b = std::min(ceil_div(nchunk, WAVES), ceil_div(1024, N > 0 ? N : 1));
+  if (top > 0) b = std::min<int64_t>(b, SHARED_MAX);
   if (nchunk > LDS_PARTS && b == 1) b = 2;                    // the sums go through the workspace
   return static_cast<int>(b);
 }
 
 int64_t score_ws_bytes(int64_t N, int64_t V, int top) {
   const int64_t nchunk = ceil_div(V, CHUNK);
-  const int nblk = blocks_per_row(N, nchunk);
+  const int nblk = blocks_per_row(N, nchunk, top);
   if (nblk == 1) return 0;
-  return N * (nblk * static_cast<int64_t>(top) * 8 + nchunk * 12);
+  return N * (nblk * WAVES * static_cast<int64_t>(top) * 8 + nchunk * 12);
 }
 
 det_status check_logits(int dt, const void* z, int64_t N, int64_t V, int64_t s_row, double scale) {
@@ -589,10 +631,10 @@ det_status check_logits(int dt, const void* z, int64_t N, int64_t V, int64_t s_r
 
 det_status launch_score(ScoreArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
   a.nchunk = static_cast<int>(ceil_div(a.V, CHUNK));
-  a.nblk = blocks_per_row(a.N, a.nchunk);
+  a.nblk = blocks_per_row(a.N, a.nchunk, a.top);
   a.wpr = a.nchunk >= WAVES ? WAVES : a.nchunk;
   if (a.wpr == 3) a.wpr = 4;
-  a.cap = a.top > 0 ? (LANE_ELEMS + 1) * a.top : 0;
+  a.cap = a.top > 0 ? ((LANE_ELEMS + 1) * a.top + 15) / 16 * 16 : 0;   // rank_keys reads to a multiple of 16
   a.status = det_device_status_word();
   if (a.status == nullptr) return DET_EHIP;
   if (a.nblk > 1) {
@@ -601,11 +643,11 @@ det_status launch_score(ScoreArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
     if (ws == nullptr || !aligned8(ws) || ws_bytes < static_cast<size_t>(need))
       return fail(DET_EINVAL, "workspace: %lld bytes, 8-byte aligned, are needed", (long long)need);
     a.lists = static_cast<uint64_t*>(ws);
-    a.parts = reinterpret_cast<float*>(a.lists + a.N * a.nblk * a.top);
+    a.parts = reinterpret_cast<float*>(a.lists + a.N * a.nblk * WAVES * a.top);
   }
   const int rpb = WAVES / a.wpr;
   const int64_t blocks = a.nblk > 1 ? a.N * a.nblk : ceil_div(a.N, rpb);
-  const size_t lds = static_cast<size_t>(WAVES) * (a.cap + a.top) * 8 +
+  const size_t lds = static_cast<size_t>(WAVES) * (a.cap + (a.top + 1) / 2 * 2) * 8 +
                      (a.nblk > 1 ? 0 : static_cast<size_t>(rpb) * a.nchunk * 12);
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * WAVES);
   if (a.dt == DET_F32) {
@@ -617,14 +659,14 @@ det_status launch_score(ScoreArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
   }
   det_status st = hip_check(hipGetLastError(), "score launch");
   if (st != DET_OK || a.nblk == 1) return st;
-  const size_t jl = static_cast<size_t>(a.nblk + 1) * a.top * 8;
+  const size_t jl = a.top > 0 ? (TOP_MAX + static_cast<size_t>(a.nblk) * WAVES * a.top + 16) * 8 : 0;
   hipLaunchKernelGGL(k_score_join, dim3(static_cast<unsigned>(a.N)), dim3(256), jl, s, a);
   return hip_check(hipGetLastError(), "score join launch");
 }
 
 det_status launch_grad(GradArgs a, hipStream_t s) {
   a.nchunk = static_cast<int>(ceil_div(a.V, CHUNK));
-  a.nblk = blocks_per_row(a.N, a.nchunk);
+  a.nblk = blocks_per_row(a.N, a.nchunk, 0);
   const int n = a.mode == MODE_DISTILL ? a.K : 1 + a.top;
   const dim3 grid(static_cast<unsigned>(a.N * a.nblk)), block(64 * WAVES);
   const size_t lds = static_cast<size_t>(n) * 8;

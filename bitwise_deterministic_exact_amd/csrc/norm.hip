@@ -8,13 +8,17 @@
 // The reductions over a row are fp32 in a fixed tree that C alone decides.
 //
 // The weights' gradients are sums over rows (tokens).  A workgroup adds a
-// chunk of 16 or 32 consecutive rows in fp32 in a fixed order while it forms dx, and
-// the chunks' sums are added as exact integers (the digits of the long
-// accumulator) and rounded once: any split of the rows at multiples of 32,
-// and any order of the chunks, gives the same bits.
+// chunk of 16, 32 or 64 consecutive rows in fp32 in a fixed order while it
+// forms dx, and the chunks' sums are added as exact integers (the digits of
+// the long accumulator) and rounded once: any split of the rows at multiples
+// of 64, and any order of the chunks, gives the same bits.
 #include <algorithm>
+#include <type_traits>
 
 #include "rowops.h"
+
+// every fused multiply-add below is written as one: the compiler forms none
+#pragma clang fp contract(off)
 
 namespace {
 
@@ -22,80 +26,134 @@ using namespace rowops;
 
 // ---------------------------------------------------------------- geometry
 //
-// T threads own a row, S vectors of W elements each (vector s of thread t
-// starts at element (s T + t) W); G rows at a time in a workgroup.  W is 8
-// when every 8 elements of the narrowest operand fill 16 bytes (all bf16), else 4.
+// T threads own a row (as few waves as hold C elements), S vectors of W
+// elements each: vector s of thread t starts at element (s T + t) W.  G rows
+// at a time in a workgroup.  W is 8 when x and y are both bf16 (16 bytes),
+// else 4; 1 for rows shorter than that.  All of it follows from C and the
+// types, so the sums' order does.
+//
+// Every access is a whole vector: one that would pass the row's end starts at
+// C - W instead.  Its first `own` elements are then the previous vector's too:
+// they are left out of the sums and written a second time, with the same value
+// (each operation below is spelled out, so every copy of it rounds alike).
+// With the tail's loads element by element under a branch the loads of a
+// ragged wave waited for each other (8000 x 5000 bf16 forward 52 us, 42 this
+// way; backward 97 and 61); with the tail's stores element by element the
+// backward took 120 us.
 
-constexpr int chunk_rows(int64_t C) { return C <= 2048 ? 16 : DET_NORM_SHARD_ROWS; }
+// rows whose dw and db are added in fp32: each divides DET_NORM_SHARD_ROWS.
+// Few rows mean many workgroups (16 rows of 4096 columns: two per CU at 8192
+// tokens) but more chunk sums to write and add again (8 bytes per column and
+// chunk against 6 per element: 8 % at 16 rows, 4 % at 32).
+constexpr int chunk_rows(int64_t C) { return C <= 512 ? 64 : C <= 4096 ? 16 : 32; }
 
-// The sum over a row's T threads of N values at once.  One barrier: the
-// buffers alternate, so a buffer is rewritten only after every thread has
-// passed the barrier that follows its last reads.
-template <int T, int G, int NV>
-struct RowSum {
-  static constexpr int WPR = T / 64;
-  float buf[2][G][WPR][NV];
+// W elements of type DT as loaded, 16 or 8 bytes
+template <int DT, int W>
+struct Raw {
+  static constexpr int U = (W * Elem<DT>::BYTES + 3) / 4;
+  uint32_t u[U];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < U; ++i) u[i] = 0u;
+  }
+  // from element `at` of the row at p (a scalar address, a 32-bit offset)
+  __device__ __forceinline__ void load(const char* p, int at) {
+    const char* const q = p + static_cast<uint32_t>(at * Elem<DT>::BYTES);
+    if constexpr (W == 1) {
+      if constexpr (DT == DET_F32) u[0] = *reinterpret_cast<const uint32_t*>(q);
+      else u[0] = *reinterpret_cast<const uint16_t*>(q);
+    } else if constexpr (U == 4 && DT == DET_F32) {
+      const u32x4_a4 v = *reinterpret_cast<const u32x4_a4*>(q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = v[i];
+    } else if constexpr (U == 4) {
+      const u32x4_a2 v = *reinterpret_cast<const u32x4_a2*>(q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = v[i];
+    } else {
+      const u32x2_a2 v = *reinterpret_cast<const u32x2_a2*>(q);
+      u[0] = v[0];
+      u[1] = v[1];
+    }
+  }
+  __device__ __forceinline__ void floats(float (&v)[W]) const {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      if constexpr (DT == DET_F32) v[j] = __uint_as_float(u[j]);
+      else v[j] = __uint_as_float((j & 1) ? u[j / 2] & 0xFFFF0000u : u[j / 2] << 16);
+    }
+  }
 };
-template <int T, int G, int NV>
-__device__ __forceinline__ void row_sum(RowSum<T, G, NV>& m, int& turn, int group, int wave_in_row,
-                                        float (&v)[NV]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (T > 64) {
-    if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) m.buf[turn][group][wave_in_row][i] = v[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < T / 64; ++w) s += m.buf[turn][group][w][i];
-      v[i] = s;
-    }
-    turn ^= 1;
-  }
-}
 
 template <int DT, int W>
-__device__ __forceinline__ void load_part(const void* p, int64_t row0, int64_t at, int64_t C, float (&v)[W]) {
-  if (at + W <= C) {
-    load_vec<DT, W>(p, row0 + at, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = at + j < C ? load_elem<DT>(p, row0 + at + j) : 0.0f;
-  }
+__device__ __forceinline__ void store_row(char* p, int at, const float (&v)[W]) {
+  char* const q = p + static_cast<uint32_t>(at * Elem<DT>::BYTES);
+  if constexpr (W == 1) store_elem<DT>(q, 0, v[0]);
+  else store_vec<DT, W>(q, 0, v);
 }
-template <int DT, int W>
-__device__ __forceinline__ void store_part(void* p, int64_t row0, int64_t at, int64_t C, const float (&v)[W]) {
-  if (at + W <= C) {
-    store_vec<DT, W>(p, row0 + at, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      if (at + j < C) store_elem<DT>(p, row0 + at + j, v[j]);
-  }
+template <int DT>
+__device__ __forceinline__ const char* row_at(const void* p, int64_t i) {
+  return static_cast<const char*>(p) + i * Elem<DT>::BYTES;
+}
+template <int DT>
+__device__ __forceinline__ char* row_at(void* p, int64_t i) {
+  return static_cast<char*>(p) + i * Elem<DT>::BYTES;
 }
 // w and b: their type is a run-time choice (they are read once per workgroup)
 template <int W>
-__device__ __forceinline__ void load_weights(int dt, const void* p, int64_t at, int64_t C, float missing,
-                                             float (&v)[W]) {
+__device__ __forceinline__ void load_weights(int dt, const void* p, int at, float missing, float (&v)[W]) {
   if (p == nullptr) {
 #pragma unroll
     for (int j = 0; j < W; ++j) v[j] = missing;
+  } else if constexpr (W == 1) {
+    v[0] = load_elem(dt, p, at);
   } else if (dt == DET_F32) {
-    load_part<DET_F32, W>(p, 0, at, C, v);
+    load_vec<DET_F32, W>(p, at, v);
   } else {
-    load_part<DET_BF16, W>(p, 0, at, C, v);
+    load_vec<DET_BF16, W>(p, at, v);
   }
+}
+
+// where vector s of thread t starts, and its first element that no other
+// vector has (W: none)
+struct Place {
+  int at, own;
+};
+template <int W>
+__device__ __forceinline__ Place place(int s, int T, int t, int C) {
+  const int at = (s * T + t) * W, from = min(at, C - W);
+  return {from, min(at - from, W)};
+}
+
+// The sum of two values over a row's waves (wpr of them from wave `first`).
+// One barrier: the buffers alternate, so one is rewritten only after every
+// thread has passed the barrier that follows its last reads.
+struct RowSum {
+  float buf[2][16][2];
+};
+__device__ __forceinline__ void row_sum(RowSum& m, int& turn, int wave, int first, int wpr, float (&v)[2]) {
+  v[0] = wave_sum(v[0]);
+  v[1] = wave_sum(v[1]);
+  if (wpr == 1) return;                                       // uniform
+  if ((threadIdx.x & 63) == 0) {
+    m.buf[turn][wave][0] = v[0];
+    m.buf[turn][wave][1] = v[1];
+  }
+  __syncthreads();
+  v[0] = v[1] = 0.0f;
+  for (int w = 0; w < wpr; ++w) {
+    v[0] += m.buf[turn][first + w][0];
+    v[1] += m.buf[turn][first + w][1];
+  }
+  turn ^= 1;
 }
 
 // ---------------------------------------------------------------- forward
 struct NormArgs {
   const void* x; int64_t s_x;
   const void* w; const void* b;
-  int64_t N, C;
+  int64_t N;
+  int C, T, G;
   float eps, inv_c;
   int w_dt;
   void* y;
@@ -103,60 +161,71 @@ struct NormArgs {
   int rows;                               // rows per workgroup, a multiple of G
 };
 
-template <int XT, int YT, int T, int S, int W, int G>
-__global__ __launch_bounds__(T * G) void k_norm(NormArgs a) {
-  __shared__ RowSum<T, G, 2> sm;
+// d = x - m0 with m0 the rounded mean; the sum of d corrects both the mean and
+// the variance, so an offset that is large beside the spread costs no
+// precision.  The next row's loads are in flight while this one is summed and
+// written.  (Moments per wave joined behind one barrier instead of two: the
+// same time on bf16 rows of 4096, 20 % more on 5120, from 115 registers
+// instead of 84.)
+template <int XT, int YT, int S, int W, int MAXT>
+__global__ __launch_bounds__(MAXT) void k_norm(NormArgs a) {
+  __shared__ RowSum sm;
   int turn = 0;
-  const int t = threadIdx.x % T, group = threadIdx.x / T, wr = t >> 6;
+  // a workgroup is T x G threads and T whole waves: a wave's row, and its address, are scalars
+  const int t = threadIdx.x, group = __builtin_amdgcn_readfirstlane(threadIdx.y), wpr = a.T >> 6;
+  const int first = group * wpr, wave = first + __builtin_amdgcn_readfirstlane(t >> 6);
+  Place at[S];
   float w[S][W], b[S][W];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int64_t at = static_cast<int64_t>(s * T + t) * W;
-    load_weights<W>(a.w_dt, a.w, at, a.C, 1.0f, w[s]);
-    load_weights<W>(a.w_dt, a.b, at, a.C, 0.0f, b[s]);
+    at[s] = place<W>(s, a.T, t, a.C);
+    load_weights<W>(a.w_dt, a.w, at[s].at, 1.0f, w[s]);
+    load_weights<W>(a.w_dt, a.b, at[s].at, 0.0f, b[s]);
   }
-  for (int r = group; r < a.rows; r += G) {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * a.rows + r;
-    const bool live = row < a.N;
+  Raw<XT, W> next[S];
+  auto fetch = [&](int64_t row) {         // past the last row: that row again, not used
+    const char* const x = row_at<XT>(a.x, min(row, a.N - 1) * a.s_x);
+#pragma unroll
+    for (int s = 0; s < S; ++s) next[s].load(x, at[s].at);
+  };
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows;
+  fetch(row0 + group);
+  for (int r = group; r < a.rows; r += a.G) {
+    const int64_t row = row0 + r;
     float v[S][W];
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int64_t at = static_cast<int64_t>(s * T + t) * W;
-      if (live) load_part<XT, W>(a.x, row * a.s_x, at, a.C, v[s]);
-      else {
+      next[s].floats(v[s]);
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[s][j] = 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < W; ++j) sum[0] += v[s][j];
+      for (int j = 0; j < W; ++j) sum[0] += j >= at[s].own ? v[s][j] : 0.0f;
     }
-    row_sum<T, G, 2>(sm, turn, group, wr, sum);
-    // d = x - m0 with m0 the rounded mean; the sum of d corrects m0
+    if (r + a.G < a.rows) fetch(row + a.G);
+    row_sum(sm, turn, wave, first, wpr, sum);
     const float m0 = sum[0] * a.inv_c;
     float sq[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int64_t at = static_cast<int64_t>(s * T + t) * W;
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        v[s][j] = at + j < a.C ? v[s][j] - m0 : 0.0f;
-        sq[0] += v[s][j] * v[s][j];
-        sq[1] += v[s][j];
+        v[s][j] -= m0;
+        const float d = j >= at[s].own ? v[s][j] : 0.0f;
+        sq[0] = fmaf(d, d, sq[0]);
+        sq[1] += d;
       }
     }
-    row_sum<T, G, 2>(sm, turn, group, wr, sq);
+    row_sum(sm, turn, wave, first, wpr, sq);
+    if (row >= a.N) continue;
     const float off = sq[1] * a.inv_c;
-    const float var = fmaxf(sq[0] * a.inv_c - off * off, 0.0f);
+    const float var = fmaxf(fmaf(-off, off, sq[0] * a.inv_c), 0.0f);
     const float rstd = 1.0f / sqrtf((sq[0] != sq[0] ? sq[0] : var) + a.eps);
-    if (!live) continue;
     const float shift = -off * rstd;
+    char* const y = row_at<YT>(a.y, row * a.C);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int64_t at = static_cast<int64_t>(s * T + t) * W;
 #pragma unroll
       for (int j = 0; j < W; ++j) v[s][j] = fmaf(fmaf(v[s][j], rstd, shift), w[s][j], b[s][j]);
-      store_part<YT, W>(a.y, row * a.C, at, a.C, v[s]);
+      if (at[s].own < W) store_row<YT, W>(y, at[s].at, v[s]);
     }
     if (t == 0) {
       if (a.mean != nullptr) a.mean[row] = m0 + off;
@@ -171,103 +240,134 @@ struct NormGradArgs {
   const void* dy; int64_t s_dy;
   const void* w; int w_dt;
   const float* mean; const float* rstd;
-  int64_t N, C;
+  int64_t N;
+  int C, T, G;
   float inv_c;
   void* dx;
   float* parts;                           // [chunks][2][C]: the chunks' dw and db; null: not needed
   int chunk;                              // rows per workgroup
 };
 
-template <int XT, int YT, int T, int S, int W, int G>
-__global__ __launch_bounds__(T * G) void k_norm_grad(NormGradArgs a) {
-  __shared__ RowSum<T, G, 2> sm;
-  extern __shared__ __align__(16) float fold[];               // [T * S * W * 2] when G > 1
+template <int P>
+struct alignas(4 * P) RunOf {
+  float v[P];
+};
+
+template <int XT, int YT, int S, int W, int MAXT>
+__global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
+  __shared__ RowSum sm;
+  extern __shared__ __align__(16) float4 fold_lds[];          // [G][2 S W / P][T] runs of P when G > 1
   int turn = 0;
-  const int t = threadIdx.x % T, group = threadIdx.x / T, wr = t >> 6;
+  // a workgroup is T x G threads and T whole waves: a wave's row, and its address, are scalars
+  const int t = threadIdx.x, group = __builtin_amdgcn_readfirstlane(threadIdx.y), wpr = a.T >> 6;
+  const int first = group * wpr, wave = first + __builtin_amdgcn_readfirstlane(t >> 6);
+  Place at[S];
   float w[S][W], dw[S][W], db[S][W];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    load_weights<W>(a.w_dt, a.w, static_cast<int64_t>(s * T + t) * W, a.C, 1.0f, w[s]);
+    at[s] = place<W>(s, a.T, t, a.C);
+    load_weights<W>(a.w_dt, a.w, at[s].at, 1.0f, w[s]);
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[s][j] = db[s][j] = 0.0f;
   }
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * a.chunk;
-  for (int r = group; r < a.chunk; r += G) {
-    const int64_t row = first + r;
-    if (first + (r - group) >= a.N) break;                    // no group has a row left: uniform
-    const bool live = row < a.N;
-    float h[S][W], g[S][W];
-    float sum[2] = {0.0f, 0.0f};
-    const float mean = live ? a.mean[row] : 0.0f, rstd = live ? a.rstd[row] : 0.0f;
+  // the last rows first: they are what the forward pass left in the memory-side cache
+  const int64_t chunk = gridDim.x - 1 - blockIdx.x;
+  const int64_t row0 = chunk * a.chunk;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.N - row0));
+  Raw<XT, W> nx[S];
+  Raw<YT, W> ny[S];
+  float nmean = 0.0f, nrstd = 0.0f;
+  auto fetch = [&](int r) {               // past the last row: that row again, not used
+    const int64_t row = row0 + min(r, rows - 1);
+    const char* const x = row_at<XT>(a.x, row * a.s_x);
+    const char* const dy = row_at<YT>(a.dy, row * a.s_dy);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int64_t at = static_cast<int64_t>(s * T + t) * W;
-      if (live) {
-        load_part<XT, W>(a.x, row * a.s_x, at, a.C, h[s]);
-        load_part<YT, W>(a.dy, row * a.s_dy, at, a.C, g[s]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < W; ++j) h[s][j] = g[s][j] = 0.0f;
-      }
+      nx[s].load(x, at[s].at);
+      ny[s].load(dy, at[s].at);
     }
+    nmean = a.mean[row];
+    nrstd = a.rstd[row];
+  };
+  fetch(group);
+  for (int r0 = 0; r0 < rows; r0 += a.G) {
+    const int r = r0 + group;
+    float h[S][W], g[S][W];
+    float sum[2] = {0.0f, 0.0f};
+    const float mean = nmean, rstd = nrstd;
+    const bool live = r < rows;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      nx[s].floats(h[s]);
+      ny[s].floats(g[s]);
+    }
+    if (r0 + a.G < rows) fetch(r + a.G);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        h[s][j] = (h[s][j] - mean) * rstd;                    // past C: g = 0, so h counts nowhere
-        dw[s][j] += g[s][j] * h[s][j];
-        db[s][j] += g[s][j];
+        h[s][j] = (h[s][j] - mean) * rstd;
+        if (live) {                                           // uniform in a wave
+          dw[s][j] = fmaf(g[s][j], h[s][j], dw[s][j]);
+          db[s][j] += g[s][j];
+        }
         g[s][j] *= w[s][j];
-        sum[0] += g[s][j];
-        sum[1] += g[s][j] * h[s][j];
+        const float u = j >= at[s].own ? g[s][j] : 0.0f;
+        sum[0] += u;
+        sum[1] = fmaf(u, h[s][j], sum[1]);
       }
     }
     if (a.dx == nullptr) continue;                            // uniform
-    row_sum<T, G, 2>(sm, turn, group, wr, sum);
+    row_sum(sm, turn, wave, first, wpr, sum);
     if (!live) continue;
     const float m1 = sum[0] * a.inv_c, m2 = sum[1] * a.inv_c;
+    char* const dx = row_at<XT>(a.dx, (row0 + r) * a.C);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
-      for (int j = 0; j < W; ++j) g[s][j] = rstd * (g[s][j] - m1 - h[s][j] * m2);
-      store_part<XT, W>(a.dx, row * a.C, static_cast<int64_t>(s * T + t) * W, a.C, g[s]);
+      for (int j = 0; j < W; ++j) g[s][j] = rstd * fmaf(-h[s][j], m2, g[s][j] - m1);
+      if (at[s].own < W) store_row<XT, W>(dx, at[s].at, g[s]);
     }
   }
   if (a.parts == nullptr) return;
-  // the groups' sums, added in group order
-  if constexpr (G > 1) {
-    float* const mine = fold + t;
-#pragma unroll 1
-    for (int k = 1; k < G; ++k) {
-      __syncthreads();
-      if (group == k) {
+  char* const pw = reinterpret_cast<char*>(a.parts + chunk * 2 * a.C);
+  if (a.G == 1) {
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int j = 0; j < W; ++j) {
-            mine[(2 * (s * W + j)) * T] = dw[s][j];
-            mine[(2 * (s * W + j) + 1) * T] = db[s][j];
-          }
-      }
-      __syncthreads();
-      if (group == 0) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int j = 0; j < W; ++j) {
-            dw[s][j] += mine[(2 * (s * W + j)) * T];
-            db[s][j] += mine[(2 * (s * W + j) + 1) * T];
-          }
-      }
+    for (int s = 0; s < S; ++s) {
+      if (at[s].own == W) continue;
+      store_row<DET_F32, W>(pw, at[s].at, dw[s]);
+      store_row<DET_F32, W>(row_at<DET_F32>(pw, a.C), at[s].at, db[s]);
     }
+    return;
   }
-  if (group != 0) return;
-  float* const pw = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * a.C;
+  // the groups' sums, added in group order: runs of P columns, dealt to the groups
+  constexpr int P = W == 1 ? 1 : 4, Q = S * W / P;            // runs of dw; as many of db
+  using run = RunOf<P>;
+  run* const fold = reinterpret_cast<run*>(fold_lds);
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const int64_t at = static_cast<int64_t>(s * T + t) * W;
-    store_part<DET_F32, W>(pw, 0, at, a.C, dw[s]);
-    store_part<DET_F32, W>(pw, a.C, at, a.C, db[s]);
+  for (int q = 0; q < Q; ++q) {
+    constexpr int PER = W / P;
+    const int s = q / PER, j = q % PER * P;
+    run u, v;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      u.v[i] = dw[s][j + i];
+      v.v[i] = db[s][j + i];
+    }
+    fold[(group * 2 * Q + q) * a.T + t] = u;
+    fold[(group * 2 * Q + Q + q) * a.T + t] = v;
+  }
+  __syncthreads();
+  for (int q = group; q < 2 * Q; q += a.G) {
+    run v = fold[q * a.T + t];
+    for (int k = 1; k < a.G; ++k) {
+      const run u = fold[(k * 2 * Q + q) * a.T + t];
+#pragma unroll
+      for (int i = 0; i < P; ++i) v.v[i] += u.v[i];
+    }
+    const int qq = q < Q ? q : q - Q;
+    const Place to = place<W>(qq / (W / P), a.T, t, a.C);
+    if (to.own < W) store_row<DET_F32, P>(row_at<DET_F32>(pw, q < Q ? 0 : a.C), to.at + qq % (W / P) * P, v.v);
   }
 }
 
@@ -359,35 +459,49 @@ __device__ __forceinline__ void write_column(const ColArgs& a, int64_t col, D di
   if (bad) a.status[0] = 1;
 }
 
+// CB columns per workgroup: 64, or 32 or 16 (two or four chunks to a wave's
+// load) where 64 would leave CUs without one.
+template <int CB>
 __global__ __launch_bounds__(64 * COL_WAVES) void k_norm_columns(ColArgs a) {
-  __shared__ unsigned long long dg[NDIG][64];
-  __shared__ int32_t bad[64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = static_cast<int64_t>(blockIdx.x / a.split) * 64 + lane;
+  constexpr int PER = 64 / CB, STEP = COL_WAVES * PER, AHEAD = 8;
+  __shared__ unsigned long long dg[NDIG][CB];
+  __shared__ int32_t bad[CB];
+  const int lane = threadIdx.x & (CB - 1), lead = threadIdx.x / CB;
+  const int64_t col = static_cast<int64_t>(blockIdx.x / a.split) * CB + lane;
   const int part = static_cast<int>(blockIdx.x % a.split);
-  for (int i = threadIdx.x; i < NDIG * 64; i += 64 * COL_WAVES) dg[i / 64][i % 64] = 0ull;
-  if (threadIdx.x < 64) bad[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < NDIG * CB; i += 64 * COL_WAVES) dg[i / CB][i % CB] = 0ull;
+  if (threadIdx.x < CB) bad[threadIdx.x] = 0;
   __syncthreads();
   const bool in = col < 2 * a.C;
   const int64_t end = min(a.chunks, (part + 1) * a.per);
   if (in) {
-    for (int64_t k = part * a.per + wave; k < end; k += COL_WAVES) {
-      const uint32_t u = __float_as_uint(a.parts[k * 2 * a.C + col]);
-      const uint32_t ef = (u >> 23) & 0xFFu;
-      if (ef == 0xFFu) { bad[lane] = 1; continue; }
-      uint32_t sig = u & 0x7FFFFFu;
-      if (ef != 0u) sig |= 0x800000u;
-      const uint32_t o = max(ef, 1u) + 148u;
-      const uint64_t wide = static_cast<uint64_t>(sig) << (o & 31u);
-      int64_t lo = static_cast<int64_t>(wide & 0xFFFFFFFFull), hi = static_cast<int64_t>(wide >> 32);
-      if (u >> 31) { lo = -lo; hi = -hi; }
-      const int j = static_cast<int>(o >> 5) - DIG0;
-      atomicAdd(&dg[j][lane], static_cast<unsigned long long>(lo));
-      if (hi != 0) atomicAdd(&dg[j + 1][lane], static_cast<unsigned long long>(hi));
+    const float* const src = a.parts + col;
+    for (int64_t k0 = part * a.per + lead; k0 < end; k0 += AHEAD * STEP) {
+      float v[AHEAD];                     // past the end: the last chunk again, not added
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) v[i] = src[min(k0 + i * STEP, end - 1) * 2 * a.C];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const uint32_t u = k0 + i * STEP < end ? __float_as_uint(v[i]) : 0u;
+        const uint32_t ef = (u >> 23) & 0xFFu;
+        if (ef == 0xFFu) {
+          bad[lane] = 1;
+        } else if (u << 1) {
+          uint32_t sig = u & 0x7FFFFFu;
+          if (ef != 0u) sig |= 0x800000u;
+          const uint32_t o = max(ef, 1u) + 148u;
+          const uint64_t wide = static_cast<uint64_t>(sig) << (o & 31u);
+          int64_t lo = static_cast<int64_t>(wide & 0xFFFFFFFFull), hi = static_cast<int64_t>(wide >> 32);
+          if (u >> 31) { lo = -lo; hi = -hi; }
+          const int j = static_cast<int>(o >> 5) - DIG0;
+          atomicAdd(&dg[j][lane], static_cast<unsigned long long>(lo));
+          if (hi != 0) atomicAdd(&dg[j + 1][lane], static_cast<unsigned long long>(hi));
+        }
+      }
     }
   }
   __syncthreads();
-  if (threadIdx.x >= 64 || !in) return;
+  if (threadIdx.x >= CB || !in) return;
   auto digit = [&](int j) { return static_cast<int64_t>(dg[j][lane]); };
   if (a.split == 1) {
     write_column(a, col, digit, bad[lane] != 0);
@@ -416,11 +530,15 @@ __global__ __launch_bounds__(64) void k_norm_columns_join(ColArgs a) {
 // ---------------------------------------------------------------- host side
 
 int64_t chunks_of(int64_t N, int64_t C) { return ceil_div(N, chunk_rows(C)); }
-// column workgroups: at least 64 chunks (four per wave) to a run, at most SPLIT_MAX
-// runs, and no more than fill the chip twice
+// columns per workgroup of the exact sum
+int columns_of(int64_t C) { return 2 * C >= 64 * 256 ? 64 : 2 * C >= 32 * 256 ? 32 : 16; }
+// Runs of chunks per column: more than one only where a workgroup would have
+// over 2048 chunks to add (a wave then waits for 128 / PER times 8 loads,
+// longer than the join's launch), at most SPLIT_MAX, and no more than fill
+// the chip twice.
 int split_of(int64_t chunks, int64_t C) {
-  const int64_t cols = ceil_div(2 * C, 64);
-  return static_cast<int>(std::max<int64_t>(1, std::min({chunks / 64, static_cast<int64_t>(SPLIT_MAX),
+  const int64_t cols = ceil_div(2 * C, columns_of(C));
+  return static_cast<int>(std::max<int64_t>(1, std::min({chunks / 1024, static_cast<int64_t>(SPLIT_MAX),
                                                          ceil_div(512, cols)})));
 }
 int64_t parts_bytes(int64_t N, int64_t C) { return (chunks_of(N, C) * 2 * C * 4 + 15) / 16 * 16; }
@@ -441,51 +559,61 @@ det_status check_rows(int x_dt, int w_dt, int y_dt, const void* x, int64_t s_x, 
   return DET_OK;
 }
 
-// launches K<XT, YT, T, S, W, G> for the row width: T S W >= C
-#define DET_NORM_WIDTHS(LAUNCH, XT, YT)                                                        \
-  do {                                                                                         \
-    if constexpr (XT == DET_BF16 && YT == DET_BF16) {                                          \
-      if (C <= 512) LAUNCH(XT, YT, 64, 1, 8);                                                  \
-      else if (C <= 1024) LAUNCH(XT, YT, 64, 2, 8);                                            \
-      else if (C <= 2048) LAUNCH(XT, YT, 128, 2, 8);                                           \
-      else if (C <= 4096) LAUNCH(XT, YT, 256, 2, 8);                                           \
-      else if (C <= 8192) LAUNCH(XT, YT, 512, 2, 8);                                           \
-      else if (C <= 16384) LAUNCH(XT, YT, 1024, 2, 8);                                         \
-      else LAUNCH(XT, YT, 1024, 4, 8);                                                         \
-    } else {                                                                                   \
-      if (C <= 512) LAUNCH(XT, YT, 64, 2, 4);                                                  \
-      else if (C <= 1024) LAUNCH(XT, YT, 64, 4, 4);                                            \
-      else if (C <= 2048) LAUNCH(XT, YT, 128, 4, 4);                                           \
-      else if (C <= 4096) LAUNCH(XT, YT, 256, 4, 4);                                           \
-      else if (C <= 8192) LAUNCH(XT, YT, 512, 4, 4);                                           \
-      else if (C <= 16384) LAUNCH(XT, YT, 1024, 4, 4);                                         \
-      else LAUNCH(XT, YT, 1024, 8, 4);                                                         \
-    }                                                                                          \
-  } while (0)
-#define DET_NORM_TYPES(LAUNCH)                                                                 \
-  do {                                                                                         \
-    if (x_dt == DET_F32 && y_dt == DET_F32) DET_NORM_WIDTHS(LAUNCH, DET_F32, DET_F32);         \
-    else if (x_dt == DET_F32) DET_NORM_WIDTHS(LAUNCH, DET_F32, DET_BF16);                      \
-    else if (y_dt == DET_F32) DET_NORM_WIDTHS(LAUNCH, DET_BF16, DET_F32);                      \
-    else DET_NORM_WIDTHS(LAUNCH, DET_BF16, DET_BF16);                                          \
-  } while (0)
+// threads that hold a row of C elements, S W each
+int threads_of(int64_t C, int S, int W) { return static_cast<int>(ceil_div(C, 64 * S * W)) * 64; }
 
-template <int XT, int YT, int T, int S, int W>
+template <int XT, int YT, int S, int W, int MAXT>
 void launch_norm(NormArgs a, hipStream_t s) {
-  constexpr int G = T >= 256 ? 1 : 256 / T;
+  a.T = threads_of(a.C, S, W);
+  a.G = std::max(1, 256 / a.T);
   // enough workgroups for eight to a CU before rows share one (and its weights)
-  a.rows = static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, a.N / (2048 * G)))) * G;
-  hipLaunchKernelGGL((k_norm<XT, YT, T, S, W, G>), dim3(static_cast<unsigned>(ceil_div(a.N, a.rows))), dim3(T * G),
-                     0, s, a);
+  a.rows = static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, a.N / (2048 * a.G)))) * a.G;
+  hipLaunchKernelGGL((k_norm<XT, YT, S, W, MAXT>), dim3(static_cast<unsigned>(ceil_div(a.N, a.rows))), dim3(a.T, a.G), 0,
+                     s, a);
 }
 
-template <int XT, int YT, int T, int S, int W>
+template <int XT, int YT, int S, int W, int MAXT>
 void launch_norm_grad(NormGradArgs a, hipStream_t s) {
-  constexpr int G = 1024 / T;
+  a.T = threads_of(a.C, S, W);
+  a.G = std::max(1, std::min(8, 512 / a.T));
   a.chunk = chunk_rows(a.C);
-  const size_t lds = G > 1 ? static_cast<size_t>(T) * S * W * 2 * sizeof(float) : 0;
-  hipLaunchKernelGGL((k_norm_grad<XT, YT, T, S, W, G>), dim3(static_cast<unsigned>(chunks_of(a.N, a.C))),
-                     dim3(T * G), lds, s, a);
+  const size_t lds = a.G > 1 && a.parts != nullptr ? static_cast<size_t>(a.G) * a.T * S * W * 2 * sizeof(float) : 0;
+  hipLaunchKernelGGL((k_norm_grad<XT, YT, S, W, MAXT>), dim3(static_cast<unsigned>(ceil_div(a.N, a.chunk))),
+                     dim3(a.T, a.G), lds, s, a);
+}
+
+// Elements a thread holds.  Forward: 8 up to 512 columns, 16 up to 16384 (more
+// waves to a row wait longer at its barriers: 8 elements took 166 us on 16384 x
+// 8192 bf16, 16 take 106; 32 cost 12 % more on 4096 columns for their
+// registers).  Backward: 8 up to 8192 columns (dw, db and w take as much again
+// three times: 16 spill).
+template <int XT, int YT>
+void forward(const NormArgs& a, hipStream_t s) {
+  constexpr int W = XT == DET_BF16 && YT == DET_BF16 ? 8 : 4;
+  if (a.C < W) launch_norm<XT, YT, 1, 1, 512>(a, s);
+  else if (a.C <= 512) launch_norm<XT, YT, 8 / W, W, 512>(a, s);
+  else if (a.C <= 8192) launch_norm<XT, YT, 16 / W, W, 512>(a, s);
+  else if (a.C <= 16384) launch_norm<XT, YT, 16 / W, W, 1024>(a, s);
+  else launch_norm<XT, YT, 32 / W, W, 1024>(a, s);
+}
+template <int XT, int YT>
+void backward(const NormGradArgs& a, hipStream_t s) {
+  constexpr int W = XT == DET_BF16 && YT == DET_BF16 ? 8 : 4;
+  if (a.C < W) launch_norm_grad<XT, YT, 1, 1, 512>(a, s);
+  else if (a.C <= 512) launch_norm_grad<XT, YT, 8 / W, W, 512>(a, s);
+  else if (a.C <= 8192) launch_norm_grad<XT, YT, 8 / W, W, 1024>(a, s);
+  else if (a.C <= 16384) launch_norm_grad<XT, YT, 16 / W, W, 1024>(a, s);
+  else launch_norm_grad<XT, YT, 32 / W, W, 1024>(a, s);
+}
+template <class F>
+void by_types(int x_dt, int y_dt, F f) {
+  using std::integral_constant;
+  const auto f32 = integral_constant<int, DET_F32>{};
+  const auto bf16 = integral_constant<int, DET_BF16>{};
+  if (x_dt == DET_F32 && y_dt == DET_F32) f(f32, f32);
+  else if (x_dt == DET_F32) f(f32, bf16);
+  else if (y_dt == DET_F32) f(bf16, f32);
+  else f(bf16, bf16);
 }
 
 }  // namespace
@@ -504,13 +632,11 @@ det_status det_layer_norm(det_dtype x_dt, const void* x, int64_t s_x, det_dtype 
       !aligned_for(rstd, DET_F32))
     return fail(DET_EINVAL, "operands must be aligned to their element size");
   NormArgs a{};
-  a.x = x; a.s_x = s_x; a.w = w; a.b = b; a.N = N; a.C = C;
+  a.x = x; a.s_x = s_x; a.w = w; a.b = b; a.N = N; a.C = static_cast<int>(C);
   a.eps = static_cast<float>(eps); a.inv_c = 1.0f / static_cast<float>(C);
   a.w_dt = w_dt; a.y = y; a.mean = mean; a.rstd = rstd;
   hipStream_t s = static_cast<hipStream_t>(stream);
-#define DET_LAUNCH(XT, YT, T, S, W) launch_norm<XT, YT, T, S, W>(a, s)
-  DET_NORM_TYPES(DET_LAUNCH);
-#undef DET_LAUNCH
+  by_types(x_dt, y_dt, [&](auto xt, auto yt) { forward<decltype(xt)::value, decltype(yt)::value>(a, s); });
   return hip_check(hipGetLastError(), "layer norm launch");
 }
 
@@ -540,11 +666,9 @@ det_status det_layer_norm_grad(det_dtype x_dt, const void* x, int64_t s_x, det_d
   if (N > 0) {
     NormGradArgs a{};
     a.x = x; a.s_x = s_x; a.dy = dy; a.s_dy = s_dy; a.w = w; a.w_dt = w_dt;
-    a.mean = mean; a.rstd = rstd; a.N = N; a.C = C; a.inv_c = 1.0f / static_cast<float>(C);
+    a.mean = mean; a.rstd = rstd; a.N = N; a.C = static_cast<int>(C); a.inv_c = 1.0f / static_cast<float>(C);
     a.dx = dx; a.parts = sums ? static_cast<float*>(workspace) : nullptr;
-#define DET_LAUNCH(XT, YT, T, S, W) launch_norm_grad<XT, YT, T, S, W>(a, s)
-    DET_NORM_TYPES(DET_LAUNCH);
-#undef DET_LAUNCH
+    by_types(x_dt, y_dt, [&](auto xt, auto yt) { backward<decltype(xt)::value, decltype(yt)::value>(a, s); });
     st = hip_check(hipGetLastError(), "layer norm gradient launch");
     if (st != DET_OK) return st;
   }
@@ -562,11 +686,14 @@ det_status det_layer_norm_grad(det_dtype x_dt, const void* x, int64_t s_x, det_d
     c.sums = reinterpret_cast<int64_t*>(static_cast<char*>(workspace) + parts_bytes(N, C));
     c.bad = reinterpret_cast<int32_t*>(c.sums + c.split * 2 * C * NDIG);
   }
-  const int64_t cols = ceil_div(2 * C, 64);
-  hipLaunchKernelGGL(k_norm_columns, dim3(static_cast<unsigned>(cols * c.split)), dim3(64 * COL_WAVES), 0, s, c);
+  const int cb = columns_of(C);
+  const dim3 grid(static_cast<unsigned>(ceil_div(2 * C, cb) * c.split)), block(64 * COL_WAVES);
+  if (cb == 64) hipLaunchKernelGGL(k_norm_columns<64>, grid, block, 0, s, c);
+  else if (cb == 32) hipLaunchKernelGGL(k_norm_columns<32>, grid, block, 0, s, c);
+  else hipLaunchKernelGGL(k_norm_columns<16>, grid, block, 0, s, c);
   st = hip_check(hipGetLastError(), "column sum launch");
   if (st != DET_OK || c.split == 1) return st;
-  hipLaunchKernelGGL(k_norm_columns_join, dim3(static_cast<unsigned>(cols)), dim3(64), 0, s, c);
+  hipLaunchKernelGGL(k_norm_columns_join, dim3(static_cast<unsigned>(ceil_div(2 * C, 64))), dim3(64), 0, s, c);
   return hip_check(hipGetLastError(), "column join launch");
 }
 

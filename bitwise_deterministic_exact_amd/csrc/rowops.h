@@ -57,12 +57,20 @@ struct Elem<DET_BF16> {
   static constexpr int VE = 8, BYTES = 2;
 };
 
-struct __attribute__((packed, aligned(2))) Pack16 {
-  uint32_t w[4];
-};
-struct __attribute__((packed, aligned(4))) Pack16a4 {
-  uint32_t w[4];
-};
+// 16 and 8 bytes that start at any element
+using u32x4_a2 = uint32_t __attribute__((ext_vector_type(4), aligned(2)));
+using u32x4_a4 = uint32_t __attribute__((ext_vector_type(4), aligned(4)));
+using u32x2_a2 = uint32_t __attribute__((ext_vector_type(2), aligned(2)));
+#ifdef NT_LD
+#define LD(p) __builtin_nontemporal_load(p)
+#else
+#define LD(p) (*(p))
+#endif
+#ifdef NT_ST
+#define ST(p, v) __builtin_nontemporal_store(v, p)
+#else
+#define ST(p, v) (*(p) = (v))
+#endif
 
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using f32x2 = float __attribute__((ext_vector_type(2)));
@@ -100,26 +108,25 @@ __device__ __forceinline__ void load_vec(const void* p, int64_t i, float (&v)[W]
   if constexpr (DT == DET_F32) {
 #pragma unroll
     for (int j = 0; j < W / 4; ++j) {
-      const Pack16a4 u = reinterpret_cast<const Pack16a4*>(q)[j];
+      const u32x4_a4 u = LD(reinterpret_cast<const u32x4_a4*>(q) + j);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 * j + e] = __uint_as_float(u.w[e]);
+      for (int e = 0; e < 4; ++e) v[4 * j + e] = __uint_as_float(u[e]);
     }
   } else if constexpr (W == 4) {
-    struct __attribute__((packed, aligned(2))) P8 { uint32_t w[2]; };
-    const P8 u = *reinterpret_cast<const P8*>(q);
+    const u32x2_a2 u = LD(reinterpret_cast<const u32x2_a2*>(q));
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      v[2 * e] = __uint_as_float(u.w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(u.w[e] & 0xFFFF0000u);
+      v[2 * e] = __uint_as_float(u[e] << 16);
+      v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < W / 8; ++j) {
-      const Pack16 u = reinterpret_cast<const Pack16*>(q)[j];
+      const u32x4_a2 u = LD(reinterpret_cast<const u32x4_a2*>(q) + j);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[8 * j + 2 * e] = __uint_as_float(u.w[e] << 16);
-        v[8 * j + 2 * e + 1] = __uint_as_float(u.w[e] & 0xFFFF0000u);
+        v[8 * j + 2 * e] = __uint_as_float(u[e] << 16);
+        v[8 * j + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
       }
     }
   }
@@ -130,21 +137,21 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&v)[W
   if constexpr (DT == DET_F32) {
 #pragma unroll
     for (int j = 0; j < W / 4; ++j) {
-      Pack16a4 u;
+      u32x4_a4 u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u.w[e] = __float_as_uint(v[4 * j + e]);
-      reinterpret_cast<Pack16a4*>(q)[j] = u;
+      for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(v[4 * j + e]);
+      ST(reinterpret_cast<u32x4_a4*>(q) + j, u);
     }
   } else if constexpr (W == 4) {
-    struct __attribute__((packed, aligned(2))) P8 { uint32_t w[2]; };
-    *reinterpret_cast<P8*>(q) = P8{{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}};
+    const u32x2_a2 u = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    ST(reinterpret_cast<u32x2_a2*>(q), u);
   } else {
 #pragma unroll
     for (int j = 0; j < W / 8; ++j) {
-      Pack16 u;
+      u32x4_a2 u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u.w[e] = pack_bf16(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
-      reinterpret_cast<Pack16*>(q)[j] = u;
+      for (int e = 0; e < 4; ++e) u[e] = pack_bf16(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+      ST(reinterpret_cast<u32x4_a2*>(q) + j, u);
     }
   }
 }

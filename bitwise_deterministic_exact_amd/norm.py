@@ -8,7 +8,7 @@ A row's results are a function of that row: not of how many rows there are,
 nor of their strides or alignment.  The weights' gradients are sums over rows
 (tokens): chunks of consecutive rows in float32 in one fixed order, the chunks
 added exactly in the long accumulator and rounded once.  So rows sharded at
-multiples of NORM_SHARD_ROWS (32) give, through layer_norm_digits,
+multiples of NORM_SHARD_ROWS (64) give, through layer_norm_digits,
 det_combine and det_finalize, the bits of one call over all of them, as the
 K-shards of an exact GEMM do (det-train page, "Method").
 

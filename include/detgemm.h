@@ -413,7 +413,7 @@ int32_t* det_device_status_word(void);
 #define DET_ROWS_MAX ((int64_t)1 << 22)
 #define DET_HEAD_V_MAX ((int64_t)1 << 24)
 #define DET_NORM_C_MAX ((int64_t)32768)
-#define DET_NORM_SHARD_ROWS 32
+#define DET_NORM_SHARD_ROWS 64
 
 /*
  * det_layer_norm -- y = (x - mean) rstd w + b over each row of C elements,
@@ -445,9 +445,9 @@ det_status det_layer_norm(det_dtype x_dt, const void* x, int64_t s_x, det_dtype 
  *   workspace         det_layer_norm_grad_workspace_bytes(N, C), 16-byte
  *                     aligned; null when dw, db and digits all are
  * dw and db are summed in fp32 over chunks of consecutive rows in one fixed
- * order (DET_NORM_SHARD_ROWS = 32 rows, 16 for C <= 2048) and the chunks are
+ * order (64 for C <= 512, 16 for C <= 4096, else 32) and the chunks are
  * added exactly in the long accumulator and rounded once.  So the digits of
- * row shards cut at multiples of 32 rows add up (det_combine) to the digits
+ * row shards cut at multiples of DET_NORM_SHARD_ROWS add up (det_combine) to the digits
  * of all rows, and det_finalize of the sum gives the same bits as one call
  * over all rows, for any number of shards and any order of adding them.
  * An Inf or NaN chunk is noted in the device status; those sums are then NaN

@@ -98,12 +98,15 @@ def test_workspace_sizes():
     # rows that fill the chip alone, or fit one group of chunks, need none
     assert lib.det_head_workspace_bytes(4096, 131072, 0) == 0
     assert lib.det_head_workspace_bytes(1, 4 * 2048, 20) == 0
-    # 64 chunks of 12 bytes, 16 workgroups of 20 keys
-    assert lib.det_head_workspace_bytes(1, 131072, 20) == 64 * 12 + 16 * 20 * 8
+    # 64 chunks of 12 bytes, 16 workgroups of four waves' 20 keys
+    assert lib.det_head_workspace_bytes(1, 131072, 20) == 64 * 12 + 64 * 20 * 8
+    # alternatives: at most 16 workgroups to a row
+    assert lib.det_head_workspace_bytes(1, 1 << 20, 1) == 512 * 12 + 64 * 8
     assert lib.det_head_workspace_bytes(1, 0, 0) == 0 and lib.det_head_workspace_bytes(1, 100, 65) == 0
-    # chunk sums of dw and db: 32 rows to a chunk, 16 for C <= 2048
-    assert lib.det_layer_norm_grad_workspace_bytes(33, 4096) == 2 * 2 * 4096 * 4
-    assert lib.det_layer_norm_grad_workspace_bytes(33, 2048) == 3 * 2 * 2048 * 4
+    # chunk sums of dw and db: 64 rows to a chunk, 16 from 513 columns, 32 from 4097
+    assert lib.det_layer_norm_grad_workspace_bytes(65, 512) == 2 * 2 * 512 * 4
+    assert lib.det_layer_norm_grad_workspace_bytes(65, 4096) == 5 * 2 * 4096 * 4
+    assert lib.det_layer_norm_grad_workspace_bytes(65, 4100) == 3 * 2 * 4100 * 4
     assert lib.det_layer_norm_grad_workspace_bytes(0, 4096) == 0
 
 
