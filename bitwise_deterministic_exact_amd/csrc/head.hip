@@ -21,6 +21,9 @@
 
 #include "rowops.h"
 
+// every fused multiply-add below is written as one: the compiler forms none
+#pragma clang fp contract(off)
+
 namespace {
 
 using namespace rowops;
@@ -44,7 +47,7 @@ struct ScoreArgs {
   int nchunk;                             // ceil(V / CHUNK)
   int wpr;                                // waves of a workgroup that share a row (1, 2, 4)
   int nblk;                               // workgroups that share a row (> 1 only with wpr = 4)
-  int top, cap;                           // alternatives; candidates a wave's pool holds
+  int top;                                // alternatives
   // workspace of a row shared by several workgroups
   float* parts;                           // [N][nchunk][3]
   uint64_t* lists;                        // [N][nblk * WAVES][top]: the waves' lists, sorted, 0 at the end
@@ -122,98 +125,169 @@ __device__ __forceinline__ uint64_t lane_key_of_rank(uint64_t mine, int r) {
 
 // ---------------------------------------------------------------- one chunk
 
+// Vector i of a lane nominally starts at element base + (64 i + lane) VE; one
+// that would pass the row's end starts at V - VE instead, so every load is a
+// whole vector: its elements before the nominal start belong to the vector
+// before it.  (With the row's last elements one by one under a branch, the
+// loads of that wave waited for each other.)
 template <int DT>
+__device__ __forceinline__ int64_t vector_start(int64_t at, int64_t V) {
+  return V >= Elem<DT>::VE ? min(at, V - Elem<DT>::VE) : at;
+}
+
+// a chunk's logits as they are loaded; MASK: -inf in the places of elements
+// that are not the vector's own
+template <int DT, bool MASK, bool NT>
 __device__ __forceinline__ void load_chunk(const void* row, int64_t base, int64_t V, int lane,
                                            float (&v)[LANE_ELEMS]) {
   constexpr int VE = Elem<DT>::VE, NV = LANE_ELEMS / VE;
   if (base + CHUNK <= V) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      load_vec<DT, VE>(row, base + (i * 64 + lane) * VE, reinterpret_cast<float (&)[VE]>(v[i * VE]));
-  } else {
+      load_vec<DT, VE, NT>(row, base + (i * 64 + lane) * VE, reinterpret_cast<float (&)[VE]>(v[i * VE]));
+  } else if (V >= VE) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t at = base + (i * 64 + lane) * VE;
-      if (at + VE <= V) {
-        load_vec<DT, VE>(row, at, reinterpret_cast<float (&)[VE]>(v[i * VE]));
-      } else {
+    for (int i = 0; i < NV; ++i)
+      load_vec<DT, VE, NT>(row, vector_start<DT>(base + (i * 64 + lane) * VE, V),
+                           reinterpret_cast<float (&)[VE]>(v[i * VE]));
+    if constexpr (MASK) {
 #pragma unroll
-        for (int j = 0; j < VE; ++j) v[i * VE + j] = at + j < V ? load_elem<DT>(row, at + j) : -INFINITY;
+      for (int i = 0; i < NV; ++i) {
+        const int64_t at = base + (i * 64 + lane) * VE;
+        const int own = static_cast<int>(at - vector_start<DT>(at, V));
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[i * VE + j] = j >= own ? v[i * VE + j] : -INFINITY;
       }
     }
+  } else {                               // fewer elements than a vector: lane 0, one by one
+#pragma unroll
+    for (int j = 0; j < LANE_ELEMS; ++j)
+      v[j] = lane == 0 && j < V ? load_elem<DT>(row, j) : -INFINITY;
   }
 }
 
-// A wave's running list of its row's largest keys, in its part of the LDS:
-// `list` (top keys, sorted, L of them) and `pool` (list + candidates).
-//
-// A chunk's candidates are the elements above the list's last value (later
-// indices lose ties).  While the list is short, or when a chunk has more
-// candidates than the pool holds, the bar is raised first: each lane's largest
-// (value, vector) is a lower bound for one distinct element, so the top-th
-// largest of the 64 lane bests is a bar that at least `top` elements reach,
-// and all that reach it lie in `top` lanes, 32 elements each: the pool's size.
+// The largest keys of the logits a wave has seen, found without keeping the
+// logits.  Every chunk leaves only its lanes' maxima in the LDS; after at most
+// STEP_CHUNKS chunks the (lane, chunk) pairs whose best possible key passes
+// the bar are listed, and only those pairs' logits are read again (from the
+// caches), 64 vectors at a time.  On unordered rows that is little more than
+// one pair per key.  The bar is the last key of a full list; before that, the
+// top-th largest of the pairs' maxima, which at least `top` logits reach.
+// Candidates collect in a pool, which is ranked down to `top` keys (and the
+// bar raised) whenever 64 more might not fit, so ties, masks and rows built
+// against it cost time but no correctness.
+//   1024 x 131072 bf16, top 20: 108 us with the logits of a chunk kept in
+//   registers for its candidates (123 registers, a ranking per chunk).
+constexpr int STEP_CHUNKS = 8, POOL = 256;
+
+struct TopLds {
+  uint64_t pool[POOL];
+  uint64_t list[TOP_MAX];
+  float lane_max[STEP_CHUNKS * 64];
+  uint16_t pairs[STEP_CHUNKS * 64];
+};
+
 template <int DT>
 struct TopList {
   static constexpr int VE = Elem<DT>::VE, NV = LANE_ELEMS / VE;
-  uint64_t* pool;
-  uint64_t* list;
-  int top, cap, L;
-  float bar;                             // the list's last value once it is full
+  TopLds& m;
+  const void* row;
+  int64_t V;
+  int top, n;                            // n keys in the pool
+  uint64_t bar;                          // keys up to it are not wanted
 
-  __device__ __forceinline__ int append(const float (&v)[LANE_ELEMS], const float (&vmax)[NV], int64_t base,
-                                        int64_t V, int lane, bool full, uint64_t floor_key) {
-    const uint32_t fo = static_cast<uint32_t>(floor_key >> 32);
-    const float fv = floor_key == 0 ? -INFINITY : order_value(fo);
-    const uint32_t fvec = 0xFFFFFFFFu - static_cast<uint32_t>(floor_key);
-    int n = L;
+  __device__ __forceinline__ void prune(int lane) {
+    wave_sync();
+    rank_keys(m.pool, n, m.list, top, lane, 64);
+    wave_sync();
+    n = min(n, top);
+    if (lane < n) m.pool[lane] = m.list[lane];
+    wave_sync();
+    if (n == top) bar = max(bar, m.list[top - 1]);
+  }
+
+  // chunks first, first + step, ..: `count` of them, their lane maxima in m.lane_max
+  __device__ __forceinline__ void take(int64_t first, int64_t step, int count, int lane) {
+    wave_sync();
+    if (n < top) {
+      // the top-th largest of the pairs' maxima, bit by bit from the top; any
+      // value that exactly `top` of them reach will do
+      uint32_t o[STEP_CHUNKS], t = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint32_t vec = i * 64 + lane;
-      // at the floor's value only vectors up to the floor's count
-      const bool some = (!full || vmax[i] > bar) && (vmax[i] > fv || (vmax[i] == fv && vec <= fvec));
-      if (__ballot(some) == 0) continue;
+      for (int i = 0; i < STEP_CHUNKS; ++i) {
+        o[i] = 0;
+        if (i < count && (first + i * step) * CHUNK + lane * VE < V) o[i] = order_bits(m.lane_max[i * 64 + lane]);
+      }
+#pragma unroll 1
+      for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+        int reach = 0;
 #pragma unroll
+        for (int i = 0; i < STEP_CHUNKS; ++i)
+          if (i < count) reach += __popcll(__ballot(o[i] >= (t | bit)));
+        if (reach >= top) t |= bit;
+        if (reach == top) break;
+      }
+      bar = max(bar, static_cast<uint64_t>(t) << 32);         // below every logit of that value
+    }
+    int pairs = 0;
+    for (int i = 0; i < count; ++i) {
+      const bool hit = best_key(i, lane, first + i * step) > bar;
+      const uint64_t b = __ballot(hit);
+      if (hit)
+        m.pairs[pairs + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32),
+                                                  __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), 0))] =
+            static_cast<uint16_t>(i * 64 + lane);
+      pairs += __popcll(b);
+    }
+    wave_sync();
+    // NV lanes to a pair, one for each of its vectors
+    for (int p = lane / NV; p - lane / NV < pairs; p += 64 / NV) {
+      const int e = p < pairs ? m.pairs[p] : 0;
+      const int64_t ch = first + (e >> 6) * step;
+      const bool on = p < pairs && best_key(e >> 6, e & 63, ch) > bar;
+      if (__ballot(on) == 0) continue;
+      const int64_t at = ch * CHUNK + ((lane & (NV - 1)) * 64 + (e & 63)) * VE;
+      const int64_t from = vector_start<DT>(at, V);
+      float v[VE];
+#pragma unroll
+      for (int j = 0; j < VE; ++j) v[j] = -INFINITY;
+      if (on && at < V) {
+        if (V >= VE) {
+          load_vec<DT, VE>(row, from, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VE; ++j)
+            if (j < V) v[j] = load_elem<DT>(row, j);
+        }
+      }
+#pragma unroll 1
       for (int j = 0; j < VE; ++j) {
-        const float x = v[i * VE + j];
-        const int64_t at = base + static_cast<int64_t>(vec) * VE + j;
-        const bool in = at < V && (!full || x > bar) && (x > fv || (x == fv && vec <= fvec));
-        const uint64_t b = __ballot(in);
+        const float x = v[0];
+#pragma unroll
+        for (int i = 0; i + 1 < VE; ++i) v[i] = v[i + 1];
+        // NaN is no candidate: its row's results are NaN
+        const uint64_t key = on && from + j >= at && from + j < V && x == x
+                                 ? key_of(order_bits(x), static_cast<uint32_t>(from + j)) : 0;
+        uint64_t b = __ballot(key > bar);
         if (b == 0) continue;
-        const int pos = n + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32),
-                                                      __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), 0));
-        if (in && pos < cap) pool[pos] = key_of(order_bits(x), static_cast<uint32_t>(at));
+        if (n + 64 > POOL) {
+          prune(lane);
+          b = __ballot(key > bar);
+          if (b == 0) continue;
+        }
+        if (key > bar)
+          m.pool[n + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32),
+                                               __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), 0))] = key;
         n += __popcll(b);
       }
     }
-    return n;
+    prune(lane);
   }
 
-  __device__ __forceinline__ uint64_t raise(const float (&vmax)[NV], float lane_max, int64_t base, int64_t V,
-                                            int lane) const {
-    uint32_t first = 0;
-#pragma unroll
-    for (int i = NV - 1; i >= 0; --i)
-      if (vmax[i] == lane_max) first = i * 64 + lane;
-    const uint64_t mine = base + static_cast<int64_t>(lane) * VE < V ? key_of(order_bits(lane_max), first) : 0;
-    return lane_key_of_rank(mine, top - 1);
-  }
-
-  __device__ __forceinline__ void add(const float (&v)[LANE_ELEMS], const float (&vmax)[NV], float lane_max,
-                                      int64_t base, int64_t V, int lane) {
-    const bool full = L == top;
-    if (full && __ballot(lane_max > bar) == 0) return;
-    int n = cap + 1;
-    if (full) n = append(v, vmax, base, V, lane, true, 0);
-    if (n > cap) n = append(v, vmax, base, V, lane, full, raise(vmax, lane_max, base, V, lane));
-    if (n > cap) n = cap;                // cannot be: the raised bar leaves at most 32 top candidates
-    wave_sync();
-    rank_keys(pool, n, list, top, lane, 64);
-    wave_sync();
-    L = n < top ? n : top;
-    for (int e = lane; e < L; e += 64) pool[e] = list[e];
-    wave_sync();
-    if (L == top) bar = order_value(static_cast<uint32_t>(list[top - 1] >> 32));
+  // no logit of lane `l` in the i-th listed chunk has a larger key
+  __device__ __forceinline__ uint64_t best_key(int i, int l, int64_t ch) const {
+    const int64_t at = ch * CHUNK + l * VE;
+    return at < V ? key_of(order_bits(m.lane_max[i * 64 + l]), static_cast<uint32_t>(at)) : 0;
   }
 };
 
@@ -341,7 +415,6 @@ __device__ __forceinline__ void finish_distill(const ScoreArgs& a, const RowSums
 // of at most one or two chunks share a workgroup (wpr = 1, 2).
 template <int DT, bool TOP>
 __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
-  constexpr int VE = Elem<DT>::VE, NV = LANE_ELEMS / VE;
   extern __shared__ __align__(16) uint64_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rpb = WAVES / a.wpr;                              // rows per workgroup
@@ -351,28 +424,25 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
   const int rw = wave % a.wpr;                                // this wave within the row and workgroup
   const bool live = row < a.N;
   const bool whole = a.nblk == 1;
-  // LDS: per wave a pool (cap) and a list (top); then the rows' chunk sums
-  const int per_wave = a.cap + (a.top + 1) / 2 * 2;           // even: the pools stay 16-byte aligned
-  uint64_t* const pool = lds + wave * per_wave;
-  uint64_t* const list = pool + a.cap;
-  float* const lparts = reinterpret_cast<float*>(lds + WAVES * per_wave);
+  // LDS: the waves' lists, then the rows' chunk sums
+  TopLds* const tops = reinterpret_cast<TopLds*>(lds);
+  float* const lparts = reinterpret_cast<float*>(tops + (TOP ? WAVES : 0));
   float* const parts = whole ? lparts + (wave / a.wpr) * a.nchunk * 3 : a.parts + row * a.nchunk * 3;
+  TopLds& mine = tops[wave];             // not touched without TOP
 
-  TopList<DT> tl{pool, list, a.top, a.cap, 0, 0.0f};
   if (live) {
     const void* const zr = static_cast<const char*>(a.z) + row * a.s_row * Elem<DT>::BYTES;
-    for (int ch = part * a.wpr + rw; ch < a.nchunk; ch += a.nblk * a.wpr) {
+    TopList<DT> tl{mine, zr, a.V, a.top, 0, 0};
+    const int step = a.nblk * a.wpr;
+    int waiting = 0;                     // chunks whose lane maxima wait for `take`
+    for (int ch = part * a.wpr + rw; ch < a.nchunk; ch += step) {
       const int64_t base = static_cast<int64_t>(ch) * CHUNK;
       float v[LANE_ELEMS];
-      load_chunk<DT>(zr, base, a.V, lane, v);
-      float vmax[NV], lane_max = -INFINITY;
+      // read once (alternatives are read again from where the loads left them)
+      load_chunk<DT, true, !TOP>(zr, base, a.V, lane, v);
+      float lane_max = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        vmax[i] = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < VE; ++j) vmax[i] = fmaxf(vmax[i], v[i * VE + j]);
-        lane_max = fmaxf(lane_max, vmax[i]);
-      }
+      for (int j = 0; j < LANE_ELEMS; ++j) lane_max = fmaxf(lane_max, v[j]);
       const float m = wave_max(lane_max);
       const float ref = m == -INFINITY ? 0.0f : m;
       float s = 0.0f, u = 0.0f;
@@ -381,14 +451,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
         const float d = (v[j] - ref) * a.c;
         const float e = __builtin_amdgcn_exp2f(d);
         s += e;
-        u += e * d;
+        u = fmaf(e, d, u);
       }
       if (u != u && s == s) {            // 0 * -inf: masked logits add nothing
         u = 0.0f;
 #pragma unroll
         for (int j = 0; j < LANE_ELEMS; ++j) {
           const float d = (v[j] - ref) * a.c;
-          u += __builtin_amdgcn_exp2f(d) * fmaxf(d, -2000.0f);
+          u = fmaf(__builtin_amdgcn_exp2f(d), fmaxf(d, -2000.0f), u);
         }
       }
       s = wave_sum(s);
@@ -398,28 +468,38 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
         parts[3 * ch + 1] = s;
         parts[3 * ch + 2] = u;
       }
-      if constexpr (TOP) tl.add(v, vmax, lane_max, base, a.V, lane);
+      if constexpr (TOP) {
+        mine.lane_max[waiting * 64 + lane] = lane_max;
+        ++waiting;
+        if (waiting == STEP_CHUNKS || ch + step >= a.nchunk) {
+          tl.take(ch - static_cast<int64_t>(waiting - 1) * step, step, waiting, lane);
+          waiting = 0;
+        }
+      }
     }
-    if constexpr (TOP)
-      for (int e = tl.L + lane; e < a.top; e += 64) list[e] = 0;     // a wave with few elements
-    wave_sync();
+    if constexpr (TOP) {
+      if (lane >= tl.n && lane < a.top) mine.list[lane] = 0;  // a wave with few elements
+      wave_sync();
+    }
   }
   if (whole) __syncthreads();            // uniform: the other waves' sums and lists
   if (!live) return;
   if (!whole) {                          // k_score_join does the rest
-    if (TOP && lane < a.top) a.lists[((row * a.nblk + part) * WAVES + wave) * a.top + lane] = list[lane];
+    if (TOP && lane < a.top) a.lists[((row * a.nblk + part) * WAVES + wave) * a.top + lane] = mine.list[lane];
     return;
   }
   if (rw != 0) return;
+  const uint64_t* list = mine.list;
   if (TOP && a.wpr > 1) {
-    // the row's wave lists, gathered into this wave's pool (cap >= wpr * top), joined
+    // the row's wave lists, gathered into this wave's pool, joined into the next one's
     for (int w = 0; w < a.wpr; ++w)
-      if (lane < a.top) pool[w * a.top + lane] = lds[(wave + w) * per_wave + a.cap + lane];
+      if (lane < a.top) mine.pool[w * a.top + lane] = tops[wave + w].list[lane];
+    uint64_t* const joined = tops[wave + 1].pool;
+    if (lane < a.top) joined[lane] = 0;  // a row with a NaN may hold fewer than `top` keys
     wave_sync();
-    if (lane < a.top) list[lane] = 0;    // a workgroup may hold fewer than `top` elements
+    rank_keys(mine.pool, a.wpr * a.top, joined, a.top, lane, 64);
     wave_sync();
-    rank_keys(pool, a.wpr * a.top, list, a.top, lane, 64);
-    wave_sync();
+    list = joined;
   }
   const RowSums r = join(a, parts, row, lane);
   if (a.mode == MODE_DISTILL) finish_distill(a, r, row, lane);
@@ -428,10 +508,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
 }
 
 // The end of rows that several workgroups shared: one workgroup per row.  Of
-// the n lists' keys only those can be among the top that reach a bar: with j =
-// ceil(top / n), the ceil(top / j)-th largest of the lists' j-th keys, which
-// at least `top` keys reach.  On unordered rows that leaves about 1.5 top keys
-// of n top to be ranked.
+// the lists' keys only those can be among the top that reach a bar: for any j,
+// the ceil(top / j)-th largest of the lists' j-th keys, which at least `top`
+// keys reach.  With j = ceil(2 top / n) of n lists, on unordered rows, about
+// twice `top` keys reach it and are ranked.
 __global__ __launch_bounds__(256) void k_score_join(ScoreArgs a) {
   extern __shared__ __align__(16) uint64_t lds[];
   __shared__ int count;
@@ -444,8 +524,11 @@ __global__ __launch_bounds__(256) void k_score_join(ScoreArgs a) {
   if (a.top > 0) {
     const uint64_t* const src = a.lists + row * n;
     if (threadIdx.x < 64) {
-      const int j = (a.top + lists - 1) / lists;
-      const uint64_t b = lane_key_of_rank(lane < lists ? src[lane * a.top + j - 1] : 0, (a.top + j - 1) / j - 1);
+      const bool some = lane < lists && src[lane * a.top] != 0;
+      const int held = max(__popcll(__ballot(some)), 1);      // lists with a key (none: a row of NaN)
+      const int j = min((2 * a.top + held - 1) / held, a.top);
+      uint64_t b = lane_key_of_rank(some ? src[lane * a.top + j - 1] : 0, (a.top + j - 1) / j - 1);
+      if (b == 0) b = lane_key_of_rank(some ? src[lane * a.top + a.top - 1] : 0, 0);   // short lists
       if (lane == 0) {
         bar = b > 0 ? b : 1;
         count = 0;
@@ -561,19 +644,28 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
   for (int ch = part * WAVES + wave; ch < a.nchunk; ch += a.nblk * WAVES) {
     const int64_t base = static_cast<int64_t>(ch) * CHUNK;
     float v[LANE_ELEMS];
-    load_chunk<DT>(zr, base, a.V, lane, v);
+    load_chunk<DT, false, false>(zr, base, a.V, lane, v);
 #pragma unroll
     for (int j = 0; j < LANE_ELEMS; ++j) v[j] = grad_elem<ENT>(r, v[j]);
-    const bool full = base + CHUNK <= a.V;
+    if (base + CHUNK <= a.V) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t at = base + (i * 64 + lane) * VE;
-      if (full || at + VE <= a.V) {
-        store_vec<DT, VE>(dr, at, reinterpret_cast<const float (&)[VE]>(v[i * VE]));
-      } else {
+      for (int i = 0; i < NV; ++i)
+        store_vec<DT, VE>(dr, base + (i * 64 + lane) * VE, reinterpret_cast<const float (&)[VE]>(v[i * VE]));
+    } else {
+      // a vector that was moved back from the row's end writes its first
+      // elements a second time, with the same values; where they are the
+      // chunk's before (another wave's, perhaps another workgroup's), only its own
 #pragma unroll
-        for (int j = 0; j < VE; ++j)
-          if (at + j < a.V) store_elem<DT>(dr, at + j, v[i * VE + j]);
+      for (int i = 0; i < NV; ++i) {
+        const int64_t at = base + (i * 64 + lane) * VE, from = vector_start<DT>(at, a.V);
+        if (at >= a.V) continue;
+        if (from >= base && a.V >= VE) {
+          store_vec<DT, VE>(dr, from, reinterpret_cast<const float (&)[VE]>(v[i * VE]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < VE; ++j)
+            if (from + j >= at && from + j < a.V) store_elem<DT>(dr, from + j, v[i * VE + j]);
+        }
       }
     }
   }
@@ -634,7 +726,6 @@ det_status launch_score(ScoreArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
   a.nblk = blocks_per_row(a.N, a.nchunk, a.top);
   a.wpr = a.nchunk >= WAVES ? WAVES : a.nchunk;
   if (a.wpr == 3) a.wpr = 4;
-  a.cap = a.top > 0 ? ((LANE_ELEMS + 1) * a.top + 15) / 16 * 16 : 0;   // rank_keys reads to a multiple of 16
   a.status = det_device_status_word();
   if (a.status == nullptr) return DET_EHIP;
   if (a.nblk > 1) {
@@ -647,7 +738,7 @@ det_status launch_score(ScoreArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
   }
   const int rpb = WAVES / a.wpr;
   const int64_t blocks = a.nblk > 1 ? a.N * a.nblk : ceil_div(a.N, rpb);
-  const size_t lds = static_cast<size_t>(WAVES) * (a.cap + (a.top + 1) / 2 * 2) * 8 +
+  const size_t lds = (a.top > 0 ? WAVES * sizeof(TopLds) : 0) +
                      (a.nblk > 1 ? 0 : static_cast<size_t>(rpb) * a.nchunk * 12);
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * WAVES);
   if (a.dt == DET_F32) {

@@ -61,16 +61,12 @@ struct Elem<DET_BF16> {
 using u32x4_a2 = uint32_t __attribute__((ext_vector_type(4), aligned(2)));
 using u32x4_a4 = uint32_t __attribute__((ext_vector_type(4), aligned(4)));
 using u32x2_a2 = uint32_t __attribute__((ext_vector_type(2), aligned(2)));
-#ifdef NT_LD
-#define LD(p) __builtin_nontemporal_load(p)
-#else
-#define LD(p) (*(p))
-#endif
-#ifdef NT_ST
-#define ST(p, v) __builtin_nontemporal_store(v, p)
-#else
-#define ST(p, v) (*(p) = (v))
-#endif
+// NT: data that is read once and is not wanted in the caches
+template <bool NT, class T>
+__device__ __forceinline__ T load_as(const T* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  else return *p;
+}
 
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using f32x2 = float __attribute__((ext_vector_type(2)));
@@ -102,18 +98,18 @@ __device__ __forceinline__ void store_elem(int dt, void* p, int64_t i, float v) 
 
 // W consecutive elements from element i on, W a multiple of a 16-byte access's
 // VE or (bf16) half of one
-template <int DT, int W>
+template <int DT, int W, bool NT = false>
 __device__ __forceinline__ void load_vec(const void* p, int64_t i, float (&v)[W]) {
   const char* const q = static_cast<const char*>(p) + i * Elem<DT>::BYTES;
   if constexpr (DT == DET_F32) {
 #pragma unroll
     for (int j = 0; j < W / 4; ++j) {
-      const u32x4_a4 u = LD(reinterpret_cast<const u32x4_a4*>(q) + j);
+      const u32x4_a4 u = load_as<NT>(reinterpret_cast<const u32x4_a4*>(q) + j);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * j + e] = __uint_as_float(u[e]);
     }
   } else if constexpr (W == 4) {
-    const u32x2_a2 u = LD(reinterpret_cast<const u32x2_a2*>(q));
+    const u32x2_a2 u = load_as<NT>(reinterpret_cast<const u32x2_a2*>(q));
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       v[2 * e] = __uint_as_float(u[e] << 16);
@@ -122,7 +118,7 @@ __device__ __forceinline__ void load_vec(const void* p, int64_t i, float (&v)[W]
   } else {
 #pragma unroll
     for (int j = 0; j < W / 8; ++j) {
-      const u32x4_a2 u = LD(reinterpret_cast<const u32x4_a2*>(q) + j);
+      const u32x4_a2 u = load_as<NT>(reinterpret_cast<const u32x4_a2*>(q) + j);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[8 * j + 2 * e] = __uint_as_float(u[e] << 16);
@@ -140,18 +136,18 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&v)[W
       u32x4_a4 u;
 #pragma unroll
       for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(v[4 * j + e]);
-      ST(reinterpret_cast<u32x4_a4*>(q) + j, u);
+      *(reinterpret_cast<u32x4_a4*>(q) + j) = u;
     }
   } else if constexpr (W == 4) {
     const u32x2_a2 u = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-    ST(reinterpret_cast<u32x2_a2*>(q), u);
+    *(reinterpret_cast<u32x2_a2*>(q)) = u;
   } else {
 #pragma unroll
     for (int j = 0; j < W / 8; ++j) {
       u32x4_a2 u;
 #pragma unroll
       for (int e = 0; e < 4; ++e) u[e] = pack_bf16(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
-      ST(reinterpret_cast<u32x4_a2*>(q) + j, u);
+      *(reinterpret_cast<u32x4_a2*>(q) + j) = u;
     }
   }
 }
