@@ -113,6 +113,11 @@ __device__ __forceinline__ void rank_keys(const uint64_t* pool, int n, uint64_t*
   }
 }
 
+// how many lanes below this one are set in b
+__device__ __forceinline__ int lanes_below(uint64_t b) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), 0));
+}
+
 // the key of rank r (0 = largest) among the lanes' distinct nonzero keys, or
 // 0 when there are not that many
 __device__ __forceinline__ uint64_t lane_key_of_rank(uint64_t mine, int r) {
@@ -196,8 +201,40 @@ struct TopList {
   int top, n;                            // n keys in the pool
   uint64_t bar;                          // keys up to it are not wanted
 
+  // down to `top` keys: 64 or fewer by rank, sorted; more by the largest value
+  // that `top` of them reach, bit by bit (ranking 256 keys took 10 us)
   __device__ __forceinline__ void prune(int lane) {
     wave_sync();
+    if (n > 64) {
+      uint64_t k[POOL / 64], t = 0;
+#pragma unroll
+      for (int i = 0; i < POOL / 64; ++i) k[i] = i * 64 + lane < n ? m.pool[i * 64 + lane] : 0;
+      // one value throughout (masked or constant logits): only the indices decide
+      int same = 0;
+#pragma unroll
+      for (int i = 0; i < POOL / 64; ++i) same += __popcll(__ballot(k[i] != 0 && (k[i] >> 32) == (bar >> 32)));
+      if (same == n) t = bar & 0xFFFFFFFF00000000ull;
+#pragma unroll 1
+      for (int bit = same == n ? 31 : 63; bit >= 0; --bit) {
+        const uint64_t c = t | (1ull << bit);
+        int reach = 0;
+#pragma unroll
+        for (int i = 0; i < POOL / 64; ++i) reach += __popcll(__ballot(k[i] >= c));
+        if (reach >= top) t = c;
+        if (reach == top) break;
+      }
+      wave_sync();
+      n = 0;
+#pragma unroll
+      for (int i = 0; i < POOL / 64; ++i) {
+        const uint64_t b = __ballot(k[i] >= t);
+        if (k[i] >= t) m.pool[n + lanes_below(b)] = k[i];
+        n += __popcll(b);
+      }
+      bar = max(bar, t);
+      wave_sync();
+      return;
+    }
     rank_keys(m.pool, n, m.list, top, lane, 64);
     wave_sync();
     n = min(n, top);
@@ -207,7 +244,8 @@ struct TopList {
   }
 
   // chunks first, first + step, ..: `count` of them, their lane maxima in m.lane_max
-  __device__ __forceinline__ void take(int64_t first, int64_t step, int count, int lane) {
+  // and the largest of them
+  __device__ __forceinline__ void take(int64_t first, int64_t step, int count, float largest, int lane) {
     wave_sync();
     if (n < top) {
       // the top-th largest of the pairs' maxima, bit by bit from the top; any
@@ -218,8 +256,14 @@ struct TopList {
         o[i] = 0;
         if (i < count && (first + i * step) * CHUNK + lane * VE < V) o[i] = order_bits(m.lane_max[i * 64 + lane]);
       }
+      const uint32_t most = order_bits(largest);              // of masked or constant logits, all of them
+      int ties = 0;
+#pragma unroll
+      for (int i = 0; i < STEP_CHUNKS; ++i)
+        if (i < count) ties += __popcll(__ballot(o[i] == most));
+      if (ties >= top) t = most;
 #pragma unroll 1
-      for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+      for (uint32_t bit = ties >= top ? 0u : 0x80000000u; bit != 0; bit >>= 1) {
         int reach = 0;
 #pragma unroll
         for (int i = 0; i < STEP_CHUNKS; ++i)
@@ -234,9 +278,7 @@ struct TopList {
       const bool hit = best_key(i, lane, first + i * step) > bar;
       const uint64_t b = __ballot(hit);
       if (hit)
-        m.pairs[pairs + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32),
-                                                  __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), 0))] =
-            static_cast<uint16_t>(i * 64 + lane);
+        m.pairs[pairs + lanes_below(b)] = static_cast<uint16_t>(i * 64 + lane);
       pairs += __popcll(b);
     }
     wave_sync();
@@ -275,12 +317,11 @@ struct TopList {
           b = __ballot(key > bar);
           if (b == 0) continue;
         }
-        if (key > bar)
-          m.pool[n + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32),
-                                               __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), 0))] = key;
+        if (key > bar) m.pool[n + lanes_below(b)] = key;
         n += __popcll(b);
       }
     }
+    if (n > 64) prune(lane);             // a selection; then the list, sorted
     prune(lane);
   }
 
@@ -435,6 +476,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
     TopList<DT> tl{mine, zr, a.V, a.top, 0, 0};
     const int step = a.nblk * a.wpr;
     int waiting = 0;                     // chunks whose lane maxima wait for `take`
+    float largest = -INFINITY;
     for (int ch = part * a.wpr + rw; ch < a.nchunk; ch += step) {
       const int64_t base = static_cast<int64_t>(ch) * CHUNK;
       float v[LANE_ELEMS];
@@ -471,9 +513,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
       if constexpr (TOP) {
         mine.lane_max[waiting * 64 + lane] = lane_max;
         ++waiting;
+        largest = fmaxf(largest, m);
         if (waiting == STEP_CHUNKS || ch + step >= a.nchunk) {
-          tl.take(ch - static_cast<int64_t>(waiting - 1) * step, step, waiting, lane);
+          tl.take(ch - static_cast<int64_t>(waiting - 1) * step, step, waiting, largest, lane);
           waiting = 0;
+          largest = -INFINITY;
         }
       }
     }
@@ -516,38 +560,40 @@ __global__ __launch_bounds__(256) void k_score_join(ScoreArgs a) {
   extern __shared__ __align__(16) uint64_t lds[];
   __shared__ int count;
   __shared__ uint64_t bar;
+  __shared__ RowSums sums;
   const int64_t row = blockIdx.x;
+  if (threadIdx.x >= 192) {               // the last wave: everything but the alternatives
+    const RowSums r = join(a, a.parts + row * a.nchunk * 3, row, threadIdx.x - 192);
+    if (threadIdx.x == 192) sums = r;
+    if (a.mode == MODE_DISTILL) finish_distill(a, r, row, threadIdx.x - 192);
+    else finish_score(a, r, row, threadIdx.x - 192);
+  }
+  if (a.top == 0) return;                 // uniform
   const int lane = threadIdx.x & 63;
   const int lists = a.nblk * WAVES, n = lists * a.top;
   uint64_t* const best = lds;                                 // [top]
   uint64_t* const pool = lds + TOP_MAX;                       // [n + 16]: the keys that reach the bar
-  if (a.top > 0) {
-    const uint64_t* const src = a.lists + row * n;
-    if (threadIdx.x < 64) {
-      const bool some = lane < lists && src[lane * a.top] != 0;
-      const int held = max(__popcll(__ballot(some)), 1);      // lists with a key (none: a row of NaN)
-      const int j = min((2 * a.top + held - 1) / held, a.top);
-      uint64_t b = lane_key_of_rank(some ? src[lane * a.top + j - 1] : 0, (a.top + j - 1) / j - 1);
-      if (b == 0) b = lane_key_of_rank(some ? src[lane * a.top + a.top - 1] : 0, 0);   // short lists
-      if (lane == 0) {
-        bar = b > 0 ? b : 1;
-        count = 0;
-      }
+  const uint64_t* const src = a.lists + row * n;
+  if (threadIdx.x < 64) {
+    const bool some = lane < lists && src[lane * a.top] != 0;
+    const int held = max(__popcll(__ballot(some)), 1);      // lists with a key (none: a row of NaN)
+    const int j = min((2 * a.top + held - 1) / held, a.top);
+    uint64_t b = lane_key_of_rank(some ? src[lane * a.top + j - 1] : 0, (a.top + j - 1) / j - 1);
+    if (b == 0) b = lane_key_of_rank(some ? src[lane * a.top + a.top - 1] : 0, 0);   // short lists
+    if (lane == 0) {
+      bar = b > 0 ? b : 1;
+      count = 0;
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < n; e += 256) {
-      const uint64_t key = src[e];
-      if (key >= bar) pool[atomicAdd(&count, 1)] = key;
-    }
-    __syncthreads();
-    rank_keys(pool, count, best, a.top, threadIdx.x, 256);
-    __syncthreads();
   }
-  if (threadIdx.x >= 64) return;
-  const RowSums r = join(a, a.parts + row * a.nchunk * 3, row, lane);
-  if (a.mode == MODE_DISTILL) finish_distill(a, r, row, lane);
-  else finish_score(a, r, row, lane);
-  if (a.top > 0) write_top(a, r, row, best, lane);
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += 256) {
+    const uint64_t key = src[e];
+    if (key >= bar) pool[atomicAdd(&count, 1)] = key;
+  }
+  __syncthreads();
+  rank_keys(pool, count, best, a.top, threadIdx.x, 256);
+  __syncthreads();
+  if (threadIdx.x < 64) write_top(a, sums, row, best, lane);
 }
 
 // ---------------------------------------------------------------- gradients

@@ -41,11 +41,12 @@ using namespace rowops;
 // way; backward 97 and 61); with the tail's stores element by element the
 // backward took 120 us.
 
-// rows whose dw and db are added in fp32: each divides DET_NORM_SHARD_ROWS.
-// Few rows mean many workgroups (16 rows of 4096 columns: two per CU at 8192
-// tokens) but more chunk sums to write and add again (8 bytes per column and
-// chunk against 6 per element: 8 % at 16 rows, 4 % at 32).
-constexpr int chunk_rows(int64_t C) { return C <= 512 ? 64 : C <= 4096 ? 16 : 32; }
+// Rows whose dw and db are added in fp32: each divides DET_NORM_SHARD_ROWS.
+// Few rows mean many workgroups (16 rows: two per CU at 8192 tokens) but more
+// chunk sums to write and add again (8 bytes per column and chunk against 6
+// per element: 8 % at 16 rows, 4 % at 32).  Wide rows of 8193 and more fill a
+// CU with one workgroup each: 16 again (3868 x 12995 bf16 132 -> 90 us).
+constexpr int chunk_rows(int64_t C) { return C <= 512 ? 64 : C <= 4096 || C > 8192 ? 16 : 32; }
 
 // W elements of type DT as loaded, 16 or 8 bytes
 template <int DT, int W>
@@ -57,21 +58,22 @@ struct Raw {
     for (int i = 0; i < U; ++i) u[i] = 0u;
   }
   // from element `at` of the row at p (a scalar address, a 32-bit offset)
+  template <bool NT = false>
   __device__ __forceinline__ void load(const char* p, int at) {
     const char* const q = p + static_cast<uint32_t>(at * Elem<DT>::BYTES);
     if constexpr (W == 1) {
       if constexpr (DT == DET_F32) u[0] = *reinterpret_cast<const uint32_t*>(q);
       else u[0] = *reinterpret_cast<const uint16_t*>(q);
     } else if constexpr (U == 4 && DT == DET_F32) {
-      const u32x4_a4 v = *reinterpret_cast<const u32x4_a4*>(q);
+      const u32x4_a4 v = load_as<NT>(reinterpret_cast<const u32x4_a4*>(q));
 #pragma unroll
       for (int i = 0; i < 4; ++i) u[i] = v[i];
     } else if constexpr (U == 4) {
-      const u32x4_a2 v = *reinterpret_cast<const u32x4_a2*>(q);
+      const u32x4_a2 v = load_as<NT>(reinterpret_cast<const u32x4_a2*>(q));
 #pragma unroll
       for (int i = 0; i < 4; ++i) u[i] = v[i];
     } else {
-      const u32x2_a2 v = *reinterpret_cast<const u32x2_a2*>(q);
+      const u32x2_a2 v = load_as<NT>(reinterpret_cast<const u32x2_a2*>(q));
       u[0] = v[0];
       u[1] = v[1];
     }
@@ -167,8 +169,10 @@ struct NormArgs {
 // written.  (Moments per wave joined behind one barrier instead of two: the
 // same time on bf16 rows of 4096, 20 % more on 5120, from 115 registers
 // instead of 84.)
-template <int XT, int YT, int S, int W, int MAXT>
-__global__ __launch_bounds__(MAXT) void k_norm(NormArgs a) {
+// ONCE: no gradient will read x again, so it is read past the caches (16384 x
+// 8192 bf16 106 -> 91 us; where the gradient follows, 282 us against 289).
+template <int XT, int YT, int S, int W, int MAXT, bool ONCE, bool AHEAD>
+__global__ __launch_bounds__(MAXT, 4) void k_norm(NormArgs a) {
   __shared__ RowSum sm;
   int turn = 0;
   // a workgroup is T x G threads and T whole waves: a wave's row, and its address, are scalars
@@ -186,12 +190,13 @@ __global__ __launch_bounds__(MAXT) void k_norm(NormArgs a) {
   auto fetch = [&](int64_t row) {         // past the last row: that row again, not used
     const char* const x = row_at<XT>(a.x, min(row, a.N - 1) * a.s_x);
 #pragma unroll
-    for (int s = 0; s < S; ++s) next[s].load(x, at[s].at);
+    for (int s = 0; s < S; ++s) next[s].template load<ONCE>(x, at[s].at);
   };
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows;
-  fetch(row0 + group);
+  if constexpr (AHEAD) fetch(row0 + group);
   for (int r = group; r < a.rows; r += a.G) {
     const int64_t row = row0 + r;
+    if constexpr (!AHEAD) fetch(row);
     float v[S][W];
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -200,7 +205,7 @@ __global__ __launch_bounds__(MAXT) void k_norm(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < W; ++j) sum[0] += j >= at[s].own ? v[s][j] : 0.0f;
     }
-    if (r + a.G < a.rows) fetch(row + a.G);
+    if (AHEAD && r + a.G < a.rows) fetch(row + a.G);
     row_sum(sm, turn, wave, first, wpr, sum);
     const float m0 = sum[0] * a.inv_c;
     float sq[2] = {0.0f, 0.0f};
@@ -253,7 +258,8 @@ struct alignas(4 * P) RunOf {
   float v[P];
 };
 
-template <int XT, int YT, int S, int W, int MAXT>
+// AHEAD: the next row's loads are in flight, where the registers allow it
+template <int XT, int YT, int S, int W, int MAXT, bool AHEAD>
 __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
   __shared__ RowSum sm;
   extern __shared__ __align__(16) float4 fold_lds[];          // [G][2 S W / P][T] runs of P when G > 1
@@ -289,9 +295,10 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
     nmean = a.mean[row];
     nrstd = a.rstd[row];
   };
-  fetch(group);
+  if constexpr (AHEAD) fetch(group);
   for (int r0 = 0; r0 < rows; r0 += a.G) {
     const int r = r0 + group;
+    if constexpr (!AHEAD) fetch(r);
     float h[S][W], g[S][W];
     float sum[2] = {0.0f, 0.0f};
     const float mean = nmean, rstd = nrstd;
@@ -301,7 +308,7 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
       nx[s].floats(h[s]);
       ny[s].floats(g[s]);
     }
-    if (r0 + a.G < rows) fetch(r + a.G);
+    if (AHEAD && r0 + a.G < rows) fetch(r + a.G);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
@@ -368,6 +375,104 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
     const int qq = q < Q ? q : q - Q;
     const Place to = place<W>(qq / (W / P), a.T, t, a.C);
     if (to.own < W) store_row<DET_F32, P>(row_at<DET_F32>(pw, q < Q ? 0 : a.C), to.at + qq % (W / P) * P, v.v);
+  }
+}
+
+// Rows of more than 16384 columns: dw and db of a whole row do not fit the
+// registers, so the columns are taken in parts of T S W.  The chunk's row sums
+// come first (one pass over all parts, kept in LDS), then each part's dx, dw
+// and db: x and dy are read twice, the second time mostly from the caches.
+template <int XT, int YT, int S, int W, int T>
+__global__ __launch_bounds__(T, 4) void k_norm_grad_wide(NormGradArgs a) {
+  __shared__ RowSum sm;
+  __shared__ float row_m[2][DET_NORM_SHARD_ROWS];
+  int turn = 0;
+  const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t chunk = gridDim.x - 1 - blockIdx.x;
+  const int64_t row0 = chunk * a.chunk;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.N - row0));
+  auto spot = [&](int part, int s) {
+    const int at = ((part * S + s) * T + t) * W, from = min(at, a.C - W);
+    return Place{from, min(at - from, W)};
+  };
+  const int nparts = (a.C + T * S * W - 1) / (T * S * W);
+  for (int r = 0; r < rows && a.dx != nullptr; ++r) {
+    const char* const x = row_at<XT>(a.x, (row0 + r) * a.s_x);
+    const char* const dy = row_at<YT>(a.dy, (row0 + r) * a.s_dy);
+    const float mean = a.mean[row0 + r], rstd = a.rstd[row0 + r];
+    float sum[2] = {0.0f, 0.0f};
+    for (int part = 0; part < nparts; ++part) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const Place at = spot(part, s);
+        Raw<XT, W> rx;
+        Raw<YT, W> ry;
+        float h[W], g[W], w[W];
+        rx.load(x, at.at);
+        ry.load(dy, at.at);
+        load_weights<W>(a.w_dt, a.w, at.at, 1.0f, w);
+        rx.floats(h);
+        ry.floats(g);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const float u = j >= at.own ? g[j] * w[j] : 0.0f;
+          sum[0] += u;
+          sum[1] = fmaf(u, (h[j] - mean) * rstd, sum[1]);
+        }
+      }
+    }
+    row_sum(sm, turn, wave, 0, T / 64, sum);
+    if (t == 0) {
+      row_m[0][r] = sum[0] * a.inv_c;
+      row_m[1][r] = sum[1] * a.inv_c;
+    }
+  }
+  __syncthreads();
+  char* const pw = reinterpret_cast<char*>(a.parts + chunk * 2 * a.C);
+  for (int part = 0; part < nparts; ++part) {
+    Place at[S];
+    float w[S][W], dw[S][W], db[S][W];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      at[s] = spot(part, s);
+      load_weights<W>(a.w_dt, a.w, at[s].at, 1.0f, w[s]);
+#pragma unroll
+      for (int j = 0; j < W; ++j) dw[s][j] = db[s][j] = 0.0f;
+    }
+    for (int r = 0; r < rows; ++r) {
+      const char* const x = row_at<XT>(a.x, (row0 + r) * a.s_x);
+      const char* const dy = row_at<YT>(a.dy, (row0 + r) * a.s_dy);
+      const float mean = a.mean[row0 + r], rstd = a.rstd[row0 + r], m1 = row_m[0][r], m2 = row_m[1][r];
+      Raw<XT, W> rx[S];
+      Raw<YT, W> ry[S];
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        rx[s].load(x, at[s].at);
+        ry[s].load(dy, at[s].at);
+      }
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        float h[W], g[W];
+        rx[s].floats(h);
+        ry[s].floats(g);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          h[j] = (h[j] - mean) * rstd;
+          dw[s][j] = fmaf(g[j], h[j], dw[s][j]);
+          db[s][j] += g[j];
+          g[j] = rstd * fmaf(-h[j], m2, g[j] * w[s][j] - m1);
+        }
+        if (a.dx != nullptr && at[s].own < W)
+          store_row<XT, W>(row_at<XT>(a.dx, (row0 + r) * a.C), at[s].at, g);
+      }
+    }
+    if (a.parts == nullptr) continue;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if (at[s].own == W) continue;
+      store_row<DET_F32, W>(pw, at[s].at, dw[s]);
+      store_row<DET_F32, W>(row_at<DET_F32>(pw, a.C), at[s].at, db[s]);
+    }
   }
 }
 
@@ -568,18 +673,30 @@ void launch_norm(NormArgs a, hipStream_t s) {
   a.G = std::max(1, 256 / a.T);
   // enough workgroups for eight to a CU before rows share one (and its weights)
   a.rows = static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, a.N / (2048 * a.G)))) * a.G;
-  hipLaunchKernelGGL((k_norm<XT, YT, S, W, MAXT>), dim3(static_cast<unsigned>(ceil_div(a.N, a.rows))), dim3(a.T, a.G), 0,
-                     s, a);
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.N, a.rows))), block(a.T, a.G);
+  if (a.rstd == nullptr) hipLaunchKernelGGL((k_norm<XT, YT, S, W, MAXT, true, (MAXT <= 512)>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_norm<XT, YT, S, W, MAXT, false, (MAXT <= 512)>), grid, block, 0, s, a);
 }
 
 template <int XT, int YT, int S, int W, int MAXT>
 void launch_norm_grad(NormGradArgs a, hipStream_t s) {
   a.T = threads_of(a.C, S, W);
-  a.G = std::max(1, std::min(8, 512 / a.T));
+  // twice the rows at a time for few long rows: 1021 x 1537 fp32 15.5 -> 13.3 us, but
+  // 32768 x 1024 bf16 52 -> 59
+  a.G = std::max(1, std::min(8, (a.C > 1024 ? 1024 : 512) / a.T));
   a.chunk = chunk_rows(a.C);
   const size_t lds = a.G > 1 && a.parts != nullptr ? static_cast<size_t>(a.G) * a.T * S * W * 2 * sizeof(float) : 0;
-  hipLaunchKernelGGL((k_norm_grad<XT, YT, S, W, MAXT>), dim3(static_cast<unsigned>(ceil_div(a.N, a.chunk))),
+  hipLaunchKernelGGL((k_norm_grad<XT, YT, S, W, MAXT, (S * W <= 8)>), dim3(static_cast<unsigned>(ceil_div(a.N, a.chunk))),
                      dim3(a.T, a.G), lds, s, a);
+}
+
+template <int XT, int YT, int S, int W, int T>
+void launch_norm_grad_wide(NormGradArgs a, hipStream_t s) {
+  a.T = T;
+  a.G = 1;
+  a.chunk = chunk_rows(a.C);
+  hipLaunchKernelGGL((k_norm_grad_wide<XT, YT, S, W, T>), dim3(static_cast<unsigned>(ceil_div(a.N, a.chunk))), dim3(T),
+                     0, s, a);
 }
 
 // Elements a thread holds.  Forward: 8 up to 512 columns, 16 up to 16384 (more
@@ -603,7 +720,7 @@ void backward(const NormGradArgs& a, hipStream_t s) {
   else if (a.C <= 512) launch_norm_grad<XT, YT, 8 / W, W, 512>(a, s);
   else if (a.C <= 8192) launch_norm_grad<XT, YT, 8 / W, W, 1024>(a, s);
   else if (a.C <= 16384) launch_norm_grad<XT, YT, 16 / W, W, 1024>(a, s);
-  else launch_norm_grad<XT, YT, 32 / W, W, 1024>(a, s);
+  else launch_norm_grad_wide<XT, YT, 8 / W, W, 1024>(a, s);
 }
 template <class F>
 void by_types(int x_dt, int y_dt, F f) {

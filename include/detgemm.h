@@ -445,7 +445,7 @@ det_status det_layer_norm(det_dtype x_dt, const void* x, int64_t s_x, det_dtype 
  *   workspace         det_layer_norm_grad_workspace_bytes(N, C), 16-byte
  *                     aligned; null when dw, db and digits all are
  * dw and db are summed in fp32 over chunks of consecutive rows in one fixed
- * order (64 for C <= 512, 16 for C <= 4096, else 32) and the chunks are
+ * order (64 for C <= 512, 32 for 4096 < C <= 8192, else 16) and the chunks are
  * added exactly in the long accumulator and rounded once.  So the digits of
  * row shards cut at multiples of DET_NORM_SHARD_ROWS add up (det_combine) to the digits
  * of all rows, and det_finalize of the sum gives the same bits as one call
