@@ -15,7 +15,7 @@ from .linear import DetLinear  # noqa: F401
 from .head import (TokenLogProbs, distill_backward, distill_forward, distill_loss, token_logprobs,  # noqa: F401
                    token_logprobs_backward, token_logprobs_forward)
 from .loss import exact_mean, exact_mse_loss  # noqa: F401
-from .norm import (DetLayerNorm, layer_norm, layer_norm_backward, layer_norm_digits,  # noqa: F401
+from .norm import (NORM_SHARD_ROWS, DetLayerNorm, layer_norm, layer_norm_backward, layer_norm_digits,  # noqa: F401
                    layer_norm_forward)
 
 __all__ = ["det_gemm", "det_gemm_noalloc", "det_gemm_partial", "det_combine", "det_finalize", "DetLinear",
@@ -23,7 +23,7 @@ __all__ = ["det_gemm", "det_gemm_noalloc", "det_gemm_partial", "det_combine", "d
            "device_status",
            "gemm_any_k", "exact_dot", "exact_dot_digits", "exact_sqdiff_digits", "exact_sum_squares",
            "exact_mse_loss", "exact_mean",
-           "layer_norm", "layer_norm_forward", "layer_norm_backward", "layer_norm_digits", "DetLayerNorm",
+           "layer_norm", "layer_norm_forward", "layer_norm_backward", "layer_norm_digits", "DetLayerNorm", "NORM_SHARD_ROWS",
            "token_logprobs", "token_logprobs_forward", "token_logprobs_backward", "TokenLogProbs",
            "distill_loss", "distill_forward", "distill_backward",
            "NUM_DIGITS", "LSB_EXPONENT", "K_MAX", "DetGemmError"]

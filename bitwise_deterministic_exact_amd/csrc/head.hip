@@ -734,17 +734,25 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
 
 // ---------------------------------------------------------------- host side
 
-// Workgroups per row: one when the rows alone give every CU about three (then
-// the row is finished in the same launch), else enough for four, or as many as
-// the row has groups of four chunks, and with alternatives at most 16 (64
-// lists to join).
+// Workgroups per row.  One, which also finishes the row, when the rows alone
+// give every CU about three workgroups, or when the row is so short that its
+// four waves are through before a second launch would be (that costs 3 to 4
+// us): 1 x 32000 fp32 7.5 us in one workgroup, 10.1 in four and a join; 1 x
+// 50257 10.1 and 9.8; 500 x 50257 20.1 and 23.5; with alternatives 1 x 32000
+// 15.0 and 14.4.  Otherwise enough for four to a CU, at most one for every
+// four chunks, and with alternatives at most 16 (64 lists to join).
 constexpr int SHARED_MAX = 16;
 int blocks_per_row(int64_t N, int64_t nchunk, int top) {
+  const int64_t turns = ceil_div(nchunk, WAVES);              // chunks a wave of one workgroup takes
   int64_t b = 1;
-  if (N < 768) b = std::min(ceil_div(nchunk, WAVES), ceil_div(1024, N > 0 ? N : 1));
+  if (N < 768 && turns > (N >= 384 ? 8 : top > 0 ? 2 : 4)) b = std::min(turns, ceil_div(1024, N > 0 ? N : 1));
   if (top > 0) b = std::min<int64_t>(b, SHARED_MAX);
   if (nchunk > LDS_PARTS && b == 1) b = 2;                    // the sums go through the workspace
   return static_cast<int>(b);
+}
+// of the gradient, which has nothing to join
+int grad_blocks_per_row(int64_t N, int64_t nchunk) {
+  return static_cast<int>(N < 768 ? std::min(ceil_div(nchunk, WAVES), ceil_div(1024, N > 0 ? N : 1)) : 1);
 }
 
 int64_t score_ws_bytes(int64_t N, int64_t V, int top) {
@@ -803,7 +811,7 @@ det_status launch_score(ScoreArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
 
 det_status launch_grad(GradArgs a, hipStream_t s) {
   a.nchunk = static_cast<int>(ceil_div(a.V, CHUNK));
-  a.nblk = blocks_per_row(a.N, a.nchunk, 0);
+  a.nblk = grad_blocks_per_row(a.N, a.nchunk);
   const int n = a.mode == MODE_DISTILL ? a.K : 1 + a.top;
   const dim3 grid(static_cast<unsigned>(a.N * a.nblk)), block(64 * WAVES);
   const size_t lds = static_cast<size_t>(n) * 8;
