@@ -505,6 +505,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
     const void* const zr = static_cast<const char*>(a.z) + row * a.s_row * Elem<DT>::BYTES;
     TopList<DT> tl{mine, zr, a.V, a.top, 0, 0};
     const int step = a.nblk * a.wpr;
+    bool masked = false;
     int waiting = 0;                     // chunks whose lane maxima wait for `take`
     float largest = -INFINITY;
     for (int ch = part * a.wpr + rw; ch < a.nchunk; ch += step) {
@@ -517,20 +518,28 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
       for (int j = 0; j < LANE_ELEMS; ++j) lane_max = fmaxf(lane_max, v[j]);
       const float m = wave_max(lane_max);
       const float ref = m == -INFINITY ? 0.0f : m;
+      // e d is 0 -inf for a masked logit.  The bound on d that gives 0 there
+      // instead changes no other bit (e is 0 long before d passes it), so it is
+      // left out until a chunk needs it, and taken from then on.
       float s = 0.0f, u = 0.0f;
-#pragma unroll
-      for (int j = 0; j < LANE_ELEMS; ++j) {
-        const float d = (v[j] - ref) * a.c;
-        const float e = __builtin_amdgcn_exp2f(d);
-        s += e;
-        u = fmaf(e, d, u);
-      }
-      if (u != u && s == s) {            // 0 * -inf: masked logits add nothing
-        u = 0.0f;
+      if (!masked) {
 #pragma unroll
         for (int j = 0; j < LANE_ELEMS; ++j) {
           const float d = (v[j] - ref) * a.c;
-          u = fmaf(__builtin_amdgcn_exp2f(d), fmaxf(d, -2000.0f), u);
+          const float e = __builtin_amdgcn_exp2f(d);
+          s += e;
+          u = fmaf(e, d, u);
+        }
+        masked = __ballot(u != u && s == s) != 0;
+      }
+      if (masked) {                      // uniform
+        s = u = 0.0f;
+#pragma unroll
+        for (int j = 0; j < LANE_ELEMS; ++j) {
+          const float d = (v[j] - ref) * a.c;
+          const float e = __builtin_amdgcn_exp2f(d);
+          s += e;
+          u = fmaf(e, fmaxf(d, -2000.0f), u);
         }
       }
       s = wave_sum(s);
