@@ -18,6 +18,7 @@
 // cut by V alone, so a row's bits are a function of that row: not of the
 // batch, of how many workgroups share a row, or of the alignment.
 #include <algorithm>
+#include <type_traits>
 
 #include "rowops.h"
 
@@ -82,12 +83,6 @@ __device__ __forceinline__ float order_value(uint32_t o) {
 __device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) {
   return (static_cast<uint64_t>(order) << 32) | (0xFFFFFFFFu - index);
 }
-__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
-  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v)), lane);
-  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v >> 32)), lane);
-  return (static_cast<uint64_t>(hi) << 32) | lo;
-}
-
 // The largest `want` of the n keys in LDS at pool[0..n), sorted, into out (not
 // overlapping the pool), by `lanes` threads numbered `t` (all of a wave, or of
 // a workgroup): each key's rank is the number of larger keys, read two to an
@@ -118,14 +113,18 @@ __device__ __forceinline__ int lanes_below(uint64_t b) {
   return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), 0));
 }
 
-// the key of rank r (0 = largest) among the lanes' distinct nonzero keys, or
-// 0 when there are not that many
-__device__ __forceinline__ uint64_t lane_key_of_rank(uint64_t mine, int r) {
-  if (__popcll(__ballot(mine != 0)) <= r) return 0;
-  int rank = 0;
-#pragma unroll 8
-  for (int l = 0; l < 64; ++l) rank += lane_u64(mine, l) > mine ? 1 : 0;
-  return lane_u64(mine, __builtin_ctzll(__ballot(mine != 0 && rank == r)));
+// A bar that `want` of the lanes' keys reach (more only if keys are equal):
+// the largest such one is sought bit by bit, but any that exactly `want` reach
+// will do.  0 when fewer keys than that are not 0.
+__device__ __forceinline__ uint64_t bar_of_lanes(uint64_t mine, int want) {
+  uint64_t t = 0;
+#pragma unroll 1
+  for (uint64_t bit = 1ull << 63; bit != 0; bit >>= 1) {
+    const int reach = __popcll(__ballot(mine >= (t | bit)));
+    if (reach >= want) t |= bit;
+    if (reach == want) break;
+  }
+  return t;
 }
 
 // ---------------------------------------------------------------- one chunk
@@ -181,21 +180,23 @@ __device__ __forceinline__ void load_chunk(const void* row, int64_t base, int64_
 // Candidates collect in a pool, which is ranked down to `top` keys (and the
 // bar raised) whenever 64 more might not fit, so ties, masks and rows built
 // against it cost time but no correctness.
-//   1024 x 131072 bf16, top 20: 108 us with the logits of a chunk kept in
-//   registers for its candidates (123 registers, a ranking per chunk).
-constexpr int STEP_CHUNKS = 8, POOL = 256;
-
+//   1024 x 131072 bf16, top 20: 75 us (50 without alternatives); 108 with the
+//   logits of a chunk kept in registers for its candidates (123 registers, a
+//   ranking per chunk).
+template <int NW>                         // waves per workgroup: 16 of them share the LDS more sparingly
 struct TopLds {
+  static constexpr int STEP_CHUNKS = NW == WAVES ? 8 : 4, POOL = NW == WAVES ? 256 : 128;
   uint64_t pool[POOL];
-  uint64_t list[TOP_MAX];
   float lane_max[STEP_CHUNKS * 64];
   uint16_t pairs[STEP_CHUNKS * 64];
 };
 
-template <int DT>
+template <int DT, int NW>
 struct TopList {
   static constexpr int VE = Elem<DT>::VE, NV = LANE_ELEMS / VE;
-  TopLds& m;
+  static constexpr int STEP_CHUNKS = TopLds<NW>::STEP_CHUNKS, POOL = TopLds<NW>::POOL;
+  TopLds<NW>& m;
+  uint64_t* list;                        // the result: sorted
   const void* row;
   int64_t V;
   int top, n;                            // n keys in the pool
@@ -235,12 +236,38 @@ struct TopList {
       wave_sync();
       return;
     }
-    rank_keys(m.pool, n, m.list, top, lane, 64);
+    rank_keys(m.pool, n, list, top, lane, 64);
     wave_sync();
     n = min(n, top);
-    if (lane < n) m.pool[lane] = m.list[lane];
+    if (lane < n) m.pool[lane] = list[lane];
     wave_sync();
-    if (n == top) bar = max(bar, m.list[top - 1]);
+    if (n == top) bar = max(bar, list[top - 1]);
+  }
+
+  // the top-th largest of the pairs' maxima, bit by bit from the top; any value
+  // that exactly `top` of them reach will do.  Of masked or constant logits
+  // all are equal to the largest.
+  template <int M>
+  __device__ __forceinline__ uint32_t value_bar(int64_t first, int64_t step, int count, uint32_t most, int lane) const {
+    uint32_t o[M], t = 0;
+    int ties = 0;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      o[i] = 0;
+      if (i < count && (first + i * step) * CHUNK + lane * VE < V) o[i] = order_bits(m.lane_max[i * 64 + lane]);
+      ties += __popcll(__ballot(o[i] == most));
+    }
+    if (ties >= top) return most;
+#pragma unroll 1
+    for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+      if ((t | bit) > most) continue;
+      int reach = 0;
+#pragma unroll
+      for (int i = 0; i < M; ++i) reach += __popcll(__ballot(o[i] >= (t | bit)));
+      if (reach >= top) t |= bit;
+      if (reach == top) break;
+    }
+    return t;
   }
 
   // chunks first, first + step, ..: `count` of them, their lane maxima in m.lane_max
@@ -248,29 +275,9 @@ struct TopList {
   __device__ __forceinline__ void take(int64_t first, int64_t step, int count, float largest, int lane) {
     wave_sync();
     if (n < top) {
-      // the top-th largest of the pairs' maxima, bit by bit from the top; any
-      // value that exactly `top` of them reach will do
-      uint32_t o[STEP_CHUNKS], t = 0;
-#pragma unroll
-      for (int i = 0; i < STEP_CHUNKS; ++i) {
-        o[i] = 0;
-        if (i < count && (first + i * step) * CHUNK + lane * VE < V) o[i] = order_bits(m.lane_max[i * 64 + lane]);
-      }
-      const uint32_t most = order_bits(largest);              // of masked or constant logits, all of them
-      int ties = 0;
-#pragma unroll
-      for (int i = 0; i < STEP_CHUNKS; ++i)
-        if (i < count) ties += __popcll(__ballot(o[i] == most));
-      if (ties >= top) t = most;
-#pragma unroll 1
-      for (uint32_t bit = ties >= top ? 0u : 0x80000000u; bit != 0; bit >>= 1) {
-        int reach = 0;
-#pragma unroll
-        for (int i = 0; i < STEP_CHUNKS; ++i)
-          if (i < count) reach += __popcll(__ballot(o[i] >= (t | bit)));
-        if (reach >= top) t |= bit;
-        if (reach == top) break;
-      }
+      const uint32_t most = order_bits(largest);
+      const uint32_t t = count == 1 ? value_bar<1>(first, step, count, most, lane)
+                                    : value_bar<STEP_CHUNKS>(first, step, count, most, lane);
       bar = max(bar, static_cast<uint64_t>(t) << 32);         // below every logit of that value
     }
     int pairs = 0;
@@ -302,22 +309,37 @@ struct TopList {
             if (j < V) v[j] = load_elem<DT>(row, j);
         }
       }
-#pragma unroll 1
-      for (int j = 0; j < VE; ++j) {
-        const float x = v[0];
+      // NaN is no candidate: its row's results are NaN
+      uint64_t key[VE];
+      int more = 0;
 #pragma unroll
-        for (int i = 0; i + 1 < VE; ++i) v[i] = v[i + 1];
-        // NaN is no candidate: its row's results are NaN
-        const uint64_t key = on && from + j >= at && from + j < V && x == x
-                                 ? key_of(order_bits(x), static_cast<uint32_t>(from + j)) : 0;
-        uint64_t b = __ballot(key > bar);
+      for (int j = 0; j < VE; ++j) {
+        key[j] = on && from + j >= at && from + j < V && v[j] == v[j]
+                     ? key_of(order_bits(v[j]), static_cast<uint32_t>(from + j)) : 0;
+        more += __popcll(__ballot(key[j] > bar));
+      }
+      if (n + more <= POOL) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const uint64_t b = __ballot(key[j] > bar);
+          if (key[j] > bar) m.pool[n + lanes_below(b)] = key[j];
+          n += __popcll(b);
+        }
+        continue;
+      }
+#pragma unroll 1
+      for (int j = 0; j < VE; ++j) {     // 64 at a time, with a smaller pool before each
+        const uint64_t k = key[0];
+#pragma unroll
+        for (int i = 0; i + 1 < VE; ++i) key[i] = key[i + 1];
+        uint64_t b = __ballot(k > bar);
         if (b == 0) continue;
         if (n + 64 > POOL) {
           prune(lane);
-          b = __ballot(key > bar);
+          b = __ballot(k > bar);
           if (b == 0) continue;
         }
-        if (key > bar) m.pool[n + lanes_below(b)] = key;
+        if (k > bar) m.pool[n + lanes_below(b)] = k;
         n += __popcll(b);
       }
     }
@@ -477,33 +499,73 @@ __device__ __forceinline__ void finish_distill(const ScoreArgs& a, const RowSums
   }
 }
 
+// The largest `top` keys of `lists` (up to 64) sorted lists of `top` keys, 0 at
+// their ends, by a whole workgroup of `threads`; sorted, in LDS from `room` on
+// (TOP_MAX + lists * top + 16 keys).  Only those keys can be among them that
+// reach a bar: for any j, the ceil(top / j)-th largest of the lists' j-th keys,
+// which at least `top` keys reach.  With j = ceil(2 top / lists), on unordered
+// rows, about twice `top` keys reach it and are ranked.
+template <class F>
+__device__ __forceinline__ uint64_t* top_of_lists(F key, int lists, int top, uint64_t* room, int threads) {
+  __shared__ int count;
+  __shared__ uint64_t bar;
+  uint64_t* const best = room;
+  uint64_t* const pool = room + TOP_MAX;
+  if (threadIdx.x < 64) {
+    const int l = threadIdx.x;
+    const bool some = l < lists && key(l, 0) != 0;
+    const int held = max(__popcll(__ballot(some)), 1);        // lists with a key (none: a row of NaN)
+    const int j = min((2 * top + held - 1) / held, top);
+    uint64_t b = bar_of_lanes(some ? key(l, j - 1) : 0, (top + j - 1) / j);
+    if (b == 0) b = bar_of_lanes(some ? key(l, top - 1) : 0, 1);          // short lists
+    if (l == 0) {
+      bar = b > 0 ? b : 1;
+      count = 0;
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < lists * top; e += threads) {
+    const uint64_t k = key(e / top, e % top);
+    if (k >= bar) pool[atomicAdd(&count, 1)] = k;
+  }
+  __syncthreads();
+  rank_keys(pool, count, best, top, threadIdx.x, threads);
+  __syncthreads();
+  return best;
+}
+
 // ---------------------------------------------------------------- the pass
 //
 // Wave w of a row (of nblk * wpr) takes chunks w, w + nblk * wpr, ...  With
-// one workgroup per row (nblk = 1) its first wave also finishes the row; rows
-// of at most one or two chunks share a workgroup (wpr = 1, 2).
-template <int DT, bool TOP>
-__global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
+// one workgroup per row (nblk = 1) one of its waves also finishes the row; rows
+// of at most one or two chunks share a workgroup (wpr = 1, 2).  4096 x 131072
+// bf16 take 165 us: 6.5 TB/s, more than a copy moves.  8.8 vector instructions
+// per logit, of which the exponential is four times as long as the others.
+template <int DT, bool TOP, int NW>
+__global__ __launch_bounds__(64 * NW) void k_score(ScoreArgs a) {
   extern __shared__ __align__(16) uint64_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rpb = WAVES / a.wpr;                              // rows per workgroup
+  const int rpb = NW / a.wpr;                                 // rows per workgroup
   const int64_t blk = blockIdx.x;
   const int64_t row = a.nblk > 1 ? blk / a.nblk : blk * rpb + wave / a.wpr;
   const int part = a.nblk > 1 ? static_cast<int>(blk % a.nblk) : 0;
   const int rw = wave % a.wpr;                                // this wave within the row and workgroup
   const bool live = row < a.N;
   const bool whole = a.nblk == 1;
-  // LDS: the waves' lists, then the rows' chunk sums
-  TopLds* const tops = reinterpret_cast<TopLds*>(lds);
-  float* const lparts = reinterpret_cast<float*>(tops + (TOP ? WAVES : 0));
+  // LDS: the waves' room for their candidates and their lists, then the rows' chunk sums
+  using Top = TopLds<NW>;
+  Top* const tops = reinterpret_cast<Top*>(lds);
+  uint64_t* const lists = reinterpret_cast<uint64_t*>(tops + (TOP ? NW : 0));
+  float* const lparts = reinterpret_cast<float*>(lists + (TOP ? NW * TOP_MAX : 0));
   float* const parts = whole ? lparts + (wave / a.wpr) * a.nchunk * 3 : a.parts + row * a.nchunk * 3;
-  TopLds& mine = tops[wave];             // not touched without TOP
+  Top& mine = tops[wave];                // these two are not touched without TOP
+  uint64_t* const list = lists + wave * TOP_MAX;
 
   Ahead ahead{};
   if (live) {
-    if (whole && rw == 0) ahead = read_ahead(a, row, lane);
+    if (whole && rw == (NW > WAVES ? NW - 1 : 0)) ahead = read_ahead(a, row, lane);   // the wave that finishes
     const void* const zr = static_cast<const char*>(a.z) + row * a.s_row * Elem<DT>::BYTES;
-    TopList<DT> tl{mine, zr, a.V, a.top, 0, 0};
+    TopList<DT, NW> tl{mine, list, zr, a.V, a.top, 0, 0};
     const int step = a.nblk * a.wpr;
     bool masked = false;
     int waiting = 0;                     // chunks whose lane maxima wait for `take`
@@ -553,7 +615,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
         mine.lane_max[waiting * 64 + lane] = lane_max;
         ++waiting;
         largest = fmaxf(largest, m);
-        if (waiting == STEP_CHUNKS || ch + step >= a.nchunk) {
+        if (waiting == Top::STEP_CHUNKS || ch + step >= a.nchunk) {
           tl.take(ch - static_cast<int64_t>(waiting - 1) * step, step, waiting, largest, lane);
           waiting = 0;
           largest = -INFINITY;
@@ -561,47 +623,58 @@ __global__ __launch_bounds__(64 * WAVES) void k_score(ScoreArgs a) {
       }
     }
     if constexpr (TOP) {
-      if (lane >= tl.n && lane < a.top) mine.list[lane] = 0;  // a wave with few elements
+      if (lane >= tl.n && lane < a.top) list[lane] = 0;       // a wave with few elements
       wave_sync();
     }
   }
   if (whole) __syncthreads();            // uniform: the other waves' sums and lists
-  if (!live) return;
-  if (!whole) {                          // k_score_join does the rest
-    if (TOP && lane < a.top) a.lists[((row * a.nblk + part) * WAVES + wave) * a.top + lane] = mine.list[lane];
+  if constexpr (NW > WAVES) {            // one row, all waves here
+    __shared__ RowSums sums;
+    if (wave == NW - 1) {
+      const RowSums r = join(a, parts, row, lane);
+      if (lane == 0) sums = r;
+      if (a.mode == MODE_DISTILL) finish_distill(a, r, row, lane, ahead);
+      else finish_score(a, r, row, lane, ahead);
+    }
+    if constexpr (TOP) {
+      // the waves' candidates are done with: their room holds the lists' keys
+      uint64_t* const best = top_of_lists([&](int l, int j) { return lists[l * TOP_MAX + j]; }, NW, a.top, lds, 64 * NW);
+      if (wave == 0) write_top(a, sums, row, best, lane);
+    }
     return;
+  } else {
+    if (!live) return;
+    if (!whole) {                        // k_score_join does the rest
+      if (TOP && lane < a.top) a.lists[((row * a.nblk + part) * WAVES + wave) * a.top + lane] = list[lane];
+      return;
+    }
+    if (rw != 0) return;
+    const uint64_t* top = list;
+    if (TOP && a.wpr > 1) {
+      // the row's wave lists, gathered into this wave's pool, joined into the next one's
+      for (int w = 0; w < a.wpr; ++w)
+        if (lane < a.top) mine.pool[w * a.top + lane] = list[w * TOP_MAX + lane];
+      uint64_t* const joined = tops[wave + 1].pool;
+      if (lane < a.top) joined[lane] = 0;  // a row with a NaN may hold fewer than `top` keys
+      wave_sync();
+      rank_keys(mine.pool, a.wpr * a.top, joined, a.top, lane, 64);
+      wave_sync();
+      top = joined;
+    }
+    const RowSums r = join(a, parts, row, lane);
+    if (a.mode == MODE_DISTILL) finish_distill(a, r, row, lane, ahead);
+    else finish_score(a, r, row, lane, ahead);
+    if constexpr (TOP) write_top(a, r, row, top, lane);
   }
-  if (rw != 0) return;
-  const uint64_t* list = mine.list;
-  if (TOP && a.wpr > 1) {
-    // the row's wave lists, gathered into this wave's pool, joined into the next one's
-    for (int w = 0; w < a.wpr; ++w)
-      if (lane < a.top) mine.pool[w * a.top + lane] = tops[wave + w].list[lane];
-    uint64_t* const joined = tops[wave + 1].pool;
-    if (lane < a.top) joined[lane] = 0;  // a row with a NaN may hold fewer than `top` keys
-    wave_sync();
-    rank_keys(mine.pool, a.wpr * a.top, joined, a.top, lane, 64);
-    wave_sync();
-    list = joined;
-  }
-  const RowSums r = join(a, parts, row, lane);
-  if (a.mode == MODE_DISTILL) finish_distill(a, r, row, lane, ahead);
-  else finish_score(a, r, row, lane, ahead);
-  if constexpr (TOP) write_top(a, r, row, list, lane);
 }
 
-// The end of rows that several workgroups shared: one workgroup per row.  Of
-// the lists' keys only those can be among the top that reach a bar: for any j,
-// the ceil(top / j)-th largest of the lists' j-th keys, which at least `top`
-// keys reach.  With j = ceil(2 top / n) of n lists, on unordered rows, about
-// twice `top` keys reach it and are ranked.
+// The end of rows that several workgroups shared: one workgroup per row, its
+// last wave for everything but the alternatives.
 __global__ __launch_bounds__(256) void k_score_join(ScoreArgs a) {
   extern __shared__ __align__(16) uint64_t lds[];
-  __shared__ int count;
-  __shared__ uint64_t bar;
   __shared__ RowSums sums;
   const int64_t row = blockIdx.x;
-  if (threadIdx.x >= 192) {               // the last wave: everything but the alternatives
+  if (threadIdx.x >= 192) {
     const int l = threadIdx.x - 192;
     const Ahead ahead = read_ahead(a, row, l);
     const RowSums r = join(a, a.parts + row * a.nchunk * 3, row, l);
@@ -610,31 +683,10 @@ __global__ __launch_bounds__(256) void k_score_join(ScoreArgs a) {
     else finish_score(a, r, row, l, ahead);
   }
   if (a.top == 0) return;                 // uniform
-  const int lane = threadIdx.x & 63;
-  const int lists = a.nblk * WAVES, n = lists * a.top;
-  uint64_t* const best = lds;                                 // [top]
-  uint64_t* const pool = lds + TOP_MAX;                       // [n + 16]: the keys that reach the bar
-  const uint64_t* const src = a.lists + row * n;
-  if (threadIdx.x < 64) {
-    const bool some = lane < lists && src[lane * a.top] != 0;
-    const int held = max(__popcll(__ballot(some)), 1);      // lists with a key (none: a row of NaN)
-    const int j = min((2 * a.top + held - 1) / held, a.top);
-    uint64_t b = lane_key_of_rank(some ? src[lane * a.top + j - 1] : 0, (a.top + j - 1) / j - 1);
-    if (b == 0) b = lane_key_of_rank(some ? src[lane * a.top + a.top - 1] : 0, 0);   // short lists
-    if (lane == 0) {
-      bar = b > 0 ? b : 1;
-      count = 0;
-    }
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < n; e += 256) {
-    const uint64_t key = src[e];
-    if (key >= bar) pool[atomicAdd(&count, 1)] = key;
-  }
-  __syncthreads();
-  rank_keys(pool, count, best, a.top, threadIdx.x, 256);
-  __syncthreads();
-  if (threadIdx.x < 64) write_top(a, sums, row, best, lane);
+  const int lists = a.nblk * WAVES;
+  const uint64_t* const src = a.lists + row * lists * a.top;
+  uint64_t* const best = top_of_lists([&](int l, int j) { return src[l * a.top + j]; }, lists, a.top, lds, 256);
+  if (threadIdx.x < 64) write_top(a, sums, row, best, threadIdx.x);
 }
 
 // ---------------------------------------------------------------- gradients
@@ -796,13 +848,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
 
 // ---------------------------------------------------------------- host side
 
-// Workgroups per row.  One, which also finishes the row, when the rows alone
-// give every CU about three workgroups, or when the row is so short that its
-// four waves are through before a second launch would be (that costs 3 to 4
-// us): 1 x 32000 fp32 7.5 us in one workgroup, 10.1 in four and a join; 1 x
-// 50257 10.1 and 9.8; 500 x 50257 20.1 and 23.5; with alternatives 1 x 32000
-// 15.0 and 14.4.  Otherwise enough for four to a CU, at most one for every
-// four chunks, and with alternatives at most 16 (64 lists to join).
+// Four-wave workgroups per row.  One, which also finishes the row, when the
+// rows alone give every CU about three workgroups, or when the row is so short
+// that its four waves are through before a second launch would be (that costs
+// 3 to 4 us): 500 x 50257 fp32 20.1 us in one workgroup, 23.5 in two and a
+// join; 500 x 131072 48 in two.  Otherwise enough for four to a CU, at most
+// one for every four chunks, and with alternatives at most 16 (64 lists to join).
 constexpr int SHARED_MAX = 16;
 int blocks_per_row(int64_t N, int64_t nchunk, int top) {
   const int64_t turns = ceil_div(nchunk, WAVES);              // chunks a wave of one workgroup takes
@@ -817,8 +868,21 @@ int grad_blocks_per_row(int64_t N, int64_t nchunk) {
   return static_cast<int>(N < 768 ? std::min(ceil_div(nchunk, WAVES), ceil_div(1024, N > 0 ? N : 1)) : 1);
 }
 
+// One workgroup of 16 waves to a row instead, in one launch, for rows of more
+// than four chunks that they pass in at most two turns: 1 x 32000 fp32 6.5 us
+// (one workgroup of four waves 7.3), 1 x 50257 7.9 (four-wave workgroups and a
+// join 10.3).  With alternatives, whose search keeps a CU's four SIMDs busy, in
+// one turn (64 x 16000 bf16 top 10 12.5 us against 15.1, but 64 x 50257 16.5
+// against 15.4).  From 128 rows on, in up to eight turns: the other CUs have
+// rows of their own (200 x 131072 fp32 20.0 against 22.2).
+constexpr int MANY = 16;
+bool many_waves(int64_t N, int64_t nchunk, int top) {
+  return N <= 256 && nchunk > WAVES && nchunk <= (N >= 128 ? 8 * MANY : top > 0 ? MANY : 2 * MANY);
+}
+
 int64_t score_ws_bytes(int64_t N, int64_t V, int top) {
   const int64_t nchunk = ceil_div(V, CHUNK);
+  if (many_waves(N, nchunk, top)) return 0;
   const int nblk = blocks_per_row(N, nchunk, top);
   if (nblk == 1) return 0;
   return N * (nblk * WAVES * static_cast<int64_t>(top) * 8 + nchunk * 12);
@@ -839,8 +903,9 @@ det_status check_logits(int dt, const void* z, int64_t N, int64_t V, int64_t s_r
 
 det_status launch_score(ScoreArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
   a.nchunk = static_cast<int>(ceil_div(a.V, CHUNK));
-  a.nblk = blocks_per_row(a.N, a.nchunk, a.top);
-  a.wpr = a.nchunk >= WAVES ? WAVES : a.nchunk;
+  const bool many = many_waves(a.N, a.nchunk, a.top);
+  a.nblk = many ? 1 : blocks_per_row(a.N, a.nchunk, a.top);
+  a.wpr = many ? MANY : a.nchunk >= WAVES ? WAVES : a.nchunk;
   if (a.wpr == 3) a.wpr = 4;
   a.status = det_device_status_word();
   if (a.status == nullptr) return DET_EHIP;
@@ -852,18 +917,23 @@ det_status launch_score(ScoreArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
     a.lists = static_cast<uint64_t*>(ws);
     a.parts = reinterpret_cast<float*>(a.lists + a.N * a.nblk * WAVES * a.top);
   }
-  const int rpb = WAVES / a.wpr;
+  const int nw = many ? MANY : WAVES, rpb = nw / a.wpr;
   const int64_t blocks = a.nblk > 1 ? a.N * a.nblk : ceil_div(a.N, rpb);
-  const size_t lds = (a.top > 0 ? WAVES * sizeof(TopLds) : 0) +
+  const size_t lds = (a.top > 0 ? nw * ((many ? sizeof(TopLds<MANY>) : sizeof(TopLds<WAVES>)) + TOP_MAX * 8) : 0) +
                      (a.nblk > 1 ? 0 : static_cast<size_t>(rpb) * a.nchunk * 12);
-  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * WAVES);
-  if (a.dt == DET_F32) {
-    if (a.top > 0) hipLaunchKernelGGL((k_score<DET_F32, true>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((k_score<DET_F32, false>), grid, block, lds, s, a);
-  } else {
-    if (a.top > 0) hipLaunchKernelGGL((k_score<DET_BF16, true>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((k_score<DET_BF16, false>), grid, block, lds, s, a);
-  }
+  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * nw);
+  auto launch = [&](auto dt, auto top) {
+    constexpr int DT = decltype(dt)::value;
+    constexpr bool TOP = decltype(top)::value;
+    if (many) hipLaunchKernelGGL((k_score<DT, TOP, MANY>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_score<DT, TOP, WAVES>), grid, block, lds, s, a);
+  };
+  auto by_top = [&](auto dt) {
+    if (a.top > 0) launch(dt, std::true_type{});
+    else launch(dt, std::false_type{});
+  };
+  if (a.dt == DET_F32) by_top(std::integral_constant<int, DET_F32>{});
+  else by_top(std::integral_constant<int, DET_BF16>{});
   det_status st = hip_check(hipGetLastError(), "score launch");
   if (st != DET_OK || a.nblk == 1) return st;
   const size_t jl = a.top > 0 ? (TOP_MAX + static_cast<size_t>(a.nblk) * WAVES * a.top + 16) * 8 : 0;
