@@ -14,7 +14,7 @@
 // Everything is one pass over the logits: a wave takes a chunk of 2048
 // consecutive logits into registers, finds its maximum m, and forms
 // S = sum 2^(c (z - m)) and U = sum c (z - m) 2^(c (z - m)), c = s log2 e.
-// The chunks' (m, S, U) are joined in 64 bits in chunk order.  The chunks are
+// The chunks' (m, S, U) are joined in 64 bits in a fixed order.  The chunks are
 // cut by V alone, so a row's bits are a function of that row: not of the
 // batch, of how many workgroups share a row, or of the alignment.
 #include <algorithm>
@@ -83,6 +83,7 @@ __device__ __forceinline__ float order_value(uint32_t o) {
 __device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) {
   return (static_cast<uint64_t>(order) << 32) | (0xFFFFFFFFu - index);
 }
+
 // The largest `want` of the n keys in LDS at pool[0..n), sorted, into out (not
 // overlapping the pool), by `lanes` threads numbered `t` (all of a wave, or of
 // a workgroup): each key's rank is the number of larger keys, read two to an
@@ -284,8 +285,7 @@ struct TopList {
     for (int i = 0; i < count; ++i) {
       const bool hit = best_key(i, lane, first + i * step) > bar;
       const uint64_t b = __ballot(hit);
-      if (hit)
-        m.pairs[pairs + lanes_below(b)] = static_cast<uint16_t>(i * 64 + lane);
+      if (hit) m.pairs[pairs + lanes_below(b)] = static_cast<uint16_t>(i * 64 + lane);
       pairs += __popcll(b);
     }
     wave_sync();
@@ -539,8 +539,9 @@ __device__ __forceinline__ uint64_t* top_of_lists(F key, int lists, int top, uin
 // Wave w of a row (of nblk * wpr) takes chunks w, w + nblk * wpr, ...  With
 // one workgroup per row (nblk = 1) one of its waves also finishes the row; rows
 // of at most one or two chunks share a workgroup (wpr = 1, 2).  4096 x 131072
-// bf16 take 165 us: 6.5 TB/s, more than a copy moves.  8.8 vector instructions
-// per logit, of which the exponential is four times as long as the others.
+// bf16 take 167 us: 6.4 TB/s, more than a copy's reads and writes together.
+// 8.8 vector instructions per logit, the exponential twice as long as the
+// others, are 0.8 of the issue slots in that time.
 template <int DT, bool TOP, int NW>
 __global__ __launch_bounds__(64 * NW) void k_score(ScoreArgs a) {
   extern __shared__ __align__(16) uint64_t lds[];

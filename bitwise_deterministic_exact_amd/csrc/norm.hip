@@ -37,8 +37,8 @@ using namespace rowops;
 // they are left out of the sums and written a second time, with the same value
 // (each operation below is spelled out, so every copy of it rounds alike).
 // With the tail's loads element by element under a branch the loads of a
-// ragged wave waited for each other (8000 x 5000 bf16 forward 52 us, 42 this
-// way; backward 97 and 61); with the tail's stores element by element the
+// ragged wave waited for each other (8000 x 5000 bf16 forward 52 us, 36 this
+// way; backward 97 and 58); with the tail's stores element by element the
 // backward took 120 us.
 
 // Rows whose dw and db are added in fp32: each divides DET_NORM_SHARD_ROWS.
@@ -53,10 +53,6 @@ template <int DT, int W>
 struct Raw {
   static constexpr int U = (W * Elem<DT>::BYTES + 3) / 4;
   uint32_t u[U];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < U; ++i) u[i] = 0u;
-  }
   // from element `at` of the row at p (a scalar address, a 32-bit offset)
   template <bool NT = false>
   __device__ __forceinline__ void load(const char* p, int at) {
@@ -127,25 +123,27 @@ __device__ __forceinline__ Place place(int s, int T, int t, int C) {
   return {from, min(at - from, W)};
 }
 
-// The sum of two values over a row's waves (wpr of them from wave `first`).
+// The sum of one or two values over a row's waves (wpr of them from wave `first`).
 // One barrier: the buffers alternate, so one is rewritten only after every
 // thread has passed the barrier that follows its last reads.
 struct RowSum {
   float buf[2][16][2];
 };
-__device__ __forceinline__ void row_sum(RowSum& m, int& turn, int wave, int first, int wpr, float (&v)[2]) {
-  v[0] = wave_sum(v[0]);
-  v[1] = wave_sum(v[1]);
+template <int NV>
+__device__ __forceinline__ void row_sum(RowSum& m, int& turn, int wave, int first, int wpr, float (&v)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
   if (wpr == 1) return;                                       // uniform
   if ((threadIdx.x & 63) == 0) {
-    m.buf[turn][wave][0] = v[0];
-    m.buf[turn][wave][1] = v[1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) m.buf[turn][wave][i] = v[i];
   }
   __syncthreads();
-  v[0] = v[1] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = 0.0f;
   for (int w = 0; w < wpr; ++w) {
-    v[0] += m.buf[turn][first + w][0];
-    v[1] += m.buf[turn][first + w][1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += m.buf[turn][first + w][i];
   }
   turn ^= 1;
 }
@@ -167,10 +165,12 @@ struct NormArgs {
 // the variance, so an offset that is large beside the spread costs no
 // precision.  The next row's loads are in flight while this one is summed and
 // written.  (Moments per wave joined behind one barrier instead of two: the
-// same time on bf16 rows of 4096, 20 % more on 5120, from 115 registers
-// instead of 84.)
+// same time on bf16 rows of 4096, 20 % more on 5120, for its 31 registers
+// more.)  15 vector instructions per element are half of the issue slots at
+// 16384 x 8192 bf16; the selections of ragged waves would make it 19, so waves
+// that hold whole vectors go without (8000 x 5000: 41 -> 36 us).
 // ONCE: no gradient will read x again, so it is read past the caches (16384 x
-// 8192 bf16 106 -> 91 us; where the gradient follows, 282 us against 289).
+// 8192 bf16 95 -> 84 us; where the gradient follows, 282 us against 289).
 template <int XT, int YT, int S, int W, int MAXT, bool ONCE, bool AHEAD>
 __global__ __launch_bounds__(MAXT, 4) void k_norm(NormArgs a) {
   __shared__ RowSum sm;
@@ -180,12 +180,15 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm(NormArgs a) {
   const int first = group * wpr, wave = first + __builtin_amdgcn_readfirstlane(t >> 6);
   Place at[S];
   float w[S][W], b[S][W];
+  bool some = false;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
     at[s] = place<W>(s, a.T, t, a.C);
     load_weights<W>(a.w_dt, a.w, at[s].at, 1.0f, w[s]);
     load_weights<W>(a.w_dt, a.b, at[s].at, 0.0f, b[s]);
+    some |= at[s].own > 0;
   }
+  const bool ragged = __ballot(some) != 0;                    // uniform: the wave holds others' elements
   Raw<XT, W> next[S];
   auto fetch = [&](int64_t row) {         // past the last row: that row again, not used
     const char* const x = row_at<XT>(a.x, min(row, a.N - 1) * a.s_x);
@@ -198,12 +201,17 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm(NormArgs a) {
     const int64_t row = row0 + r;
     if constexpr (!AHEAD) fetch(row);
     float v[S][W];
-    float sum[2] = {0.0f, 0.0f};
+    float sum[1] = {0.0f};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       next[s].floats(v[s]);
+      if (!ragged) {
 #pragma unroll
-      for (int j = 0; j < W; ++j) sum[0] += j >= at[s].own ? v[s][j] : 0.0f;
+        for (int j = 0; j < W; ++j) sum[0] += v[s][j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) sum[0] += j >= at[s].own ? v[s][j] : 0.0f;
+      }
     }
     if (AHEAD && r + a.G < a.rows) fetch(row + a.G);
     row_sum(sm, turn, wave, first, wpr, sum);
@@ -212,11 +220,20 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm(NormArgs a) {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        v[s][j] -= m0;
-        const float d = j >= at[s].own ? v[s][j] : 0.0f;
-        sq[0] = fmaf(d, d, sq[0]);
-        sq[1] += d;
+      for (int j = 0; j < W; ++j) v[s][j] -= m0;
+      if (!ragged) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          sq[0] = fmaf(v[s][j], v[s][j], sq[0]);
+          sq[1] += v[s][j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const float d = j >= at[s].own ? v[s][j] : 0.0f;
+          sq[0] = fmaf(d, d, sq[0]);
+          sq[1] += d;
+        }
       }
     }
     row_sum(sm, turn, wave, first, wpr, sq);
@@ -258,6 +275,9 @@ struct alignas(4 * P) RunOf {
   float v[P];
 };
 
+// x and dy are read once and dx written once: 16384 x 8192 bf16 take 170 us,
+// 4.9 TB/s with the 34 MB of chunk sums, where a large copy moves 5.1; 158 us
+// without the weights' sums.
 // AHEAD: the next row's loads are in flight, where the registers allow it
 template <int XT, int YT, int S, int W, int MAXT, bool AHEAD>
 __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
@@ -269,13 +289,16 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
   const int first = group * wpr, wave = first + __builtin_amdgcn_readfirstlane(t >> 6);
   Place at[S];
   float w[S][W], dw[S][W], db[S][W];
+  bool some = false;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
     at[s] = place<W>(s, a.T, t, a.C);
     load_weights<W>(a.w_dt, a.w, at[s].at, 1.0f, w[s]);
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[s][j] = db[s][j] = 0.0f;
+    some |= at[s].own > 0;
   }
+  const bool ragged = __ballot(some) != 0;                    // uniform: the wave holds others' elements
   // the last rows first: they are what the forward pass left in the memory-side cache
   const int64_t chunk = gridDim.x - 1 - blockIdx.x;
   const int64_t row0 = chunk * a.chunk;
@@ -319,9 +342,20 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
           db[s][j] += g[s][j];
         }
         g[s][j] *= w[s][j];
-        const float u = j >= at[s].own ? g[s][j] : 0.0f;
-        sum[0] += u;
-        sum[1] = fmaf(u, h[s][j], sum[1]);
+      }
+      if (!ragged) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          sum[0] += g[s][j];
+          sum[1] = fmaf(g[s][j], h[s][j], sum[1]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const float u = j >= at[s].own ? g[s][j] : 0.0f;
+          sum[0] += u;
+          sum[1] = fmaf(u, h[s][j], sum[1]);
+        }
       }
     }
     if (a.dx == nullptr) continue;                            // uniform
@@ -482,7 +516,8 @@ __global__ __launch_bounds__(T, 4) void k_norm_grad_wide(NormGradArgs a) {
 // at bit o = e + 148 of the accumulator (digit 0 weighs 2^-298) and its 24
 // bits touch digits o/32 and o/32 + 1, 4..13 of the 18.  A column's digits
 // live in LDS; the waves of a workgroup add into them with 64-bit integer
-// atomics, whose order cannot matter.
+// atomics, whose order cannot matter.  512 chunks of 8192 columns take 16 us
+// (2.1 TB/s); sums kept in registers first took 3 us longer.
 constexpr int DIG0 = 4, NDIG = 10, COL_WAVES = 16, SPLIT_MAX = 64;
 
 struct ColArgs {
