@@ -26,11 +26,14 @@ using namespace rowops;
 
 // ---------------------------------------------------------------- geometry
 //
-// T threads own a row (as few waves as hold C elements), S vectors of W
-// elements each: vector s of thread t starts at element (s T + t) W.  G rows
-// at a time in a workgroup.  W is 8 when x and y are both bf16 (16 bytes),
-// else 4; 1 for rows shorter than that.  All of it follows from C and the
-// types, so the sums' order does.
+// T threads own a row, S vectors of W elements each: vector s of thread t
+// starts at element (s T + t) W.  T is as few waves as hold C elements; for
+// short rows a power of two of a wave's lanes (500000 x 128 bf16 forward 119 ->
+// 52 us, 5.0 TB/s, backward 176 -> 89; 2000000 x 17 373 -> 44 and 646 -> 112;
+// rows of 256 keep half a wave each: 75 -> 61 and 123 -> 97).  G rows at a time
+// in a workgroup.  W is 8 when x and y are both bf16 (16 bytes), else 4; 1 for
+// rows shorter than that.  All of it follows from C and the types, so the sums'
+// order does.
 //
 // Every access is a whole vector: one that would pass the row's end starts at
 // C - W instead.  Its first `own` elements are then the previous vector's too:
@@ -47,6 +50,10 @@ using namespace rowops;
 // per element: 8 % at 16 rows, 4 % at 32).  Wide rows of 8193 and more fill a
 // CU with one workgroup each: 16 again (3868 x 12995 bf16 132 -> 90 us).
 constexpr int chunk_rows(int64_t C) { return C <= 512 ? 64 : C <= 4096 || C > 8192 ? 16 : 32; }
+
+// Rows of at most this many columns (heads' norms, and all narrower ones): a
+// wave holds several, each in 1, 2, .. 32 of its lanes.
+constexpr int SHORT_C = 256;
 
 // W elements of type DT as loaded, 16 or 8 bytes
 template <int DT, int W>
@@ -148,6 +155,20 @@ __device__ __forceinline__ void row_sum(RowSum& m, int& turn, int wave, int firs
   turn ^= 1;
 }
 
+// The same over the P lanes (1, 2, .. 32) that hold a short row: a butterfly,
+// so every one of them has the sum, and the same bits.
+template <int NV>
+__device__ __forceinline__ void lanes_sum(int P, float (&v)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {          // all branches uniform
+    if (P > 1) v[i] += dpp<0xB1>(0.0f, v[i]);                 // lane ^ 1
+    if (P > 2) v[i] += dpp<0x4E>(0.0f, v[i]);                 // lane ^ 2
+    if (P > 4) v[i] += dpp<0x141>(0.0f, v[i]);                // mirrored in 8 lanes
+    if (P > 8) v[i] += dpp<0x140>(0.0f, v[i]);                // mirrored in 16
+    if (P > 16) v[i] += __shfl_xor(v[i], 16);
+  }
+}
+
 // ---------------------------------------------------------------- forward
 struct NormArgs {
   const void* x; int64_t s_x;
@@ -171,12 +192,13 @@ struct NormArgs {
 // that hold whole vectors go without (8000 x 5000: 41 -> 36 us).
 // ONCE: no gradient will read x again, so it is read past the caches (16384 x
 // 8192 bf16 95 -> 84 us; where the gradient follows, 282 us against 289).
-template <int XT, int YT, int S, int W, int MAXT, bool ONCE, bool AHEAD>
+template <int XT, int YT, int S, int W, int MAXT, bool ONCE, bool AHEAD, bool SHORT>
 __global__ __launch_bounds__(MAXT, 4) void k_norm(NormArgs a) {
   __shared__ RowSum sm;
   int turn = 0;
-  // a workgroup is T x G threads and T whole waves: a wave's row, and its address, are scalars
-  const int t = threadIdx.x, group = __builtin_amdgcn_readfirstlane(threadIdx.y), wpr = a.T >> 6;
+  // a workgroup is T x G threads; where T is whole waves a wave's row, and its address, are scalars
+  const int t = threadIdx.x, wpr = a.T >> 6;
+  const int group = SHORT ? threadIdx.y : __builtin_amdgcn_readfirstlane(threadIdx.y);
   const int first = group * wpr, wave = first + __builtin_amdgcn_readfirstlane(t >> 6);
   Place at[S];
   float w[S][W], b[S][W];
@@ -214,7 +236,8 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm(NormArgs a) {
       }
     }
     if (AHEAD && r + a.G < a.rows) fetch(row + a.G);
-    row_sum(sm, turn, wave, first, wpr, sum);
+    if constexpr (SHORT) lanes_sum(a.T, sum);
+    else row_sum(sm, turn, wave, first, wpr, sum);
     const float m0 = sum[0] * a.inv_c;
     float sq[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -236,7 +259,8 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm(NormArgs a) {
         }
       }
     }
-    row_sum(sm, turn, wave, first, wpr, sq);
+    if constexpr (SHORT) lanes_sum(a.T, sq);
+    else row_sum(sm, turn, wave, first, wpr, sq);
     if (row >= a.N) continue;
     const float off = sq[1] * a.inv_c;
     const float var = fmaxf(fmaf(-off, off, sq[0] * a.inv_c), 0.0f);
@@ -279,13 +303,14 @@ struct alignas(4 * P) RunOf {
 // 4.9 TB/s with the 34 MB of chunk sums, where a large copy moves 5.1; 158 us
 // without the weights' sums.
 // AHEAD: the next row's loads are in flight, where the registers allow it
-template <int XT, int YT, int S, int W, int MAXT, bool AHEAD>
+template <int XT, int YT, int S, int W, int MAXT, bool AHEAD, bool SHORT>
 __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
   __shared__ RowSum sm;
   extern __shared__ __align__(16) float4 fold_lds[];          // [G][2 S W / P][T] runs of P when G > 1
   int turn = 0;
-  // a workgroup is T x G threads and T whole waves: a wave's row, and its address, are scalars
-  const int t = threadIdx.x, group = __builtin_amdgcn_readfirstlane(threadIdx.y), wpr = a.T >> 6;
+  // a workgroup is T x G threads; where T is whole waves a wave's row, and its address, are scalars
+  const int t = threadIdx.x, wpr = a.T >> 6;
+  const int group = SHORT ? threadIdx.y : __builtin_amdgcn_readfirstlane(threadIdx.y);
   const int first = group * wpr, wave = first + __builtin_amdgcn_readfirstlane(t >> 6);
   Place at[S];
   float w[S][W], dw[S][W], db[S][W];
@@ -337,7 +362,7 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         h[s][j] = (h[s][j] - mean) * rstd;
-        if (live) {                                           // uniform in a wave
+        if (live) {                                           // of a wave, or of the short row's lanes
           dw[s][j] = fmaf(g[s][j], h[s][j], dw[s][j]);
           db[s][j] += g[s][j];
         }
@@ -359,7 +384,8 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
       }
     }
     if (a.dx == nullptr) continue;                            // uniform
-    row_sum(sm, turn, wave, first, wpr, sum);
+    if constexpr (SHORT) lanes_sum(a.T, sum);
+    else row_sum(sm, turn, wave, first, wpr, sum);
     if (!live) continue;
     const float m1 = sum[0] * a.inv_c, m2 = sum[1] * a.inv_c;
     char* const dx = row_at<XT>(a.dx, (row0 + r) * a.C);
@@ -381,7 +407,8 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
     }
     return;
   }
-  // the groups' sums, added in group order: runs of P columns, dealt to the groups
+  // the groups' sums, added in group order, eight by eight (short rows have up to
+  // 64 groups): runs of P columns, dealt to the groups
   constexpr int P = W == 1 ? 1 : 4, Q = S * W / P;            // runs of dw; as many of db
   using run = RunOf<P>;
   run* const fold = reinterpret_cast<run*>(fold_lds);
@@ -400,11 +427,16 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
   }
   __syncthreads();
   for (int q = group; q < 2 * Q; q += a.G) {
-    run v = fold[q * a.T + t];
-    for (int k = 1; k < a.G; ++k) {
-      const run u = fold[(k * 2 * Q + q) * a.T + t];
+    run v;
+    for (int k0 = 0; k0 < a.G; k0 += 8) {
+      run e = fold[(k0 * 2 * Q + q) * a.T + t];
+      for (int k = k0 + 1; k < min(k0 + 8, a.G); ++k) {
+        const run u = fold[(k * 2 * Q + q) * a.T + t];
 #pragma unroll
-      for (int i = 0; i < P; ++i) v.v[i] += u.v[i];
+        for (int i = 0; i < P; ++i) e.v[i] += u.v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) v.v[i] = k0 == 0 ? e.v[i] : v.v[i] + e.v[i];
     }
     const int qq = q < Q ? q : q - Q;
     const Place to = place<W>(qq / (W / P), a.T, t, a.C);
@@ -702,26 +734,33 @@ det_status check_rows(int x_dt, int w_dt, int y_dt, const void* x, int64_t s_x, 
 // threads that hold a row of C elements, S W each
 int threads_of(int64_t C, int S, int W) { return static_cast<int>(ceil_div(C, 64 * S * W)) * 64; }
 
-template <int XT, int YT, int S, int W, int MAXT>
+// lanes that hold a short row: a power of two
+int lanes_of(int64_t C, int S, int W) {
+  int P = 1;
+  while (P * S * W < C) P *= 2;
+  return P;
+}
+
+template <int XT, int YT, int S, int W, int MAXT, bool SHORT = false>
 void launch_norm(NormArgs a, hipStream_t s) {
-  a.T = threads_of(a.C, S, W);
+  a.T = SHORT ? lanes_of(a.C, S, W) : threads_of(a.C, S, W);
   a.G = std::max(1, 256 / a.T);
   // enough workgroups for eight to a CU before rows share one (and its weights)
   a.rows = static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, a.N / (2048 * a.G)))) * a.G;
   const dim3 grid(static_cast<unsigned>(ceil_div(a.N, a.rows))), block(a.T, a.G);
-  if (a.rstd == nullptr) hipLaunchKernelGGL((k_norm<XT, YT, S, W, MAXT, true, (MAXT <= 512)>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_norm<XT, YT, S, W, MAXT, false, (MAXT <= 512)>), grid, block, 0, s, a);
+  if (a.rstd == nullptr) hipLaunchKernelGGL((k_norm<XT, YT, S, W, MAXT, true, (MAXT <= 512), SHORT>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_norm<XT, YT, S, W, MAXT, false, (MAXT <= 512), SHORT>), grid, block, 0, s, a);
 }
 
-template <int XT, int YT, int S, int W, int MAXT>
+template <int XT, int YT, int S, int W, int MAXT, bool SHORT = false>
 void launch_norm_grad(NormGradArgs a, hipStream_t s) {
-  a.T = threads_of(a.C, S, W);
+  a.T = SHORT ? lanes_of(a.C, S, W) : threads_of(a.C, S, W);
   // twice the rows at a time for few long rows: 1021 x 1537 fp32 15.5 -> 13.3 us, but
-  // 32768 x 1024 bf16 52 -> 59
-  a.G = std::max(1, std::min(8, (a.C > 1024 ? 1024 : 512) / a.T));
+  // 32768 x 1024 bf16 52 -> 59; short rows at most one chunk's
+  a.G = std::max(1, std::min(SHORT ? chunk_rows(SHORT_C) : 8, (a.C > 1024 ? 1024 : 512) / a.T));
   a.chunk = chunk_rows(a.C);
   const size_t lds = a.G > 1 && a.parts != nullptr ? static_cast<size_t>(a.G) * a.T * S * W * 2 * sizeof(float) : 0;
-  hipLaunchKernelGGL((k_norm_grad<XT, YT, S, W, MAXT, (S * W <= 8)>), dim3(static_cast<unsigned>(ceil_div(a.N, a.chunk))),
+  hipLaunchKernelGGL((k_norm_grad<XT, YT, S, W, MAXT, (S * W <= 8), SHORT>), dim3(static_cast<unsigned>(ceil_div(a.N, a.chunk))),
                      dim3(a.T, a.G), lds, s, a);
 }
 
@@ -742,7 +781,8 @@ void launch_norm_grad_wide(NormGradArgs a, hipStream_t s) {
 template <int XT, int YT>
 void forward(const NormArgs& a, hipStream_t s) {
   constexpr int W = XT == DET_BF16 && YT == DET_BF16 ? 8 : 4;
-  if (a.C < W) launch_norm<XT, YT, 1, 1, 512>(a, s);
+  if (a.C < W) launch_norm<XT, YT, 1, 1, 512, true>(a, s);
+  else if (a.C <= SHORT_C) launch_norm<XT, YT, 8 / W, W, 512, true>(a, s);
   else if (a.C <= 512) launch_norm<XT, YT, 8 / W, W, 512>(a, s);
   else if (a.C <= 8192) launch_norm<XT, YT, 16 / W, W, 512>(a, s);
   else if (a.C <= 16384) launch_norm<XT, YT, 16 / W, W, 1024>(a, s);
@@ -751,7 +791,8 @@ void forward(const NormArgs& a, hipStream_t s) {
 template <int XT, int YT>
 void backward(const NormGradArgs& a, hipStream_t s) {
   constexpr int W = XT == DET_BF16 && YT == DET_BF16 ? 8 : 4;
-  if (a.C < W) launch_norm_grad<XT, YT, 1, 1, 512>(a, s);
+  if (a.C < W) launch_norm_grad<XT, YT, 1, 1, 512, true>(a, s);
+  else if (a.C <= SHORT_C) launch_norm_grad<XT, YT, 8 / W, W, 512, true>(a, s);
   else if (a.C <= 512) launch_norm_grad<XT, YT, 8 / W, W, 512>(a, s);
   else if (a.C <= 8192) launch_norm_grad<XT, YT, 8 / W, W, 1024>(a, s);
   else if (a.C <= 16384) launch_norm_grad<XT, YT, 16 / W, W, 1024>(a, s);

@@ -334,3 +334,54 @@ def test_module_trains():
     lin(m(x)).square().mean().backward()
     assert x.grad.shape == x.shape and m.weight.grad.dtype == BF16 and m.bias.grad.shape == (64,)
     assert math.isfinite(m.weight.grad.float().sum().item())
+
+
+# Several rows to a wave: each power of two of its lanes and both sides of it,
+# rows of less than a vector; row counts around the chunk of 64, and so many
+# that workgroups take several rows in turn.  A lane adds at most 8 values and
+# a row 5 sums of lanes; a chunk's 64 rows are added within 7 + 7 + 8: the
+# bounds above hold as they are.
+@pytest.mark.parametrize("C", [2, 4, 6, 8, 9, 15, 16, 17, 31, 32, 40, 63, 64, 65, 127, 128, 129, 200, 255, 256, 257])
+@pytest.mark.parametrize("types", [(F32, BF16, F32), (BF16, BF16, BF16), (F32, F32, BF16)],
+                         ids=lambda t: "-".join(NAMES[v] for v in t))
+def test_short_rows(C, types):
+    xt, wt, yt = types
+    for N in (1, 63, 130, 2 * 2048 * 256 // min(C, 256) + 5):
+        announce(f"layer norm of short rows {N}x{C} x={NAMES[xt]} w={NAMES[wt]} y={NAMES[yt]}")
+        x, w, b, dy = _inputs(N, C, xt, wt, yt, 77 * N + C)
+        q = _formula(x, w, b, dy, 1e-5)
+        y, mean, rstd = det.layer_norm_forward(x, w, b, 1e-5, yt)
+        _check_forward(y, q, yt)
+        dx, dw, db = det.layer_norm_backward(dy, x, w, mean, rstd)
+        _check_backward(dx, dw, db, q, xt, wt)
+
+
+@pytest.mark.parametrize("C", [3, 24, 128, 250])
+def test_short_rows_of_a_wider_tensor_keep_their_bits(C):
+    # one row, a part of the rows, rows that are columns of a wider tensor
+    x, w, b, dy = _inputs(700, C, BF16, BF16, BF16, 90)
+    wide = torch.zeros(700, C + 5, dtype=BF16, device="cuda")
+    wide[:, 3:C + 3] = x
+    y, mean, rstd = det.layer_norm_forward(x, w, b)
+    dx, dw, db = det.layer_norm_backward(dy, x, w, mean, rstd)
+    xs = wide[:, 3:C + 3]
+    ys, ms, rs = det.layer_norm_forward(xs, w, b)
+    assert torch.equal(ys, y) and torch.equal(ms, mean) and torch.equal(rs, rstd)
+    assert all(torch.equal(p, q) for p, q in zip(det.layer_norm_backward(dy, xs, w, ms, rs), (dx, dw, db)))
+    for rows in (slice(0, 1), slice(699, 700), slice(65, 66), slice(3, 450)):
+        y1, m1, r1 = det.layer_norm_forward(x[rows], w, b)
+        assert torch.equal(y1, y[rows]) and torch.equal(m1, mean[rows]) and torch.equal(r1, rstd[rows])
+        assert torch.equal(det.layer_norm_backward(dy[rows], x[rows], w, m1, r1)[0], dx[rows])
+
+
+def test_short_rows_keep_nan_and_infinity_to_themselves():
+    x, w, b, dy = _inputs(130, 40, F32, F32, F32, 91)
+    y, mean, rstd = det.layer_norm_forward(x, w, b)
+    dx = det.layer_norm_backward(dy, x, w, mean, rstd)[0]
+    x[7, 3], x[8, 0] = float("nan"), float("inf")
+    y1, m1, r1 = det.layer_norm_forward(x, w, b)
+    dx1 = det.layer_norm_backward(dy, x, w, m1, r1)[0]
+    bad = torch.zeros(130, dtype=torch.bool, device="cuda")
+    bad[7:9] = True
+    assert torch.equal(y1[~bad], y[~bad]) and torch.equal(dx1[~bad], dx[~bad])
+    assert torch.isnan(y1[bad]).all() and torch.isnan(dx1[bad]).all()
