@@ -11,6 +11,7 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -87,17 +88,21 @@ std::pair<Tensor, int64_t> grad_rows(const Tensor& g, at::IntArrayRef lead, cons
   return {g.contiguous(), 1};
 }
 
-// gradients of gradients are not formed: with create_graph the results carry a node that says so
-variable_list once(variable_list grads, const variable_list& incoming, const char* name) {
-  bool want = false;
-  if (at::GradMode::is_enabled())
-    for (const auto& g : incoming) want = want || (g.defined() && g.requires_grad());
-  if (!want) return grads;
+// Gradients of gradients are not formed.  A backward pass that is itself
+// recorded (create_graph) gives gradients whose node refuses to run; it has
+// edges to everything they depend on, the saved inputs and the incoming
+// gradients, so that a derivative through any of these reaches it, also where
+// it is asked for one input alone.  Torch's own DelayedError hangs on the
+// results only: grad(loss + g.pow(2).sum(), x) would leave it out and return
+// the first-order terms.
+variable_list once(variable_list grads, const variable_list& sources, const char* name) {
+  if (!at::GradMode::is_enabled()) return grads;
+  const auto refusal = std::make_shared<torch::autograd::Error>(
+      std::string(name) + " is differentiable once",
+      torch::autograd::collect_next_edges(at::ArrayRef<Tensor>(sources)));
   for (auto& g : grads)
-    if (g.defined()) g.set_requires_grad(true);
-  auto err = std::make_shared<torch::autograd::DelayedError>(
-      std::string(name) + " is differentiable once", static_cast<int64_t>(grads.size()));
-  return err->apply(std::move(grads));
+    if (g.defined()) torch::autograd::set_history(g, refusal);
+  return grads;
 }
 
 bool wants_grad(const Tensor& t) { return t.defined() && t.requires_grad(); }
@@ -209,7 +214,7 @@ struct NormFn : torch::autograd::Function<NormFn> {
       g = norm_backward(grads[0], saved[0], w, saved[2], saved[3], ctx->needs_input_grad(0), need_w, need_b, gt,
                         false);
     }
-    variable_list r = once({g.dx, g.dw, g.db}, grads, "layer_norm");
+    variable_list r = once({g.dx, g.dw, g.db}, {saved[0], saved[1], grads[0]}, "layer_norm");
     r.resize(5);
     return r;
   }
@@ -358,7 +363,9 @@ struct ScoreFn : torch::autograd::Function<ScoreFn> {
       dz = score_backward(saved[0], opt(saved[1]), saved[2], ctx->saved_data["scale"].toDouble(),
                           ctx->saved_data["ignore"].toInt(), ti, glp, gent, gtop);
     }
-    variable_list r = once({dz}, grads, "token_logprobs");
+    variable_list sources = grads;
+    sources.push_back(saved[0]);
+    variable_list r = once({dz}, sources, "token_logprobs");
     r.resize(5);
     return r;
   }
@@ -449,7 +456,7 @@ struct DistillFn : torch::autograd::Function<DistillFn> {
       const at::NoGradGuard no_grad;
       dz = distill_backward(saved[0], saved[1], saved[2], saved[3], grads[0], ctx->saved_data["T"].toDouble());
     }
-    variable_list r = once({dz}, grads, "distill_loss");
+    variable_list r = once({dz}, {saved[0], grads[0]}, "distill_loss");
     r.resize(4);
     return r;
   }
