@@ -105,6 +105,13 @@ variable_list once(variable_list grads, const variable_list& sources, const char
   return grads;
 }
 
+// Nor are forward-mode derivatives: a result without its tangent would pass
+// for a constant, so inputs and incoming gradients that carry one are refused.
+void no_tangent(const OptTensor& t, const char* what) {
+  if (t && t->defined() && t->_fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
+    throw std::runtime_error(std::string(what) + " forms no forward-mode derivatives");
+}
+
 bool wants_grad(const Tensor& t) { return t.defined() && t.requires_grad(); }
 bool wants_grad(const OptTensor& t) { return t && t->requires_grad(); }
 
@@ -201,6 +208,7 @@ struct NormFn : torch::autograd::Function<NormFn> {
     return y;
   }
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    no_tangent(grads[0], "layer_norm");
     const auto saved = ctx->get_saved_variables();
     const OptTensor w = saved[1].defined() ? OptTensor(saved[1]) : std::nullopt;
     const auto gt = static_cast<ScalarType>(ctx->saved_data["grad_dtype"].toInt());
@@ -222,6 +230,7 @@ struct NormFn : torch::autograd::Function<NormFn> {
 
 Tensor layer_norm(const Tensor& x, const OptTensor& w, const OptTensor& b, double eps,
                   std::optional<ScalarType> out_dtype) {
+  for (const OptTensor& t : {OptTensor(x), w, b}) no_tangent(t, "layer_norm");
   if (at::GradMode::is_enabled() && (wants_grad(x) || wants_grad(w) || wants_grad(b)))
     return NormFn::apply(x, w, b, eps, out_dtype);
   return std::get<0>(norm_forward(x, w, b, eps, out_dtype, false));
@@ -353,6 +362,7 @@ struct ScoreFn : torch::autograd::Function<ScoreFn> {
     return outs;
   }
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    for (const Tensor& g : grads) no_tangent(g, "token_logprobs");
     const auto saved = ctx->get_saved_variables();
     auto opt = [](const Tensor& t) { return t.defined() ? OptTensor(t) : std::nullopt; };
     Tensor dz;
@@ -374,6 +384,7 @@ struct ScoreFn : torch::autograd::Function<ScoreFn> {
 using ScoreTuple = std::tuple<OptTensor, Tensor, Tensor, Tensor>;
 
 ScoreTuple token_logprobs(const Tensor& logits, const OptTensor& targets, double scale, int64_t top, int64_t ignore) {
+  no_tangent(logits, "token_logprobs");
   auto opt = [](const Tensor& t) { return t.defined() ? OptTensor(t) : std::nullopt; };
   if (at::GradMode::is_enabled() && wants_grad(logits)) {
     const variable_list r = ScoreFn::apply(logits, targets, scale, top, ignore);
@@ -450,6 +461,7 @@ struct DistillFn : torch::autograd::Function<DistillFn> {
     return r.loss;
   }
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    no_tangent(grads[0], "distill_loss");
     const auto saved = ctx->get_saved_variables();
     Tensor dz;
     {
@@ -463,6 +475,7 @@ struct DistillFn : torch::autograd::Function<DistillFn> {
 };
 
 Tensor distill_loss(const Tensor& logits, const Tensor& teacher, const Tensor& index, double T) {
+  no_tangent(logits, "distill_loss");
   if (at::GradMode::is_enabled() && wants_grad(logits)) return DistillFn::apply(logits, teacher.detach(), index, T);
   return distill_forward(logits, teacher, index, T).loss;
 }

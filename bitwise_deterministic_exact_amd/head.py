@@ -58,7 +58,8 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
                    top: int = 0, ignore_index: int = -100) -> TokenLogProbs:
     """Log probabilities of ``targets`` under softmax(scale * logits), the
     entropy, and the ``top`` most likely tokens with their log probabilities
-    (ties to the lower index); differentiable (once) in the logits.
+    (ties to the lower index); differentiable (once, in reverse
+    mode) in the logits.
 
     logits: float32 or bfloat16 [..., V]; targets: int64 [...] (None: no
     logprob), ``ignore_index`` gives 0 and no gradient, any other value outside
@@ -85,8 +86,8 @@ def distill_loss(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ind
                  temperature: float = 1.0) -> torch.Tensor:
     """Per row T^2 KL(q || p): q the softmax of the teacher's K logits
     (renormalised over the K), p the student's over its whole vocabulary, both
-    at temperature T; differentiable (once) in the student's logits (the
-    teacher is a constant).  float32 of the logits' leading shape; exact_mean
+    at temperature T; differentiable (once, in reverse mode) in the student's
+    logits (the teacher is a constant).  float32 of the logits' leading shape; exact_mean
     gives the batch's mean.
 
     logits: float32 or bfloat16 [..., V]; teacher_logits: float32 or bfloat16

@@ -62,8 +62,8 @@ def layer_norm_digits(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rst
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
-    """Layer norm of x over its last dimension, differentiable (once); see the
-    module docstring.  x: float32 or bfloat16 [..., C], C <= 32768; weight and
+    """Layer norm of x over its last dimension, differentiable (once, in
+    reverse mode); see the module docstring.  x: float32 or bfloat16 [..., C], C <= 32768; weight and
     bias (both optional): [C], one dtype; result of ``out_dtype`` (default x's)."""
     return _lib.ops().layer_norm(x, weight, bias, eps, out_dtype)
 

@@ -3,6 +3,7 @@ for derivatives that they do not form: an error, never a result that leaves
 terms out."""
 import pytest
 import torch
+import torch.autograd.forward_ad as fw
 
 import bitwise_deterministic_exact_amd as det
 
@@ -58,3 +59,23 @@ def test_derivatives_in_the_incoming_gradient_are_refused():
         g, = torch.autograd.grad(call(leaf).sum() * scale, leaf, create_graph=True)
         with pytest.raises(RuntimeError, match="differentiable once"):
             torch.autograd.grad(g.sum(), scale)
+
+
+def test_tangents_of_incoming_gradients_are_refused():
+    for call, shape in _ops().values():
+        leaf = _randn(*shape, seed=6).requires_grad_(True)
+        y = call(leaf)
+        with fw.dual_level():
+            dual = fw.make_dual(torch.ones_like(y), torch.ones_like(y))
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                torch.autograd.grad(y, leaf, dual)
+
+
+def test_exact_mean_takes_the_derivatives_it_can():
+    t = _randn(7, seed=8).requires_grad_(True)
+    g, = torch.autograd.grad(det.exact_mean(t * t), t, create_graph=True)
+    h, = torch.autograd.grad(g.sum(), t)           # of 2 t / 7
+    want = torch.full((7,), 2.0, device="cuda") * (torch.ones((), device="cuda") / torch.full((), 7.0, device="cuda"))
+    assert torch.equal(h, want)
+    with fw.dual_level(), pytest.raises(RuntimeError):
+        det.exact_mean(fw.make_dual(_randn(7), _randn(7)))
