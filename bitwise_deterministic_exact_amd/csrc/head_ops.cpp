@@ -7,11 +7,15 @@
 // from Python (ctypes, torch.autograd.Function) a forward and backward pass
 // took 150 us of host time on [512, 1000] logits.
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/functions/utils.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -105,7 +109,17 @@ variable_list once(variable_list grads, const variable_list& sources, const char
   return grads;
 }
 
-// Nor are forward-mode derivatives: a result without its tangent would pass
+// A trace (torch.jit.trace, make_fx) sees the allocations of the results but
+// not what fills them: the traced function would return whatever lies there.
+// So a call that is being traced is refused.
+void not_traced(const char* what) {
+  using c10::impl::TorchDispatchModeKey;
+  if (torch::jit::tracer::isTracing() || c10::impl::TorchDispatchModeTLS::get_mode(TorchDispatchModeKey::PROXY) ||
+      c10::impl::tls_is_dispatch_key_included(c10::DispatchKey::PreDispatch))
+    throw std::runtime_error(std::string(what) + " cannot be traced: its kernels are not torch operators");
+}
+
+// Forward-mode derivatives are not formed: a result without its tangent would pass
 // for a constant, so inputs and incoming gradients that carry one are refused.
 void no_tangent(const OptTensor& t, const char* what) {
   if (t && t->defined() && t->_fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
@@ -137,6 +151,7 @@ void check_norm(const Tensor& x, const OptTensor& w, const OptTensor& b, const c
 std::tuple<Tensor, Tensor, Tensor> norm_forward(const Tensor& x, const OptTensor& w, const OptTensor& b, double eps,
                                                 std::optional<ScalarType> out_dtype, bool stats) {
   const char* const what = "layer_norm";
+  not_traced(what);
   check_norm(x, w, b, what);
   const ScalarType yt = out_dtype.value_or(x.scalar_type());
   if (!known(yt)) refuse(what, ": out_dtype must be float32 or bfloat16 (got ", yt, ")");
@@ -164,6 +179,7 @@ NormGrads norm_backward(const Tensor& dy, const Tensor& x, const OptTensor& w, c
                         const Tensor& rstd, bool need_dx, bool need_dw, bool need_db,
                         std::optional<ScalarType> grad_dtype, bool digits) {
   const char* const what = "layer_norm_backward";
+  not_traced(what);
   check_norm(x, w, std::nullopt, what);
   if (dy.sizes() != x.sizes() || !known(dy.scalar_type()) || dy.device() != x.device())
     refuse(what, ": dy must be float32 or bfloat16 of x's shape on x's device");
@@ -281,6 +297,7 @@ struct Scores {
 
 Scores score_forward(const Tensor& logits, const OptTensor& targets, double scale, int64_t top, int64_t ignore) {
   const char* const what = "token_logprobs";
+  not_traced(what);
   check_logits(logits, what);
   check_scale(scale, what);
   const at::IntArrayRef lead = lead_of(logits);
@@ -312,6 +329,7 @@ Tensor score_backward(const Tensor& logits, const OptTensor& targets, const Tens
                       int64_t ignore, const OptTensor& top_index, const OptTensor& g_logprob,
                       const OptTensor& g_entropy, const OptTensor& g_top) {
   const char* const what = "token_logprobs_backward";
+  not_traced(what);
   check_logits(logits, what);
   check_scale(scale, what);
   const at::IntArrayRef lead = lead_of(logits);
@@ -412,6 +430,7 @@ struct Distilled {
 
 Distilled distill_forward(const Tensor& logits, const Tensor& teacher, const Tensor& index, double T) {
   const char* const what = "distill_loss";
+  not_traced(what);
   check_logits(logits, what);
   check_temperature(T, what);
   check_teacher(logits, teacher, index, what);
@@ -432,6 +451,7 @@ Distilled distill_forward(const Tensor& logits, const Tensor& teacher, const Ten
 Tensor distill_backward(const Tensor& logits, const Tensor& index, const Tensor& stat, const Tensor& q,
                         const Tensor& g, double T) {
   const char* const what = "distill_backward";
+  not_traced(what);
   check_logits(logits, what);
   check_temperature(T, what);
   const int64_t V = logits.size(-1), N = logits.numel() / V;
@@ -494,6 +514,7 @@ PYBIND11_MODULE(_ops, m) {
     }
   });
   using release = py::call_guard<py::gil_scoped_release>;
+  m.def("not_traced", &not_traced);
   m.def("layer_norm", &layer_norm, release());
   m.def("layer_norm_forward", [](const Tensor& x, const OptTensor& w, const OptTensor& b, double eps,
                                  std::optional<ScalarType> dt) { return norm_forward(x, w, b, eps, dt, true); },

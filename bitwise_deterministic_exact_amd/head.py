@@ -16,6 +16,8 @@ probabilities -inf, entropy 0 and no gradient.  A row with a NaN or +inf has
 NaN results (indices -1) and sets "nonfinite" in device_status().
 Arguments are checked in the compiled layer (csrc/head_ops.cpp): ValueError
 for a bad shape, dtype, device or value.
+Tracing a call (torch.jit.trace, make_fx) and forward-mode inputs are a
+RuntimeError.
 """
 from __future__ import annotations
 

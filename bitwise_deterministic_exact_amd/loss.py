@@ -28,6 +28,7 @@ from typing import Optional
 
 import torch
 
+from . import _lib
 from .api import det_finalize, exact_dot_digits, exact_sqdiff_digits, mse_grad
 
 
@@ -89,4 +90,5 @@ def exact_mean(t: torch.Tensor) -> torch.Tensor:
     elements.  Its gradient is the one value g / n, broadcast."""
     if t.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("exact_mean takes float32 or bfloat16 tensors")
+    _lib.ops().not_traced("exact_mean")
     return _ExactMean.apply(t)

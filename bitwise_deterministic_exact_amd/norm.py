@@ -16,6 +16,8 @@ x, the weights and y may each be float32 or bfloat16: a DetLinear's float32
 output can be normalised straight into the bfloat16 input of the next one.
 Arguments are checked in the compiled layer (csrc/head_ops.cpp): ValueError
 for a bad shape, dtype or device.
+Tracing a call (torch.jit.trace, make_fx) and forward-mode inputs are a
+RuntimeError.
 """
 from __future__ import annotations
 
