@@ -801,7 +801,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
     }
     const bool in = i >= 0 && i < a.V;
     lds_i[e] = in ? static_cast<int32_t>(i) : -1;
-    lds_w[e] = in ? w : 0.0f;
+    lds_w[e] = in || (a.mode == MODE_DISTILL && w != w) ? w : 0.0f;
     some |= in && w != 0.0f;
   }
   some = __syncthreads_or(some);
@@ -823,8 +823,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
   r.c = a.c;
   r.m = st.x; r.inv = st.y; r.l2s = st.z;
   if (a.mode == MODE_DISTILL) {
-    // sum q = 1, or 0 for a row without entries
-    r.A = some ? a.g[row * a.s_g] / a.scale : 0.0f;
+    // sum q = 1, or 0 for a row without entries, or all NaN (a teacher's NaN or
+    // +inf): then so is the whole row's gradient, as its loss is
+    r.A = lds_w[0] != lds_w[0] ? NAN : some ? a.g[row * a.s_g] / a.scale : 0.0f;
     r.B = 0.0f;
   } else {
     float G = 0.0f;

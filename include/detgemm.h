@@ -517,7 +517,9 @@ det_status det_token_logprobs_grad(det_dtype dt, const void* z, int64_t s_row, i
  *   loss              [N] fp32;  stat: [N][4] as above;  q: [N][K] fp32
  *   workspace         det_head_workspace_bytes(N, V, 0)
  * A row without any entry has the loss 0 and no gradient; a student row of
- * nothing but -inf the loss +inf and no gradient.
+ * nothing but -inf the loss +inf and no gradient.  A NaN or +inf among the
+ * row's logits or its teacher's makes the loss and the row's whole gradient
+ * NaN, and is noted in the device status ("non-finite").
  */
 det_status det_distill(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double temperature,
                        det_dtype teacher_dt, const void* teacher, int64_t s_teacher, const int64_t* entry,
