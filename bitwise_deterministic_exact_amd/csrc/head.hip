@@ -495,6 +495,7 @@ __device__ __forceinline__ void finish_distill(const ScoreArgs& a, const RowSums
   sum = wave_sum(sum);
   const double lsum = none ? 0.0 : log(sum), inv = none ? 0.0 : 1.0 / sum;
   double loss = 0.0;
+  bool invalid = false;
   for (int k = lane; k < a.K; k += 64) {
     const float t = teacher(k);
     float qk = 0.0f;
@@ -504,15 +505,21 @@ __device__ __forceinline__ void finish_distill(const ScoreArgs& a, const RowSums
       qk = static_cast<float>(q);
       if (q > 0.0) {
         const int64_t i = k == lane ? h.index : a.entry[e0 + k];
-        if (i < 0 || i >= a.V) loss = NAN;
+        if (i < 0 || i >= a.V) invalid = true;
         else loss += q * (d - lsum - log_prob(a, r, k == lane ? h.z : logit_at(a, row, i)));
       }
     }
     a.q[row * a.K + k] = bad ? NAN : qk;
   }
   loss = wave_sum(loss);
+  // An entry outside the vocabulary leaves the row without a loss and, by q = 0
+  // throughout, without a gradient: one without that entry's -q would push
+  // probability out of the vocabulary.
+  const bool lost = __ballot(invalid) != 0;
+  if (lost && !bad)
+    for (int k = lane; k < a.K; k += 64) a.q[row * a.K + k] = 0.0f;
   if (lane == 0) {
-    a.loss[row] = (bad || r.bad) ? NAN : static_cast<float>(loss / (a.scale * a.scale));
+    a.loss[row] = (bad || lost || r.bad) ? NAN : static_cast<float>(loss / (a.scale * a.scale));
     if (bad) a.status[0] = 1;
   }
 }

@@ -73,7 +73,7 @@ def distill_forward(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_
                     temperature: float = 1.0):
     """(loss, stat, q): distill_loss without a graph, and what
     distill_backward needs (the rows' statistics and the teacher's
-    probabilities)."""
+    probabilities, 0 in rows without a gradient)."""
     return _lib.ops().distill_forward(logits, teacher_logits, teacher_index, temperature)
 
 
@@ -95,6 +95,7 @@ def distill_loss(logits: torch.Tensor, teacher_logits: torch.Tensor, teacher_ind
     logits: float32 or bfloat16 [..., V]; teacher_logits: float32 or bfloat16
     [..., K], -inf for entries that are not there (their index is not looked
     at); teacher_index: int64 [..., K], an index may repeat; K <= 1024.  A row
-    without any entry has the loss 0 and no gradient; a NaN or +inf among a
-    row's teacher logits makes its loss and its whole gradient NaN."""
+    without any entry has the loss 0 and no gradient; one with an entry outside
+    [0, V) the loss NaN and no gradient; a NaN or +inf among a row's teacher
+    logits makes its loss and its whole gradient NaN."""
     return _lib.ops().distill_loss(logits, teacher_logits, teacher_index, temperature)

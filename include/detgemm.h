@@ -512,9 +512,12 @@ det_status det_token_logprobs_grad(det_dtype dt, const void* z, int64_t s_row, i
  *   teacher           [N] rows of K, s_teacher apart; -inf: no entry
  *   entry             [N] rows of K indices, s_entry apart; those of entries
  *                     without probability are not read as indices; any other
- *                     outside [0, V) makes the row's loss NaN
+ *                     outside [0, V) makes the row's loss NaN and leaves it
+ *                     without a gradient
  *   K                 1..1024; an index may occur more than once
- *   loss              [N] fp32;  stat: [N][4] as above;  q: [N][K] fp32
+ *   loss              [N] fp32;  stat: [N][4] as above
+ *   q                 [N][K] fp32, 0 throughout in a row without a gradient
+ *                     for want of an entry or for an invalid one
  *   workspace         det_head_workspace_bytes(N, V, 0)
  * A row without any entry has the loss 0 and no gradient; a student row of
  * nothing but -inf the loss +inf and no gradient.  A NaN or +inf among the

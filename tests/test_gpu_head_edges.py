@@ -36,3 +36,31 @@ def test_a_bad_teacher_row_has_no_finite_gradient(N, V, K, dt):
     assert torch.isnan(loss[bad]).all() and torch.isnan(dz[bad]).all()
     assert torch.isfinite(loss[~bad]).all() and torch.equal(dz[~bad], clean[~bad])
     assert det.device_status() == {"nonfinite"}
+
+
+@pytest.mark.parametrize("N,V,K", [(8, 5, 2), (8, 5000, 8), (8, 9001, 100), (8, 20000, 9)])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=NAMES.get)
+def test_an_invalid_entry_leaves_its_row_without_a_gradient(N, V, K, dt):
+    z, _ = _logits(N, V, dt, 43)
+    teacher, idx = _teacher(N, V, K, 44)
+    g = torch.ones(N, device="cuda")
+    clean = det.distill_backward(z, idx, *det.distill_forward(z, teacher, idx)[1:], g)
+    idx[1, 0], idx[2, K - 1], idx[4] = V, -1, V + 3          # one, one, all of them
+    teacher[6, 0], idx[6, 0] = -INF, -5                      # not there: not looked at
+    teacher[7, 1], idx[7, 1] = teacher[7, 0] - 102.0, -5     # e^-102: subnormal in fp32, but there
+    lost = torch.zeros(N, dtype=torch.bool, device="cuda")
+    lost[[1, 2, 4, 7]] = True
+    det.device_status()
+    loss, stat, q = det.distill_forward(z, teacher, idx)
+    dz = det.distill_backward(z, idx, stat, q, g)
+    assert torch.isnan(loss[lost]).all() and torch.isfinite(loss[~lost]).all()
+    assert torch.equal(q[lost], torch.zeros_like(q[lost]))
+    assert torch.equal(dz[lost], torch.zeros_like(dz[lost]))
+    same = ~lost
+    same[6] = False
+    assert torch.equal(dz[same], clean[same])
+    _, _, want, tol = _want_distill(z[6:7], teacher[6:7], idx[6:7], 1.0, g[6:7])
+    _check_grad(dz[6:7], want, tol, dt)
+    assert det.device_status() == set()
+    zr = z.clone().requires_grad_(True)
+    assert torch.equal(torch.autograd.grad(det.distill_loss(zr, teacher, idx), zr, g)[0], dz)
