@@ -790,14 +790,17 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
   fetch(part * waves + wave);
 
   // an index outside [0, V) adds nothing
+  constexpr int32_t LOST = -2;            // in the place of an index: q is NaN
   bool some = false;
   for (int e = threadIdx.x; e < n; e += threads) {
     int64_t i;
     float w;
+    bool lost = false;
     if (a.mode == MODE_DISTILL) {
       i = a.entry[row * a.s_entry + e];
       w = a.q[row * a.K + e];
-      w = w > 0.0f || w != w ? -w * a.g[row * a.s_g] / a.scale : 0.0f;
+      lost = w != w;
+      w = w > 0.0f ? -w * a.g[row * a.s_g] / a.scale : 0.0f;
     } else if (e == 0) {
       i = a.target != nullptr ? a.target[row * a.s_target] : -1;
       w = i == a.ignore || a.glp == nullptr ? 0.0f : a.glp[row * a.s_glp];
@@ -807,13 +810,15 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
       w = a.gtop != nullptr ? a.gtop[row * a.s_gtop + (e - 1) * a.s_gtop_k] : 0.0f;
     }
     const bool in = i >= 0 && i < a.V;
-    lds_i[e] = in ? static_cast<int32_t>(i) : -1;
-    lds_w[e] = in || (a.mode == MODE_DISTILL && w != w) ? w : 0.0f;
+    lds_i[e] = lost ? LOST : in ? static_cast<int32_t>(i) : -1;
+    lds_w[e] = in ? w : 0.0f;
     some |= in && w != 0.0f;
   }
   some = __syncthreads_or(some);
   const float ws = a.mode == MODE_DISTILL ? 1.0f : a.scale;
-  const bool empty = st.y == 0.0f;        // such a row has no gradient at all
+  // such a row has no gradient at all, whatever comes in (the log probability
+  // -inf of its target easily makes that infinite or NaN)
+  const bool empty = st.y == 0.0f;
   for (int e = threadIdx.x; e < n; e += threads) {
     const int i = lds_i[e];
     float w = 0.0f;
@@ -832,14 +837,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
   if (a.mode == MODE_DISTILL) {
     // sum q = 1, or 0 for a row without entries, or all NaN (a teacher's NaN or
     // +inf): then so is the whole row's gradient, as its loss is
-    r.A = lds_w[0] != lds_w[0] ? NAN : some ? a.g[row * a.s_g] / a.scale : 0.0f;
+    r.A = lds_i[0] == LOST ? NAN : some && !empty ? a.g[row * a.s_g] / a.scale : 0.0f;
     r.B = 0.0f;
   } else {
     float G = 0.0f;
     for (int e = 0; e < n; ++e) G += lds_w[e];
     const float gent = a.gent != nullptr ? a.gent[row * a.s_gent] : 0.0f;
-    r.A = -a.scale * (G + gent * st.w);
-    r.B = -a.scale * gent * static_cast<float>(LN2);
+    r.A = empty ? 0.0f : -a.scale * (G + gent * st.w);
+    r.B = empty ? 0.0f : -a.scale * gent * static_cast<float>(LN2);
   }
   __syncthreads();
   const int i_lane = lane < n ? own_i[lane] : -1;             // -1 is no chunk's

@@ -495,7 +495,8 @@ det_status det_token_logprobs(det_dtype dt, const void* z, int64_t s_row, int64_
  *   g_top             [N][top] fp32 with strides s_g_top, s_g_top_k; null: none
  *   dz                [N] rows of V of type dt, s_dz >= V apart; must not
  *                     overlap z
- * A row of nothing but -inf gets zeros.  Errors as for det_token_logprobs.
+ * A row of nothing but -inf gets zeros, also where what comes in is not
+ * finite.  Errors as for det_token_logprobs.
  */
 det_status det_token_logprobs_grad(det_dtype dt, const void* z, int64_t s_row, int64_t N, int64_t V, double scale,
                                    const int64_t* target, int64_t s_target, int64_t ignore, int top,

@@ -64,3 +64,29 @@ def test_an_invalid_entry_leaves_its_row_without_a_gradient(N, V, K, dt):
     assert det.device_status() == set()
     zr = z.clone().requires_grad_(True)
     assert torch.equal(torch.autograd.grad(det.distill_loss(zr, teacher, idx), zr, g)[0], dz)
+
+
+@pytest.mark.parametrize("V", [5, 3000, 20000])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=NAMES.get)
+@pytest.mark.parametrize("g", [INF, -INF, NAN])
+def test_rows_without_a_token_have_no_gradient_whatever_comes_in(V, dt, g):
+    N = 5
+    z, t = _logits(N, V, dt, 45)
+    z[1], z[3] = -INF, -INF
+    r, stat = det.token_logprobs_forward(z, t, top=2)
+    one = torch.ones(N, device="cuda")
+    come = one.clone()
+    come[[1, 3]] = g
+    two = come[:, None].expand(N, 2)
+    for kw in ({"g_logprob": come}, {"g_entropy": come}, {"g_top": two},
+               {"g_logprob": come, "g_entropy": come, "g_top": two}):
+        dz = det.token_logprobs_backward(z, t, stat, top_index=r.top_index, **kw)
+        want = det.token_logprobs_backward(z, t, stat, top_index=r.top_index,
+                                           **{k: torch.ones_like(v) for k, v in kw.items()})
+        assert torch.isfinite(want).all() and torch.equal(dz, want)
+        assert torch.equal(dz[[1, 3]], torch.zeros_like(dz[:2]))
+    teacher, idx = _teacher(N, V, 3, 46)
+    _, stat, q = det.distill_forward(z, teacher, idx)
+    dz = det.distill_backward(z, idx, stat, q, come)
+    assert torch.equal(dz, det.distill_backward(z, idx, stat, q, one))
+    assert torch.equal(dz[[1, 3]], torch.zeros_like(dz[:2]))
