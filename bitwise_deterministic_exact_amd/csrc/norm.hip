@@ -564,10 +564,11 @@ struct ColArgs {
   int32_t* status;
 };
 
-// digits to fp32, rounded once (nearest-even): carries first, then the top
-// 24 bits with the rest as a sticky bit
+// digits to a value of the gradient's type, rounded once (nearest-even):
+// carries first, then the top 24 bits (bf16: 8) with the rest as a sticky bit.
+// By way of fp32 a bf16 gradient would be rounded twice: 1 + 2^-8 + 2^-30 to 1.
 template <class D>
-__device__ __forceinline__ float round_column(D digit) {
+__device__ __forceinline__ float round_column(D digit, bool bf16) {
   uint32_t w[NDIG + 1];
   int64_t carry = 0;
 #pragma unroll
@@ -604,8 +605,9 @@ __device__ __forceinline__ float round_column(D digit) {
   uint64_t win = (static_cast<uint64_t>(hi) << 32) | lo;      // its bit 0 weighs 2^(32 (DIG0 + top - 1) - 298)
   int q = 32 * (DIG0 + top - 1) - 298;
   const int n = 64 - __builtin_clzll(win);                    // n >= 33
-  int cut = n - 24;                                           // bits below the 24 kept ones
-  cut = max(cut, -149 - q);                                   // subnormal results keep 2^-149
+  // the bits below the kept ones; subnormal results keep 2^-149 (bf16: 2^-133)
+  const int cut = bf16 ? max(n - 8, -133 - q) : max(n - 24, -149 - q);
+  if (cut > 64) return neg ? -0.0f : 0.0f;                    // bf16, top = 0: 69, and less than 2^-138
   if (cut > 0) {
     const uint64_t rest = win & ((1ull << cut) - 1ull), half = 1ull << (cut - 1);
     win >>= cut;
@@ -620,7 +622,7 @@ template <class D>
 __device__ __forceinline__ void write_column(const ColArgs& a, int64_t col, D digit, bool bad) {
   void* const out = col < a.C ? a.dw : a.db;
   if (out != nullptr) {
-    const float v = bad ? NAN : round_column(digit);
+    const float v = bad ? NAN : round_column(digit, a.w_dt == DET_BF16);
     store_elem(a.w_dt, out, col < a.C ? col : col - a.C, v);
   }
   if (a.digits != nullptr) {

@@ -9,8 +9,8 @@ nor of their strides or alignment.  The weights' gradients are sums over rows
 (tokens): chunks of consecutive rows in float32 in one fixed order, the chunks
 added exactly in the long accumulator and rounded once.  So rows sharded at
 multiples of NORM_SHARD_ROWS (64) give, through layer_norm_digits,
-det_combine and det_finalize, the bits of one call over all of them, as the
-K-shards of an exact GEMM do (det-train page, "Method").
+det_combine and det_finalize, the bits of one call's float32 gradients over
+all of them, as the K-shards of an exact GEMM do (det-train page, "Method").
 
 x, the weights and y may each be float32 or bfloat16: a DetLinear's float32
 output can be normalised straight into the bfloat16 input of the next one.

@@ -449,7 +449,7 @@ det_status det_layer_norm(det_dtype x_dt, const void* x, int64_t s_x, det_dtype 
  * added exactly in the long accumulator and rounded once.  So the digits of
  * row shards cut at multiples of DET_NORM_SHARD_ROWS add up (det_combine) to the digits
  * of all rows, and det_finalize of the sum gives the same bits as one call
- * over all rows, for any number of shards and any order of adding them.
+ * with fp32 dw and db over all rows, for any number of shards and any order of adding them.
  * An Inf or NaN chunk is noted in the device status; those sums are then NaN
  * (their digits unspecified).
  * Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
