@@ -437,6 +437,8 @@ det_status det_layer_norm(det_dtype x_dt, const void* x, int64_t s_x, det_dtype 
  * rstd and g = dy w:
  *   dx = rstd (g - sum g / C - h sum (g h) / C)
  *   dw = sum over rows of dy h,   db = sum over rows of dy
+ * (the mean of h, what the rounding of `mean` to fp32 leaves in it, is taken out
+ * of rows further from 0 than 16 spreads, so there too an offset costs none)
  *   x, mean, rstd     as det_layer_norm read and wrote them
  *   dy                [N] rows of C of type y_dt, s_dy apart
  *   dx                [N][C] contiguous, type x_dt; null: not needed
