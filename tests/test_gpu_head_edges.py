@@ -9,7 +9,7 @@ import torch
 
 import bitwise_deterministic_exact_amd as det
 from tests.gpu_util import announce
-from tests.test_gpu_head import _check_grad, _close, _logits, _teacher, _want_distill
+from tests.test_gpu_head import _check_grad, _logits, _teacher, _want_distill
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,29 @@ def test_rows_without_a_token_have_no_gradient_whatever_comes_in(V, dt, g):
     dz = det.distill_backward(z, idx, stat, q, come)
     assert torch.equal(dz, det.distill_backward(z, idx, stat, q, one))
     assert torch.equal(dz[[1, 3]], torch.zeros_like(dz[:2]))
+
+
+# ------------------------------------------------------------ distillation's gradient, entry by entry
+
+def _check_distill_grad(dz, z, teacher, idx, T, g):
+    """_want_distill's bound; the K values that may be added at one token count
+    where they are added, at the entries (off them the bound is p's alone)."""
+    _, _, want, tol = _want_distill(z, teacher, idx, T, g)
+    q = torch.softmax(teacher.double() / T, -1)
+    own = torch.zeros_like(want).scatter_add_(-1, torch.where(q > 0, idx, 0), q)
+    _check_grad(dz, want, tol + idx.shape[-1] * 2.0 ** -24 * T * g.abs().double()[:, None] * own, z.dtype)
+    off = own == 0
+    assert (tol[off] <= want[off].abs() / 64 + 2.0 ** -125).all()   # so a 0 in the place of p_j does not pass
+
+
+@pytest.mark.parametrize("N,V,K", [(1, 1, 1), (3, 5, 4), (2, 2049, 7), (1, 50257, 64), (5, 8193, 33), (1030, 700, 20),
+                                   (1100, 9000, 64), (3, 4000, 1000), (2, 5, 40)])
+@pytest.mark.parametrize("dt,tdt", [(F32, F32), (BF16, BF16), (BF16, F32)], ids=lambda t: NAMES[t])
+@pytest.mark.parametrize("T", [1.0, 2.5])
+def test_distillation_gradient_of_every_token(N, V, K, dt, tdt, T):
+    announce(f"distill gradient {N}x{V} K={K} {NAMES[dt]} teacher {NAMES[tdt]} T={T}")
+    z, _ = _logits(N, V, dt, N + V)
+    teacher, idx = _teacher(N, V, K, K, tdt)
+    g = torch.rand(N, device="cuda") - 0.3
+    _, stat, q = det.distill_forward(z, teacher, idx, temperature=T)
+    _check_distill_grad(det.distill_backward(z, idx, stat, q, g, temperature=T), z, teacher, idx, T, g)
