@@ -8,8 +8,10 @@ import pytest
 import torch
 
 import bitwise_deterministic_exact_amd as det
+from bitwise_deterministic_exact_amd import _lib
 from tests.gpu_util import announce
-from tests.test_gpu_head import _check_grad, _logits, _teacher, _want_distill
+from tests.test_gpu_head import (_check_grad, _check_scores, _close, _logits, _teacher, _want_distill,
+                                 _want_grad)
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +118,95 @@ def test_distillation_gradient_of_every_token(N, V, K, dt, tdt, T):
     g = torch.rand(N, device="cuda") - 0.3
     _, stat, q = det.distill_forward(z, teacher, idx, temperature=T)
     _check_distill_grad(det.distill_backward(z, idx, stat, q, g, temperature=T), z, teacher, idx, T, g)
+
+
+# ------------------------------------------------------------ rows that several workgroups share
+
+# without alternatives: one to 512 workgroups' sums of a row in the workspace, by
+# few rows, by 384 and more, and by rows of more chunks than one workgroup holds
+SHARED = [(1, 131072), (1, 200003), (3, 70001), (300, 50257), (400, 140000), (1, (1 << 20) + 5), (2, 1 << 24)]
+
+
+@pytest.mark.parametrize("N,V", SHARED)
+@pytest.mark.parametrize("dt", [F32, BF16], ids=NAMES.get)
+def test_scores_of_rows_that_workgroups_share(N, V, dt):
+    announce(f"shared rows, scores {N}x{V} {NAMES[dt]}")
+    assert _lib.load().det_head_workspace_bytes(N, V, 0) > 0
+    z, t = _logits(N, V, dt, 47 + N, masked=True)
+    if N > 2:
+        z[1] = -INF
+        z[2], t[2] = -INF, V - 1
+        z[2, V - 1] = 3.0
+    r, stat = det.token_logprobs_forward(z, t, scale=0.7)
+    _check_scores(r, z, t, 0.7, 0)
+    g = torch.Generator().manual_seed(48)
+    glp, gent = torch.randn(N, generator=g).cuda(), (0.1 * torch.randn(N, generator=g)).cuda()
+    dz = det.token_logprobs_backward(z, t, stat, scale=0.7, g_logprob=glp, g_entropy=gent)
+    _check_grad(dz, *_want_grad(z, t, 0.7, glp, gent), dt)
+    for i in {0, N // 2, N - 1}:                   # alone a row has other workgroups, and the same bits
+        r1, s1 = det.token_logprobs_forward(z[i:i + 1], t[i:i + 1], scale=0.7)
+        assert torch.equal(s1, stat[i:i + 1]) and torch.equal(r1.logprob, r.logprob[i:i + 1])
+        d1 = det.token_logprobs_backward(z[i:i + 1], t[i:i + 1], s1, scale=0.7, g_logprob=glp[i:i + 1],
+                                         g_entropy=gent[i:i + 1])
+        assert torch.equal(d1, dz[i:i + 1])
+    if N > 2:                                      # a NaN stays in its row
+        z[0, V // 3] = NAN
+        det.device_status()
+        r1 = det.token_logprobs(z, t, scale=0.7)
+        assert torch.isnan(r1.logprob[0]) and torch.isnan(r1.entropy[0])
+        assert torch.equal(r1.logprob[1:], r.logprob[1:]) and torch.equal(r1.entropy[1:], r.entropy[1:])
+        assert det.device_status() == {"nonfinite"}
+
+
+@pytest.mark.parametrize("N,V", SHARED)
+@pytest.mark.parametrize("dt", [F32, BF16], ids=NAMES.get)
+def test_distillation_of_rows_that_workgroups_share(N, V, dt):
+    announce(f"shared rows, distillation {N}x{V} {NAMES[dt]}")
+    assert _lib.load().det_head_workspace_bytes(N, V, 0) > 0
+    K, T = 100, 2.0                                # more entries than a wave has lanes
+    z, _ = _logits(N, V, dt, 49 + N)
+    g = torch.Generator().manual_seed(50)
+    idx = torch.randint(0, V, (N, K), generator=g).cuda()
+    teacher = (2.5 * torch.randn(N, K, generator=g)).cuda()
+    idx[:, 70:80] = idx[:, :10]                    # repeated
+    teacher[:, 90:] = -INF                         # not there, and not looked at
+    idx[:, 90:] = -7
+    if N > 2:
+        teacher[2], idx[1, 65] = -INF, V           # no entry at all; an invalid one
+    gr = torch.rand(N, generator=g).cuda() - 0.3
+    loss, stat, q = det.distill_forward(z, teacher, idx, temperature=T)
+    dz = det.distill_backward(z, idx, stat, q, gr, temperature=T)
+    keep = [i for i in range(N) if N <= 2 or i != 1]
+    lw, ltol, _, _ = _want_distill(z[keep], teacher[keep], idx[keep], T, gr[keep])
+    _close("loss", loss[keep], lw, ltol)
+    some = [i for i in keep if N <= 2 or i != 2]
+    _check_distill_grad(dz[some], z[some], teacher[some], idx[some], T, gr[some])
+    if N > 2:
+        assert torch.isnan(loss[1]) and loss[2] == 0
+        assert torch.equal(dz[1:3], torch.zeros_like(dz[1:3]))
+    for i in {0, N // 2, N - 1}:
+        l1, s1, q1 = det.distill_forward(z[i:i + 1], teacher[i:i + 1], idx[i:i + 1], temperature=T)
+        assert torch.equal(l1.nan_to_num(7.0), loss[i:i + 1].nan_to_num(7.0)) and torch.equal(q1, q[i:i + 1])
+        assert torch.equal(det.distill_backward(z[i:i + 1], idx[i:i + 1], s1, q1, gr[i:i + 1], temperature=T), dz[i:i + 1])
+
+
+def test_many_rows_of_more_chunks_than_a_workgroup_holds():
+    # 800 rows of just over 2^20 logits (four different ones, read with their own
+    # targets): two workgroups to a row, where a row alone has 129
+    N, V = 800, (1 << 20) + 5
+    assert _lib.load().det_head_workspace_bytes(N, V, 0) > 0
+    assert _lib.load().det_head_workspace_bytes(N, V - 5, 0) == 0
+    four, _ = _logits(4, V, BF16, 51, masked=True)
+    t = torch.randint(0, V, (N,), generator=torch.Generator().manual_seed(52)).cuda()
+    which = torch.arange(N, device="cuda") % 4
+    z = four[which]
+    r, stat = det.token_logprobs_forward(z, t)
+    _check_scores(type(r)(r.logprob[:4], r.entropy[:4], r.top_logprob[:4], r.top_index[:4]), z[:4], t[:4], 1.0, 0)
+    g = torch.rand(N, device="cuda")
+    dz = det.token_logprobs_backward(z, t, stat, g_logprob=g, g_entropy=g)
+    _check_grad(dz[:4], *_want_grad(z[:4], t[:4], 1.0, g[:4], g[:4]), BF16)
+    for i in range(0, N, 57):
+        r1, s1 = det.token_logprobs_forward(four[i % 4:i % 4 + 1], t[i:i + 1])
+        assert torch.equal(s1, stat[i:i + 1]) and torch.equal(r1.logprob, r.logprob[i:i + 1])
+        assert torch.equal(det.token_logprobs_backward(z[i:i + 1], t[i:i + 1], s1, g_logprob=g[i:i + 1],
+                                                       g_entropy=g[i:i + 1]), dz[i:i + 1])
