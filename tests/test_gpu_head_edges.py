@@ -4,6 +4,8 @@ incoming gradients that are not finite, rows that several workgroups share.
 
 Tolerances are those of test_gpu_head.py, whose derivation they use.
 """
+import math
+
 import pytest
 import torch
 
@@ -210,3 +212,32 @@ def test_many_rows_of_more_chunks_than_a_workgroup_holds():
         assert torch.equal(s1, stat[i:i + 1]) and torch.equal(r1.logprob, r.logprob[i:i + 1])
         assert torch.equal(det.token_logprobs_backward(z[i:i + 1], t[i:i + 1], s1, g_logprob=g[i:i + 1],
                                                        g_entropy=g[i:i + 1]), dz[i:i + 1])
+
+
+# ------------------------------------------------------------ exact_mean
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=NAMES.get)
+@pytest.mark.parametrize("shape", [(1,), (), (3, 1001), (64, 64), (100003,)])
+def test_exact_mean_and_its_gradient_bit_for_bit(dt, shape):
+    t = (torch.randn(shape, generator=torch.Generator().manual_seed(53)) * 3).to(dt)
+    n = max(t.numel(), 1)
+    # fsum rounds the exact sum to 64 bits, far from a tie of fp32 here
+    total = torch.tensor(math.fsum(t.double().reshape(-1).tolist()), dtype=torch.float64).float()
+    x = t.cuda().requires_grad_(True)
+    m = det.exact_mean(x)
+    assert m.shape == () and m.dtype == F32 and torch.equal(m.detach().cpu(), total / torch.tensor(float(n)))
+    g, = torch.autograd.grad(3.0 * m, x)
+    assert g.shape == x.shape and g.dtype == dt
+    assert torch.equal(g.cpu(), (torch.tensor(3.0) / torch.tensor(float(n))).to(dt).expand(shape))
+    if t.dim() == 2:
+        assert torch.equal(det.exact_mean(x.detach().t()), m.detach())
+        assert torch.equal(det.exact_mean(x.detach()[:, ::2]), det.exact_mean(x.detach()[:, ::2].contiguous()))
+
+
+def test_exact_mean_loses_nothing_and_takes_no_elements():
+    t = torch.tensor([1e30, 1.0, 2.0, -1e30], device="cuda")
+    assert det.exact_mean(t).item() == 0.75
+    for dt in (F32, BF16):
+        x = torch.empty(0, 4, dtype=dt, device="cuda", requires_grad=True)
+        m = det.exact_mean(x)
+        assert m.item() == 0.0 and torch.autograd.grad(m, x)[0].shape == (0, 4)
