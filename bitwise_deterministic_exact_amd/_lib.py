@@ -16,12 +16,9 @@ DET_PATH_AUTO, DET_PATH_ACCUMULATOR, DET_PATH_SLICES, DET_PATH_AUTO_HOST = 0, 1,
 NUM_DIGITS = 18
 LSB_EXPONENT = -298
 K_MAX = 1 << 19
-ROWS_MAX = 1 << 22
-HEAD_V_MAX = 1 << 24
+# of the head operators, for what Python itself checks; the header has them all
 NORM_C_MAX = 32768
 NORM_SHARD_ROWS = 64
-TOP_MAX = 64
-ENTRIES_MAX = 1024
 
 _lib = None
 _ops = None

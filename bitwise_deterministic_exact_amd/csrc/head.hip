@@ -32,8 +32,8 @@ using namespace rowops;
 constexpr int CHUNK_BITS = 11, CHUNK = 1 << CHUNK_BITS;       // logits per wave and step
 constexpr int LANE_ELEMS = CHUNK / 64;    // 32 in registers per lane
 constexpr int WAVES = 4;                  // per workgroup
-constexpr int TOP_MAX = 64;               // alternatives per row: one per lane
-constexpr int ENTRIES_MAX = 1024;         // teacher entries per row
+constexpr int TOP_MAX = DET_HEAD_TOP_MAX;                     // alternatives per row: one per lane
+static_assert(TOP_MAX == 64);
 constexpr int LDS_PARTS = 512;            // chunks of a row whose (m, S, U) fit one workgroup's LDS
 constexpr double LOG2E = 1.4426950408889634074, LN2 = 0.69314718055994530942;
 
@@ -1073,7 +1073,7 @@ det_status det_distill(det_dtype dt, const void* z, int64_t s_row, int64_t N, in
   det_status st = check_logits(dt, z, N, V, s_row, 1.0 / temperature);
   if (st != DET_OK) return st;
   if (!known_dtype(teacher_dt)) return fail(DET_EDTYPE, "unknown teacher dtype %d", static_cast<int>(teacher_dt));
-  if (K < 1 || K > ENTRIES_MAX) return fail(DET_EINVAL, "K = %lld must lie in 1..%d", (long long)K, ENTRIES_MAX);
+  if (K < 1 || K > DET_HEAD_ENTRIES_MAX) return fail(DET_EINVAL, "K = %lld must lie in 1..%d", (long long)K, DET_HEAD_ENTRIES_MAX);
   if (s_teacher < 0 || s_entry < 0) return fail(DET_EINVAL, "negative stride");
   if (N == 0) return DET_OK;
   if (teacher == nullptr || entry == nullptr || loss == nullptr || stat == nullptr || q == nullptr)
@@ -1096,7 +1096,7 @@ det_status det_distill_grad(det_dtype dt, const void* z, int64_t s_row, int64_t 
   if (!(temperature > 0.0)) return fail(DET_EINVAL, "the temperature must be positive");
   det_status st = check_logits(dt, z, N, V, s_row, 1.0 / temperature);
   if (st != DET_OK) return st;
-  if (K < 1 || K > ENTRIES_MAX) return fail(DET_EINVAL, "K = %lld must lie in 1..%d", (long long)K, ENTRIES_MAX);
+  if (K < 1 || K > DET_HEAD_ENTRIES_MAX) return fail(DET_EINVAL, "K = %lld must lie in 1..%d", (long long)K, DET_HEAD_ENTRIES_MAX);
   if (s_entry < 0 || s_g < 0 || s_dz < V) return fail(DET_EINVAL, "negative stride, or gradient rows that overlap");
   if (N == 0) return DET_OK;
   if (entry == nullptr || stat == nullptr || q == nullptr || g == nullptr || dz == nullptr)

@@ -254,8 +254,6 @@ Tensor layer_norm(const Tensor& x, const OptTensor& w, const OptTensor& b, doubl
 
 // ---------------------------------------------------------------- logits
 
-constexpr int TOP_MAX = 64, ENTRIES_MAX = 1024;
-
 void check_logits(const Tensor& z, const char* what) {
   if (!known(z.scalar_type())) refuse(what, ": logits must be float32 or bfloat16 (got ", z.scalar_type(), ")");
   if (z.dim() < 1 || z.size(-1) < 1 || z.size(-1) > DET_HEAD_V_MAX)
@@ -302,8 +300,8 @@ Scores score_forward(const Tensor& logits, const OptTensor& targets, double scal
   check_scale(scale, what);
   const at::IntArrayRef lead = lead_of(logits);
   const int64_t V = logits.size(-1), N = logits.numel() / V;
-  if (top < 0 || top > TOP_MAX || top > V)
-    refuse(what, ": top must lie in 0..min(", TOP_MAX, ", V) (got ", top, ")");
+  if (top < 0 || top > DET_HEAD_TOP_MAX || top > V)
+    refuse(what, ": top must lie in 0..min(", DET_HEAD_TOP_MAX, ", V) (got ", top, ")");
   if (targets) check_index(*targets, lead, logits, "targets", what);
   on_gpu(logits, what, "logits");
   const c10::DeviceGuard guard(logits.device());
@@ -418,8 +416,8 @@ void check_teacher(const Tensor& z, const Tensor& teacher, const Tensor& index, 
   if (!known(teacher.scalar_type()) || teacher.device() != z.device())
     refuse(what, ": teacher logits must be float32 or bfloat16 on the logits' device");
   if (teacher.dim() != z.dim() || lead_of(teacher) != lead_of(z) || teacher.size(-1) < 1 ||
-      teacher.size(-1) > ENTRIES_MAX)
-    refuse(what, ": teacher logits must be [..., K] with the logits' leading shape and 1 <= K <= ", ENTRIES_MAX,
+      teacher.size(-1) > DET_HEAD_ENTRIES_MAX)
+    refuse(what, ": teacher logits must be [..., K] with the logits' leading shape and 1 <= K <= ", DET_HEAD_ENTRIES_MAX,
            " (got ", teacher.sizes(), ")");
   check_index(index, teacher.sizes(), z, "the teacher's indices", what);
 }
@@ -456,9 +454,9 @@ Tensor distill_backward(const Tensor& logits, const Tensor& index, const Tensor&
   check_temperature(T, what);
   const int64_t V = logits.size(-1), N = logits.numel() / V;
   check_stat(stat, N, logits, what);
-  if (q.dim() != 2 || q.size(0) != N || q.size(1) < 1 || q.size(1) > ENTRIES_MAX || q.scalar_type() != at::kFloat ||
+  if (q.dim() != 2 || q.size(0) != N || q.size(1) < 1 || q.size(1) > DET_HEAD_ENTRIES_MAX || q.scalar_type() != at::kFloat ||
       q.device() != logits.device())
-    refuse(what, ": q must be float32 [", N, ", K] with 1 <= K <= ", ENTRIES_MAX, " on the logits' device");
+    refuse(what, ": q must be float32 [", N, ", K] with 1 <= K <= ", DET_HEAD_ENTRIES_MAX, " on the logits' device");
   const int64_t K = q.size(1);
   check_index(index, with_last(lead_of(logits), K), logits, "the teacher's indices", what);
   on_gpu(logits, what, "logits");

@@ -412,6 +412,8 @@ int32_t* det_device_status_word(void);
  */
 #define DET_ROWS_MAX ((int64_t)1 << 22)
 #define DET_HEAD_V_MAX ((int64_t)1 << 24)
+#define DET_HEAD_TOP_MAX 64      /* alternatives per row */
+#define DET_HEAD_ENTRIES_MAX 1024 /* teacher entries per row */
 #define DET_NORM_C_MAX ((int64_t)32768)
 #define DET_NORM_SHARD_ROWS 64
 
@@ -471,7 +473,7 @@ det_status det_layer_norm_grad(det_dtype x_dt, const void* x, int64_t s_x, det_d
  *   scale             1 / temperature, in [1e-6, 1e6)
  *   target            [N], s_target apart (null: no logprob); `ignore` gives
  *                     the log probability 0, any other value outside [0, V) NaN
- *   top               0..64, at most V; ordered by value, ties by lower index
+ *   top               0..DET_HEAD_TOP_MAX, at most V; ordered by value, ties by lower index
  *   logprob, entropy  [N] fp32; entropy may be null, logprob without targets
  *   stat              [N][4] fp32, 16-byte aligned: the maximum, 1 / S, log2 S
  *                     (S = sum 2^(scale log2e (z - max))) and the entropy
@@ -517,7 +519,7 @@ det_status det_token_logprobs_grad(det_dtype dt, const void* z, int64_t s_row, i
  *                     without probability are not read as indices; any other
  *                     outside [0, V) makes the row's loss NaN and leaves it
  *                     without a gradient
- *   K                 1..1024; an index may occur more than once
+ *   K                 1..DET_HEAD_ENTRIES_MAX; an index may occur more than once
  *   loss              [N] fp32;  stat: [N][4] as above
  *   q                 [N][K] fp32, 0 throughout in a row without a gradient
  *                     for want of an entry or for an invalid one
