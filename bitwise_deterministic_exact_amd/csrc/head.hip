@@ -894,10 +894,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_score_grad(GradArgs a) {
 
 // Four-wave workgroups per row.  One, which also finishes the row, when the
 // rows alone give every CU about three workgroups, or when the row is so short
-// that its four waves are through before a second launch would be (that costs
-// 3 to 4 us): 500 x 50257 fp32 20.1 us in one workgroup, 23.5 in two and a
-// join; 500 x 131072 48 in two.  Otherwise enough for four to a CU, at most
-// one for every four chunks, and with alternatives at most 16 (64 lists to join).
+// that its four waves are through before a join would be.  Otherwise enough for
+// four to a CU, at most one for every four chunks, and with alternatives at
+// most 16 (64 lists to join).  Kernels alone, us, in one workgroup and shared:
+//   rows   50257 fp32     131072 fp32    131072 bf16    50257 bf16, top 20
+//   300    18.1  18.0     32.3  31.9     29.1  21.1     34.1  33.2
+//   500    21.8  23.8     46.0  48.2     31.4  29.9     36.5  41.6
+//   767    30.5  32.2     66.6  66.1     38.9  41.2     41.4  50.0
+//   1000   37.2  39.7     83.9  83.8     48.2  52.4     46.0  55.9
+// Of 1 .. 1000 rows of 5000 .. 131072 logits, fp32 and bf16, with 20
+// alternatives and without, this rule and many_waves are within 11 % of the best of one,
+// two or as many workgroups as here and of 16 waves, except at 1 and 16 x 50257
+// fp32 (8.1 and 9.1 us, shared 6.6 and 7.3), 256 rows and less of 5000 with
+// alternatives (14, 16 waves 12), 500 x 131072 bf16 top 20 (59, two workgroups
+// 50), 300 x 50257 fp32 top 20 (35, two 31), 384 x 131072 fp32 top 20 (61, two
+// 54) and 128 x 131072 bf16 (14.6, shared by 16 12.8).
 constexpr int SHARED_MAX = 16;
 int blocks_per_row(int64_t N, int64_t nchunk, int top) {
   const int64_t turns = ceil_div(nchunk, WAVES);              // chunks a wave of one workgroup takes
@@ -913,12 +924,14 @@ int grad_blocks_per_row(int64_t N, int64_t nchunk) {
 }
 
 // One workgroup of 16 waves to a row instead, in one launch, for rows of more
-// than four chunks that they pass in at most two turns: 1 x 32000 fp32 6.5 us
-// (one workgroup of four waves 7.3), 1 x 50257 7.9 (four-wave workgroups and a
-// join 10.3).  With alternatives, whose search keeps a CU's four SIMDs busy, in
-// one turn (64 x 16000 bf16 top 10 12.5 us against 15.1, but 64 x 50257 16.5
-// against 15.4).  From 128 rows on, in up to eight turns: the other CUs have
-// rows of their own (200 x 131072 fp32 20.0 against 22.2).
+// than four chunks that they pass in at most two turns: 1 x 32000 fp32 6.7 us
+// (one workgroup of four waves 9.0, several and a join 6.4), 200 x 17000 7.0
+// (8.9, 9.5).  The second launch also costs the host: 1 x 50257, called and not
+// replayed from a graph, 7.9 against 10.3.  With alternatives, whose search
+// keeps a CU's four SIMDs busy, in one turn (64 x 17000 bf16 top 20 16.3, 21.3,
+// 17.0; 64 x 50257 20.5 against 19.4 shared).  From 128 rows on, in up to eight
+// turns: the other CUs have rows of their own (200 x 131072 fp32 22.5, 29.9,
+// 24.2).
 constexpr int MANY = 16;
 bool many_waves(int64_t N, int64_t nchunk, int top) {
   return N <= 256 && nchunk > WAVES && nchunk <= (N >= 128 ? 8 * MANY : top > 0 ? MANY : 2 * MANY);

@@ -332,7 +332,9 @@ __global__ __launch_bounds__(MAXT, 4) void k_norm_grad(NormGradArgs a) {
     some |= at[s].own > 0;
   }
   const bool ragged = __ballot(some) != 0;                    // uniform: the wave holds others' elements
-  // the last rows first: they are what the forward pass left in the memory-side cache
+  // the last rows first: they are what the forward pass left in the memory-side
+  // cache (with it 16384 x 8192 bf16 282 us, the first rows first 289; 8192 x 4096
+  // fp32 140 and 145)
   const int64_t chunk = gridDim.x - 1 - blockIdx.x;
   const int64_t row0 = chunk * a.chunk;
   const int rows = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.N - row0));
@@ -801,8 +803,13 @@ void launch_norm(NormArgs a, hipStream_t s) {
 template <int XT, int YT, int S, int W, int MAXT, bool SHORT = false>
 void launch_norm_grad(NormGradArgs a, hipStream_t s) {
   a.T = SHORT ? lanes_of(a.C, S, W) : threads_of(a.C, S, W);
-  // twice the rows at a time for few long rows: 1021 x 1537 fp32 15.5 -> 13.3 us, but
-  // 32768 x 1024 bf16 52 -> 59; short rows at most one chunk's
+  // Rows at a time: 1024 threads' from 1025 columns on, 512 up to there; short
+  // rows at most one chunk's.  The number of rows may not decide, for the order
+  // of dw's sums follows.  With half of that from 1025 columns on, few rows
+  // wait longer and many wait less: 1021 x 1537 fp32 15.6 -> 17.2 us, 100 x 3000
+  // bf16 16.6 -> 23.1, 1021 x 4096 28.4 both ways, but 32768 x 1025 bf16 90.8 ->
+  // 79.1, 8192 x 2048 30.6 -> 29.1, 32768 x 3000 146.7 -> 154.5.  With twice up to 1024
+  // columns the same: 1021 x 768 fp32 11.8 -> 11.0, 32768 x 1024 bf16 53.3 -> 62.0.
   a.G = std::max(1, std::min(SHORT ? chunk_rows(SHORT_C) : 8, (a.C > 1024 ? 1024 : 512) / a.T));
   a.chunk = chunk_rows(a.C);
   const size_t lds = a.G > 1 && a.parts != nullptr ? static_cast<size_t>(a.G) * a.T * S * W * 2 * sizeof(float) : 0;
