@@ -19,6 +19,7 @@ K_MAX = 1 << 19
 # of the head operators, for what Python itself checks; the header has them all
 NORM_C_MAX = 32768
 NORM_SHARD_ROWS = 64
+GATED_MAX = 65536
 
 _lib = None
 _ops = None
@@ -72,6 +73,14 @@ def load() -> ctypes.CDLL:
                          ctypes.c_size_t, vp], c_int),
         "det_distill_grad": ([c_int, vp, i64, i64, i64, ctypes.c_double, vp, i64, i64, vp, vp, vp, i64, vp, i64, vp],
                              c_int),
+        "det_gated_linear_workspace_bytes": ([i64, i64, i64, c_int, c_int], i64),
+        "det_gated_linear": ([vp, i64, vp, i64, vp, i64, i64, i64, i64, c_int, c_int, vp, c_int, vp, vp, vp, vp, vp,
+                              ctypes.c_size_t, vp], c_int),
+        "det_gated_linear_grad_workspace_bytes": ([i64, i64, i64, c_int, c_int], i64),
+        "det_gated_linear_grad": ([c_int, vp, i64, vp, i64, vp, vp, i64, vp, i64, c_int, vp, vp, vp, vp, i64, i64,
+                                   i64, c_int, vp, vp, vp, vp, ctypes.c_size_t, vp], c_int),
+        "det_int8_pack": ([c_int, vp, i64, i64, i64, vp, vp, vp], c_int),
+        "det_int8_unpack": ([vp, i64, vp, i64, i64, c_int, vp, vp], c_int),
         "det_set_gemm_path": ([c_int, c_int], c_int),
         "det_set_kernel_events": ([vp, vp], None),
         "det_device_status": ([vp, c_int, ctypes.POINTER(c_int)], c_int),

@@ -9,14 +9,14 @@ import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", f) for f in ("detgemm.hip", "head.hip", "norm.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("detgemm.hip", "head.hip", "norm.hip", "gated.hip", "int8_block.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdetgemm.so")
 # the benchmark's LDS-atomic peak probe: its own library, never loaded by the package
 PROBE_SOURCES = [os.path.join(PKG, "csrc", "lds_probe.hip")]
 PROBE_LIB = os.path.join(PKG, "liblds_probe.so")
-# the torch side of the head operators (autograd, streams): host code only
-OPS_SOURCE = os.path.join(PKG, "csrc", "head_ops.cpp")
+# the torch side of the operators (autograd, streams): host code only
+OPS_SOURCES = [os.path.join(PKG, "csrc", f) for f in ("head_ops.cpp", "block_ops.cpp")]
 OPS_LIB = os.path.join(PKG, "_ops.so")
 ARCH = "gfx950"
 
@@ -50,18 +50,30 @@ def _hipcc(sources, out: str, verbose: bool) -> str:
 
 def _host_ops(verbose: bool) -> str:
     """Compile the torch extension module against libdetgemm.so (which must
-    be built) and the installed torch."""
+    be built) and the installed torch, its sources side by side."""
     from torch.utils.cpp_extension import include_paths, library_paths
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
-           *[f"-I{p}" for p in (INCLUDE, *include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"])],
-           "-o", OPS_LIB + ".tmp", OPS_SOURCE, f"-L{PKG}", "-l:libdetgemm.so",
-           *[f"-L{p}" for p in library_paths()], "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
-           "-Wl,-rpath,$ORIGIN"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stderr}")
+    flags = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+             *[f"-I{p}" for p in (INCLUDE, *include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"])]]
+    objects = [f"{OPS_LIB}.{i}.o" for i in range(len(OPS_SOURCES))]
+    cmds = [["g++", *flags, "-c", "-o", o, src] for o, src in zip(objects, OPS_SOURCES)]
+    link = ["g++", "-shared", "-o", OPS_LIB + ".tmp", *objects, f"-L{PKG}", "-l:libdetgemm.so",
+            *[f"-L{p}" for p in library_paths()], "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+            "-Wl,-rpath,$ORIGIN"]
+    try:
+        for batch in (cmds, [link]):
+            procs = []
+            for cmd in batch:
+                if verbose:
+                    print(" ".join(cmd), flush=True)
+                procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+            outs = [p.communicate()[0] for p in procs]
+            for p, out in zip(procs, outs):
+                if p.returncode != 0:
+                    raise RuntimeError(f"g++ failed ({p.returncode}):\n{out}")
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(OPS_LIB + ".tmp", OPS_LIB)
     return OPS_LIB
 

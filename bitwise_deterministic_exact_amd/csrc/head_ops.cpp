@@ -6,78 +6,13 @@
 // step on small inputs too, where the time of a call is the host's: marshalled
 // from Python (ctypes, torch.autograd.Function) a forward and backward pass
 // took 150 us of host time on [512, 1000] logits.
-#include <ATen/ATen.h>
-#include <c10/core/AutogradState.h>
-#include <c10/core/DeviceGuard.h>
-#include <c10/core/impl/LocalDispatchKeySet.h>
-#include <c10/core/impl/TorchDispatchModeTLS.h>
-#include <c10/hip/HIPStream.h>
-#include <torch/csrc/autograd/custom_function.h>
-#include <torch/csrc/autograd/functions/basic_ops.h>
-#include <torch/csrc/autograd/functions/utils.h>
-#include <torch/csrc/jit/frontend/tracer.h>
-#include <torch/csrc/utils/pybind.h>
+#include "ops_common.h"
 
-#include <optional>
-#include <sstream>
-#include <string>
-#include <tuple>
-
-#include "detgemm.h"
-
-namespace py = pybind11;
-using at::Tensor;
-using c10::ScalarType;
-using torch::autograd::AutogradContext;
-using torch::autograd::variable_list;
-using OptTensor = std::optional<Tensor>;
+void bind_block(py::module_& m);          // block_ops.cpp
 
 namespace {
 
-// ---------------------------------------------------------------- checks
-
-template <class... A>
-[[noreturn]] void refuse(const A&... parts) {
-  std::ostringstream s;
-  (s << ... << parts);
-  throw py::value_error(s.str());
-}
-
-bool known(ScalarType t) { return t == at::kFloat || t == at::kBFloat16; }
-det_dtype dt_of(ScalarType t) { return t == at::kFloat ? DET_F32 : DET_BF16; }
-
-void on_gpu(const Tensor& t, const char* what, const char* name) {
-  if (!t.is_cuda()) refuse(what, ": ", name, " must be on a GPU");
-}
-
-void* stream_of(const Tensor& t) {
-  return static_cast<void*>(c10::hip::getCurrentHIPStream(t.get_device()).stream());
-}
-
-// the library's status as the exceptions the rest of the package raises: bad
-// arguments are ValueError, a HIP failure is DetGemmError
-struct HipFailure : std::runtime_error {
-  using std::runtime_error::runtime_error;
-};
 PyObject* g_hip_error = nullptr;               // the package's DetGemmError, held by the module
-
-void ok(det_status st) {
-  if (st == DET_OK) return;
-  if (st == DET_EHIP) throw HipFailure(det_last_error());
-  throw py::value_error(det_last_error());
-}
-
-const void* in(const Tensor& t) { return t.const_data_ptr(); }
-const void* in(const OptTensor& t) { return t ? t->const_data_ptr() : nullptr; }
-template <class T>
-T* out(const Tensor& t) { return t.defined() ? static_cast<T*>(t.mutable_data_ptr()) : nullptr; }
-
-// [..., C] as [N, C] rows with adjacent elements: a copy only when one stride
-// cannot describe the rows, or a row's elements are apart
-Tensor rows(const Tensor& t) {
-  Tensor r = t.dim() == 2 ? t : t.reshape({t.numel() / t.size(-1), t.size(-1)});
-  return r.size(1) <= 1 || r.stride(1) == 1 ? r : r.contiguous();
-}
 
 // an incoming gradient over the flattened rows and its stride; one broadcast
 // value stays one value
@@ -91,43 +26,6 @@ std::pair<Tensor, int64_t> grad_rows(const Tensor& g, at::IntArrayRef lead, cons
   if (one) return {g, 0};
   return {g.contiguous(), 1};
 }
-
-// Gradients of gradients are not formed.  A backward pass that is itself
-// recorded (create_graph) gives gradients whose node refuses to run; it has
-// edges to everything they depend on, the saved inputs and the incoming
-// gradients, so that a derivative through any of these reaches it, also where
-// it is asked for one input alone.  Torch's own DelayedError hangs on the
-// results only: grad(loss + g.pow(2).sum(), x) would leave it out and return
-// the first-order terms.
-variable_list once(variable_list grads, const variable_list& sources, const char* name) {
-  if (!at::GradMode::is_enabled()) return grads;
-  const auto refusal = std::make_shared<torch::autograd::Error>(
-      std::string(name) + " is differentiable once",
-      torch::autograd::collect_next_edges(at::ArrayRef<Tensor>(sources)));
-  for (auto& g : grads)
-    if (g.defined()) torch::autograd::set_history(g, refusal);
-  return grads;
-}
-
-// A trace (torch.jit.trace, make_fx) sees the allocations of the results but
-// not what fills them: the traced function would return whatever lies there.
-// So a call that is being traced is refused.
-void not_traced(const char* what) {
-  using c10::impl::TorchDispatchModeKey;
-  if (torch::jit::tracer::isTracing() || c10::impl::TorchDispatchModeTLS::get_mode(TorchDispatchModeKey::PROXY) ||
-      c10::impl::tls_is_dispatch_key_included(c10::DispatchKey::PreDispatch))
-    throw std::runtime_error(std::string(what) + " cannot be traced: its kernels are not torch operators");
-}
-
-// Forward-mode derivatives are not formed: a result without its tangent would pass
-// for a constant, so inputs and incoming gradients that carry one are refused.
-void no_tangent(const OptTensor& t, const char* what) {
-  if (t && t->defined() && t->_fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
-    throw std::runtime_error(std::string(what) + " forms no forward-mode derivatives");
-}
-
-bool wants_grad(const Tensor& t) { return t.defined() && t.requires_grad(); }
-bool wants_grad(const OptTensor& t) { return t && t->requires_grad(); }
 
 // ---------------------------------------------------------------- layer norm
 
@@ -280,13 +178,6 @@ void check_stat(const Tensor& stat, int64_t N, const Tensor& like, const char* w
   if (stat.dim() != 2 || stat.size(0) != N || stat.size(1) != 4 || stat.scalar_type() != at::kFloat ||
       stat.device() != like.device())
     refuse(what, ": stat must be float32 [", N, ", 4] on the logits' device");
-}
-
-at::IntArrayRef lead_of(const Tensor& t) { return t.sizes().slice(0, t.dim() - 1); }
-std::vector<int64_t> with_last(at::IntArrayRef lead, int64_t n) {
-  std::vector<int64_t> s(lead.begin(), lead.end());
-  s.push_back(n);
-  return s;
 }
 
 struct Scores {
@@ -498,8 +389,6 @@ Tensor distill_loss(const Tensor& logits, const Tensor& teacher, const Tensor& i
   return distill_forward(logits, teacher, index, T).loss;
 }
 
-OptTensor opt(const Tensor& t) { return t.defined() ? OptTensor(t) : std::nullopt; }
-
 }  // namespace
 
 PYBIND11_MODULE(_ops, m) {
@@ -507,7 +396,7 @@ PYBIND11_MODULE(_ops, m) {
   py::register_exception_translator([](std::exception_ptr p) {
     try {
       if (p) std::rethrow_exception(p);
-    } catch (const HipFailure& e) {
+    } catch (const detops::HipFailure& e) {
       PyErr_SetString(g_hip_error, e.what());
     }
   });
@@ -535,4 +424,5 @@ PYBIND11_MODULE(_ops, m) {
     return std::make_tuple(r.loss, r.stat, r.q);
   }, release());
   m.def("distill_backward", &distill_backward, release());
+  bind_block(m);
 }

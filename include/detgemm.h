@@ -543,6 +543,94 @@ det_status det_distill_grad(det_dtype dt, const void* z, int64_t s_row, int64_t 
                             const int64_t* entry, int64_t s_entry, int64_t K, const float* stat, const float* q,
                             const float* g, int64_t s_g, void* dz, int64_t s_dz, void* stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * The gated projection between a norm and a DetLinear, activations kept in 8
+ * bits for the backward pass, and the losses of post-training on token log
+ * probabilities.  As above, every result is a fixed function of its inputs: a
+ * row's results depend on that row (and the weights) alone, repetition gives
+ * the same bits, no floating-point atomics are used.
+ */
+#define DET_GATED_MAX ((int64_t)65536)
+#define DET_INT8_NAN (-128)      /* the exponent byte of a block that was not finite */
+
+typedef enum { DET_ACT_SILU = 0, DET_ACT_GELU = 1, DET_ACT_GELU_TANH = 2 } det_activation;
+/* what the forward call keeps of both projections: nothing, bf16, 8-bit blocks */
+typedef enum { DET_SAVE_NONE = 0, DET_SAVE_BF16 = 1, DET_SAVE_INT8 = 2 } det_save;
+
+/*
+ * det_gated_linear -- h = act(g) u with g = x w_gate^T and u = x w_up^T.
+ *   x                 [N] rows of C bf16, s_x apart
+ *   w_gate, w_up      [F] rows of C bf16, s_gate and s_up apart
+ *   act               silu g / (1 + e^-g); gelu g Phi(g); gelu_tanh
+ *                     0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
+ *   h                 [N][F] contiguous of type h_dt
+ *   save              what gate and up ([N][F] contiguous) get: nothing (null
+ *                     pointers), g and u in bf16, or int8 codes whose blocks'
+ *                     exponents go to gate_exp and up_exp [N][ceil(F / 32)]
+ *                     (the format of det_int8_pack)
+ *   workspace         det_gated_linear_workspace_bytes(N, C, F, save, aligned),
+ *                     256-byte aligned; `aligned`: x and both weights start at
+ *                     multiples of 16 bytes and their strides are multiples of
+ *                     8 in [C, 2^22]
+ * g and u are fp32 sums over k in one fixed order (matrix-core products of 32 k
+ * each, ascending), h is rounded once; values that are not finite take part as
+ * IEEE arithmetic has it.  N <= 2^22, C and F <= 65536.
+ * Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
+ */
+int64_t det_gated_linear_workspace_bytes(int64_t N, int64_t C, int64_t F, det_save save, int aligned);
+
+det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int64_t s_gate, const void* w_up,
+                            int64_t s_up, int64_t N, int64_t C, int64_t F, det_activation act, det_dtype h_dt, void* h,
+                            det_save save, void* gate, void* up, int8_t* gate_exp, int8_t* up_exp, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * det_gated_linear_grad -- the gradients of det_gated_linear.  With dg = dh u
+ * act'(g) and du = dh act(g), formed in fp32 from the saved g and u and rounded
+ * to bf16:
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ *   dh                [N] rows of F of type dh_dt, s_dh apart
+ *   x, x_exp          as the forward call read x (x_exp null), or its int8 codes
+ *                     (rows s_x apart) and exponents [N][ceil(C / 32)]
+ *   save, gate, up, gate_exp, up_exp   as the forward call wrote them
+ *   dx                [N][C] bf16 contiguous; null: not needed
+ *   dw_gate, dw_up    [F][C] bf16 contiguous; both null: not needed
+ *   workspace         det_gated_linear_grad_workspace_bytes(N, C, F, dx != null,
+ *                     dw_gate != null), 256-byte aligned
+ * Each gradient is an fp32 sum in one fixed order, rounded once: dx over the
+ * features of the gate, then of up; the weights' over the rows in ascending
+ * order, so these depend on how rows are cut into calls.
+ */
+int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, int need_dx, int need_dw);
+
+det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, const void* x, int64_t s_x,
+                                 const int8_t* x_exp, const void* w_gate, int64_t s_gate, const void* w_up,
+                                 int64_t s_up, det_save save, const void* gate, const void* up, const int8_t* gate_exp,
+                                 const int8_t* up_exp, int64_t N, int64_t C, int64_t F, det_activation act, void* dx,
+                                 void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * det_int8_pack -- rows in 8 bits: 32 consecutive elements of a row (the last
+ * block may be shorter) share a power of two 2^e, the least with the largest
+ * magnitude below 127.5 2^e, e in [-126, 121]; code = x 2^-e to nearest, ties to
+ * even, within +-127.  A value is off by at most 2^e / 2 (2^e above 127.5 2^121).
+ * A block with a NaN or an infinity gets the exponent DET_INT8_NAN and is noted
+ * in the device status ("non-finite").
+ *   x                 [N] rows of C of type dt, s_x apart
+ *   codes             [N][C] int8 contiguous
+ *   exps              [N][ceil(C / 32)] contiguous
+ * det_int8_unpack -- y = code 2^e, exact in fp32 and in bf16; NaN throughout a
+ * block of exponent DET_INT8_NAN.
+ *   codes             [N] rows of C, s_codes apart; y [N][C] of type dt
+ * N <= 2^31, C <= 2^24.  Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
+ */
+det_status det_int8_pack(det_dtype dt, const void* x, int64_t s_x, int64_t N, int64_t C, int8_t* codes, int8_t* exps,
+                         void* stream);
+
+det_status det_int8_unpack(const int8_t* codes, int64_t s_codes, const int8_t* exps, int64_t N, int64_t C,
+                           det_dtype dt, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,324 @@
+"""The gated projection on the GPU: products bit for bit on integers, h and the
+gradients against 64 bits, batch independence, layouts, checkpoints in 8 bits,
+differences, streams and graph replays."""
+import math
+
+import pytest
+import torch
+
+import bitwise_deterministic_exact_amd as det
+from tests.gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+# a rounding is off by at most half a step of the value
+U = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+# fp32 sums of n products: at most this relative to the sum of their magnitudes,
+# one rounding (of either kind, so a whole step) per addition
+def sum_bound(n):
+    return (n + 2) * 2.0 ** -23
+
+
+ACTS = ("silu", "gelu", "gelu_tanh")
+# few tokens (16, 32 and 64 at a time), tiles of 128 (ragged both ways, one and many steps of k, odd widths),
+# tiles of 256 (ragged both ways)
+SIZES = [(1, 64, 16), (1, 31, 1), (3, 1, 5), (16, 32, 33), (17, 100, 64), (33, 257, 130), (64, 192, 48), (48, 2048, 96),
+         (65, 64, 64), (130, 128, 100), (129, 100, 257), (300, 512, 31), (200, 65, 200), (4100, 64, 2100),
+         (2100, 192, 4099)]
+
+
+def integers(g, *shape, top=3):
+    return torch.randint(-top, top + 1, shape, generator=g, device=DEV).to(BF16)
+
+
+def operands(seed, N, C, F, normal=True):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    if not normal:
+        return integers(g, N, C), integers(g, F, C), integers(g, F, C)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    return r(N, C).to(BF16), (r(F, C) / math.sqrt(C)).to(BF16), (r(F, C) / math.sqrt(C)).to(BF16)
+
+
+def act64(kind, g):
+    if kind == "silu":
+        return torch.nn.functional.silu(g)
+    return torch.nn.functional.gelu(g, approximate="none" if kind == "gelu" else "tanh")
+
+
+def slope64(kind, g):
+    g = g.detach().requires_grad_(True)
+    return torch.autograd.grad(act64(kind, g).sum(), g)[0]
+
+
+def within(got, want, bound, what):
+    bad = ~((got.double() - want).abs() <= bound)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, worst "
+                           f"{((got.double() - want).abs() / bound.clamp(min=1e-300)).max().item():.3g} of the bound")
+
+
+@pytest.mark.parametrize("N,C,F", SIZES)
+def test_products_are_exact_on_integers(N, C, F):
+    # every partial sum is an integer below 2^24: g and u have to be exact
+    announce(f"gated integers {N} {C} {F}")
+    x, wg, wu = operands(1, N, C, F, normal=False)
+    _, s = det.gated_linear_forward(x, wg, wu)
+    for got, w in ((s.gate, wg), (s.up, wu)):
+        want = (x.double() @ w.double().t()).to(F32)           # an integer below 2^24: exact
+        assert torch.equal(got, want.to(BF16))
+    # the same products where nothing is kept (few tokens take another kernel): act(g) ~ g from 32 on is g
+    one = torch.zeros(F, C, device=DEV, dtype=BF16)
+    one[:, 0] = 64.0
+    x[:, 0] = 1.0
+    h = det.gated_linear(x, one, wu, out_dtype=F32)
+    assert torch.equal(h, 64.0 * (x.double() @ wu.double().t()).to(F32))
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("N,C,F", SIZES)
+def test_forward_against_64_bits(N, C, F, act, out):
+    announce(f"gated forward {N} {C} {F} {act} {out}")
+    x, wg, wu = operands(2, N, C, F)
+    X, G, W = x.double(), wg.double(), wu.double()
+    g, u = X @ G.t(), X @ W.t()
+    eg, eu = (sum_bound(C) * (X.abs() @ w.abs().t()) for w in (G, W))
+    a = act64(act, g)
+    # |act'| <= 1.13; the activation and the product round a few times in 32 bits (8 half steps),
+    # in the exponent too (another |g| of them)
+    ea = 1.2 * eg + (8 + g.abs()) * U[F32] * a.abs() + 1e-37
+    bound = ea * (u.abs() + eu) + a.abs() * eu + U[out] * (a * u).abs() * 1.01 + 1e-37
+    h = det.gated_linear(x, wg, wu, activation=act, out_dtype=out)
+    assert h.dtype == out
+    within(h, a * u, bound, "h")
+    kept, _ = det.gated_linear_forward(x, wg, wu, activation=act, out_dtype=out)
+    assert torch.equal(h, kept)
+
+
+def reference_grads(act, dh, x, wg, wu, g, u):
+    """(value, bound) of dx, dw_gate, dw_up in 64 bits from the g and u that the gradient reads."""
+    D, X, G, W = dh.double(), x.double(), wg.double(), wu.double()
+    a, s = act64(act, g), slope64(act, g)
+    dg, du = D * u * s, D * a
+    # formed in 32 bits (8 half steps; the slope's parts may cancel: 8 of their sizes, |g| in the exponent), rounded to bf16
+    eg = U[BF16] * dg.abs() * 1.01 + (8 + g.abs()) * U[F32] * (D * u).abs() * (1 + g.abs())
+    eu = U[BF16] * du.abs() * 1.01 + (8 + g.abs()) * U[F32] * (D * g).abs()
+    ag, au = dg.abs() + eg, du.abs() + eu
+    out = []
+    N, F = g.shape
+    dx = dg @ G + du @ W
+    out.append((dx, eg @ G.abs() + eu @ W.abs() + sum_bound(2 * F + 64) * (ag @ G.abs() + au @ W.abs()) + U[BF16] * dx.abs()))
+    for d, e, m in ((dg, eg, ag), (du, eu, au)):
+        w = d.t() @ X
+        out.append((w, e.t() @ X.abs() + sum_bound(N + 64) * (m.t() @ X.abs()) + U[BF16] * w.abs()))
+    return out
+
+
+@pytest.mark.parametrize("act,dtype", [("silu", BF16), ("gelu", F32), ("gelu_tanh", BF16)])
+@pytest.mark.parametrize("N,C,F", SIZES)
+def test_gradients_against_64_bits(N, C, F, act, dtype):
+    announce(f"gated gradients {N} {C} {F} {act} {dtype}")
+    x, wg, wu = operands(3, N, C, F)
+    dh = torch.randn(N, F, device=DEV, generator=torch.Generator(device=DEV).manual_seed(4)).to(dtype)
+    h, s = det.gated_linear_forward(x, wg, wu, activation=act, out_dtype=dtype)
+    got = det.gated_linear_backward(dh, x, wg, wu, s, activation=act)
+    want = reference_grads(act, dh, x, wg, wu, s.gate.double(), s.up.double())
+    for name, t, (v, b) in zip(("dx", "dw_gate", "dw_up"), got, want):
+        assert t.dtype == BF16
+        within(t, v, b + 1e-37, name)
+    # each alone, and through autograd: the same bits
+    assert torch.equal(det.gated_linear_backward(dh, x, wg, wu, s, activation=act, need_dw=False)[0], got[0])
+    only = det.gated_linear_backward(dh, x, wg, wu, s, activation=act, need_dx=False)
+    assert only[0] is None and torch.equal(only[1], got[1]) and torch.equal(only[2], got[2])
+    leaves = [t.clone().requires_grad_(True) for t in (x, wg, wu)]
+    again = det.gated_linear(*leaves, activation=act, out_dtype=dtype)
+    assert torch.equal(again.detach(), h)
+    for a, b in zip(torch.autograd.grad(again, leaves, dh), got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("N,C,F", [(1, 31, 1), (17, 100, 64), (130, 128, 100), (300, 96, 33), (4100, 64, 2100)])
+def test_int8_checkpoint(N, C, F):
+    announce(f"gated int8 {N} {C} {F}")
+    # integers: g and u are exact, and so are their codes
+    x, wg, wu = operands(5, N, C, F, normal=False)
+    _, s = det.gated_linear_forward(x, wg, wu, checkpoint="int8")
+    for packed, w in ((s.gate, wg), (s.up, wu)):
+        want = det.pack_int8((x.double() @ w.double().t()).to(F32))
+        assert torch.equal(packed.codes, want.codes) and torch.equal(packed.exponents, want.exponents)
+    x, wg, wu = operands(6, N, C, F)
+    dh = torch.randn(N, F, device=DEV, generator=torch.Generator(device=DEV).manual_seed(7)).to(BF16)
+    h, s = det.gated_linear_forward(x, wg, wu, checkpoint="int8")
+    assert torch.equal(h, det.gated_linear_forward(x, wg, wu)[0])
+    px = det.pack_int8(x)
+    got = det.gated_linear_backward(dh, px, wg, wu, s)
+    values = [det.unpack_int8(t).double() for t in (px, s.gate, s.up)]
+    for name, t, (v, b) in zip(("dx", "dw_gate", "dw_up"), got,
+                               reference_grads("silu", dh, values[0], wg, wu, values[1], values[2])):
+        within(t, v, b + 1e-37, name)
+    # what autograd does: the same, and the saved tensors are the 8-bit ones
+    leaves = [t.clone().requires_grad_(True) for t in (x, wg, wu)]
+    sizes = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (sizes.append((t.dtype, t.numel())), t)[1], lambda t: t):
+        again = det.gated_linear(*leaves, checkpoint="int8")
+    kept = sum(n for d, n in sizes if d == torch.int8)
+    assert kept == N * (C + 2 * F) + N * ((C + 31) // 32 + 2 * ((F + 31) // 32))
+    assert sum(n for d, n in sizes if d != torch.int8) == 2 * F * C        # the weights
+    for a, b in zip(torch.autograd.grad(again, leaves, dh), got):
+        assert torch.equal(a, b)
+    # a packed x with bfloat16 projections, too
+    _, sb = det.gated_linear_forward(x, wg, wu)
+    mixed = det.gated_linear_backward(dh, px, wg, wu, sb)
+    plain = det.gated_linear_backward(dh, x, wg, wu, sb)
+    assert torch.equal(mixed[0], plain[0])
+    full = det.gated_linear_backward(dh, det.unpack_int8(px, BF16), wg, wu, sb)
+    assert torch.equal(mixed[1], full[1]) and torch.equal(mixed[2], full[2])
+
+
+@pytest.mark.parametrize("C,F", [(64, 2100), (100, 70), (192, 4099)])
+def test_a_token_is_the_same_in_any_batch(C, F):
+    # few tokens, tiles of 128 and of 256 rows: one chain of sums
+    x, wg, wu = operands(8, 4100, C, F)
+    dh = torch.randn(4100, F, device=DEV, generator=torch.Generator(device=DEV).manual_seed(9))
+    h, s = det.gated_linear_forward(x, wg, wu, out_dtype=F32)
+    dx = det.gated_linear_backward(dh, x, wg, wu, s, need_dw=False)[0]
+    for a, b in ((0, 1), (4099, 4100), (5, 21), (100, 164), (64, 193), (1000, 1700)):
+        part, t = det.gated_linear_forward(x[a:b], wg, wu, out_dtype=F32)
+        assert torch.equal(part, h[a:b])
+        assert torch.equal(det.gated_linear(x[a:b], wg, wu, out_dtype=F32), h[a:b])
+        assert torch.equal(det.gated_linear_backward(dh[a:b], x[a:b], wg, wu, t, need_dw=False)[0], dx[a:b])
+
+
+@pytest.mark.parametrize("N", [3, 70, 300])
+@pytest.mark.parametrize("C", [64, 100, 128])
+def test_layouts(N, C):
+    F = 65
+    x, wg, wu = operands(10, N, C, F)
+    h, s = det.gated_linear_forward(x, wg, wu)
+    dh = torch.randn(N, F, device=DEV).to(BF16)
+    want = det.gated_linear_backward(dh, x, wg, wu, s)
+    room = lambda t, off, pad: torch.zeros(t.shape[0], t.shape[1] + pad, device=DEV, dtype=t.dtype)[:, off:off + t.shape[1]].copy_(t)
+    views = [(room(x, 1, 3), room(wg, 8, 16), room(wu, 2, 2)), (room(x, 8, 8), room(wg, 0, 8), wu),
+             (x.t().contiguous().t(), wg.t().contiguous().t(), room(wu, 8, 24))]
+    for v in views:
+        h2, s2 = det.gated_linear_forward(*v)
+        assert torch.equal(h2, h) and torch.equal(det.gated_linear(*v), h)
+        for d in (dh, room(dh, 3, 4), dh.t().contiguous().t()):
+            for a, b in zip(det.gated_linear_backward(d, *v, s2), want):
+                assert torch.equal(a, b)
+    # one row repeated, leading dimensions, a gradient that is one value
+    e = x[:1].expand(N, C)
+    assert torch.equal(det.gated_linear(e, wg, wu), det.gated_linear(x[:1], wg, wu).expand(N, F))
+    x3 = x.reshape(N, 1, C).requires_grad_(True)
+    y = det.gated_linear(x3, wg, wu)
+    assert y.shape == (N, 1, F)
+    gx, = torch.autograd.grad(y.sum(), x3)
+    assert torch.equal(gx.reshape(N, C), det.gated_linear_backward(torch.ones_like(h), x, wg, wu, s, need_dw=False)[0])
+
+
+def test_no_rows():
+    x, wg, wu = operands(11, 4, 40, 24)
+    x = x[:0].requires_grad_(True)
+    for ck in (None, "int8"):
+        w = wg.clone().requires_grad_(True)
+        h = det.gated_linear(x, w, wu, checkpoint=ck)
+        assert h.shape == (0, 24)
+        gx, gw = torch.autograd.grad(h, (x, w), torch.empty_like(h))
+        assert gx.shape == (0, 40) and torch.equal(gw, torch.zeros_like(w))
+
+
+def test_rows_that_are_not_finite_stay_by_themselves():
+    x, wg, wu = operands(12, 200, 96, 130)
+    clean, s0 = det.gated_linear_forward(x, wg, wu, out_dtype=F32, checkpoint="int8")
+    bad = x.clone()
+    bad[3, 5], bad[70, 0], bad[199, 95] = float("nan"), float("inf"), -float("inf")
+    rows = torch.ones(200, dtype=torch.bool, device=DEV)
+    rows[[3, 70, 199]] = False
+    h, s = det.gated_linear_forward(bad, wg, wu, out_dtype=F32, checkpoint="int8")
+    assert torch.equal(h[rows], clean[rows]) and torch.isnan(h[3]).all() and not torch.isfinite(h[70]).any()
+    assert torch.equal(s.gate.codes[rows], s0.gate.codes[rows])
+    assert (s.gate.exponents[~rows] == -128).all() and (s.up.exponents[~rows] == -128).all()
+    # large arguments: the activations reach their limits
+    wide = torch.full((70, 1), 3.0e4, device=DEV, dtype=BF16)
+    one = torch.ones(8, 1, device=DEV, dtype=BF16)
+    for act in ACTS:
+        assert torch.equal(det.gated_linear(wide, one, one, activation=act), (wide * wide).expand(70, 8).to(BF16))
+        low = det.gated_linear(wide, -one, one, activation=act)
+        assert (low == 0).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_gradients_against_differences(act):
+    # f = sum(dh h) along a direction of each input; h has 32 bits, the inputs move by what bf16 holds exactly
+    N, C, F = 24, 48, 40
+    g = torch.Generator(device=DEV).manual_seed(13)
+    leaves = [(integers(g, *s, top=4).double() / 8).to(BF16).requires_grad_(True) for s in ((N, C), (F, C), (F, C))]
+    dh = torch.randn(N, F, device=DEV, generator=g)
+    grads = torch.autograd.grad(det.gated_linear(*leaves, activation=act, out_dtype=F32), leaves, dh)
+    step = 2.0 ** -6
+    for i, t in enumerate(leaves):
+        d = integers(g, *t.shape, top=1)
+        f = []
+        for sign in (1, -1):
+            moved = [l.detach() if j != i else (l.detach().double() + sign * step * d.double()).to(BF16) for j, l in enumerate(leaves)]
+            assert all(torch.equal((l.detach().double() + sign * step * d.double()), m.double()) for j, (l, m) in enumerate(zip(leaves, moved)) if j == i)
+            f.append((det.gated_linear(*moved, activation=act, out_dtype=F32).double() * dh.double()).sum())
+        slope = (f[0] - f[1]) / (2 * step)
+        want = (grads[i].double() * d.double()).sum()
+        # third derivatives along d: |d|^3 terms of size step^2 / 6; roundings of the gradient's elements
+        noise = 2 * U[BF16] * (grads[i].double() * d.double()).norm() * 4 + step ** 2 * dh.double().abs().sum() * 8
+        assert abs(slope - want) <= noise, (i, slope.item(), want.item(), noise.item())
+
+
+def test_streams_and_graphs():
+    x, wg, wu = operands(14, 300, 100, 70)
+    dh = torch.randn(300, 70, device=DEV).to(BF16)
+    for ck in (None, "int8"):
+        def step(x, wg, wu, dh):
+            h, s = det.gated_linear_forward(x, wg, wu, checkpoint=ck)
+            kx = det.pack_int8(x) if ck else x
+            return (h, det.gated_linear(x[:20], wg, wu), *det.gated_linear_backward(dh, kx, wg, wu, s))
+        want = step(x, wg, wu, dh)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = step(x, wg, wu, dh)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        # leaves made for the capture, replayed on new data with eager work between
+        bufs = [t.clone() for t in (x, wg, wu, dh)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = step(*bufs)
+        for k in range(3):
+            fresh = operands(20 + k, 300, 100, 70)
+            for b, t in zip(bufs, fresh):
+                b.copy_(t)
+            graph.replay()
+            eager = step(*bufs)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs, eager))
+
+
+def test_second_derivatives_are_refused():
+    x, wg, wu = operands(15, 20, 32, 16)
+    for ck in (None, "int8"):
+        for i in range(3):
+            leaves = [t.clone().requires_grad_(j == i) for j, t in enumerate((x, wg, wu))]
+            h = det.gated_linear(*leaves, checkpoint=ck, out_dtype=F32)
+            g, = torch.autograd.grad(h.sum(), leaves[i], create_graph=True)
+            with pytest.raises(RuntimeError, match="differentiable once"):
+                torch.autograd.grad(g.float().square().sum(), leaves[i])
+
+
+def test_module_and_a_feed_forward_block():
+    torch.manual_seed(0)
+    up = det.DetGatedLinear(96, 200, activation="gelu_tanh", device=DEV, checkpoint="int8")
+    down = det.DetLinear(200, 96, device=DEV, dtype=BF16)
+    x = torch.randn(2, 50, 96, device=DEV).to(BF16).requires_grad_(True)
+    y = down(up(x))
+    assert y.shape == (2, 50, 96) and y.dtype == F32
+    grads = torch.autograd.grad(det.exact_mse_loss(y), [x, *up.parameters(), *down.parameters()])
+    assert all(torch.isfinite(g).all() and g.dtype == BF16 for g in grads)
+    again = torch.autograd.grad(det.exact_mse_loss(down(up(x))), [x, *up.parameters(), *down.parameters()])
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
