@@ -2,9 +2,12 @@
 
 The det-train operations (page "det-train", sections "Usage" and "Method"):
 det_gemm, det_gemm_partial, det_combine, det_finalize and the DetLinear
-module; and around it the head of a language model: layer norm, token log
-probabilities and distillation, forward and backward (norm.py, head.py).  The kernels live in libdetgemm.so (C ABI: include/detgemm.h); this
-package only marshals torch tensors into it.
+module; and around it, of a language model: layer norm, token log
+probabilities and distillation (norm.py, head.py), the gated projection of a
+feed-forward block with activations kept in 8 bits (gated.py, packed.py) and the
+losses of post-training (policy.py), forward and backward.  The kernels live in
+libdetgemm.so (C ABI: include/detgemm.h); this package only marshals torch
+tensors into it.
 """
 from ._lib import K_MAX, LSB_EXPONENT, NUM_DIGITS, DetGemmError  # noqa: F401
 from .api import (det_combine, det_finalize, det_gemm, det_gemm_noalloc, det_gemm_partial,  # noqa: F401
@@ -20,6 +23,8 @@ from .loss import exact_mean, exact_mse_loss  # noqa: F401
 from .norm import (NORM_SHARD_ROWS, DetLayerNorm, layer_norm, layer_norm_backward, layer_norm_digits,  # noqa: F401
                    layer_norm_forward)
 from .packed import PackedInt8, pack_int8, unpack_int8  # noqa: F401
+from .policy import (PolicyLoss, PreferenceLoss, policy_loss, policy_loss_backward, policy_loss_forward,  # noqa: F401
+                     preference_loss, preference_loss_backward, preference_loss_forward)
 
 __all__ = ["det_gemm", "det_gemm_noalloc", "det_gemm_partial", "det_combine", "det_finalize", "DetLinear",
            "round_f32_to_bf16", "has_nonfinite", "set_gemm_path", "last_gemm_plan", "gemm_path", "get_gemm_path",
@@ -31,4 +36,6 @@ __all__ = ["det_gemm", "det_gemm_noalloc", "det_gemm_partial", "det_combine", "d
            "distill_loss", "distill_forward", "distill_backward",
            "gated_linear", "gated_linear_forward", "gated_linear_backward", "GatedState", "DetGatedLinear",
            "pack_int8", "unpack_int8", "PackedInt8",
+           "policy_loss", "policy_loss_forward", "policy_loss_backward", "PolicyLoss",
+           "preference_loss", "preference_loss_forward", "preference_loss_backward", "PreferenceLoss",
            "NUM_DIGITS", "LSB_EXPONENT", "K_MAX", "DetGemmError"]

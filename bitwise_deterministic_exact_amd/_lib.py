@@ -81,6 +81,14 @@ def load() -> ctypes.CDLL:
                                    i64, c_int, vp, vp, vp, vp, ctypes.c_size_t, vp], c_int),
         "det_int8_pack": ([c_int, vp, i64, i64, i64, vp, vp, vp], c_int),
         "det_int8_unpack": ([vp, i64, vp, i64, i64, c_int, vp, vp], c_int),
+        "det_policy_loss_workspace_bytes": ([i64, i64, c_int], i64),
+        "det_policy_loss": ([vp, i64, vp, i64, vp, i64, c_int, vp, i64, vp, i64, i64, i64, *[ctypes.c_double] * 3, c_int,
+                             vp, vp, vp, vp, vp, ctypes.c_size_t, vp], c_int),
+        "det_policy_loss_grad": ([vp, i64, vp, i64, vp, i64, c_int, vp, i64, vp, i64, i64, i64, *[ctypes.c_double] * 3,
+                                  c_int, vp, vp, i64, i64, vp, vp], c_int),
+        "det_preference_loss": ([vp, i64, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, i64, i64, i64, c_int,
+                                 *[ctypes.c_double] * 3, c_int, vp, vp, vp, vp, vp], c_int),
+        "det_preference_loss_grad": ([vp, i64, i64, vp, i64, i64, i64, vp, vp, i64, vp, vp, vp], c_int),
         "det_set_gemm_path": ([c_int, c_int], c_int),
         "det_set_kernel_events": ([vp, vp], None),
         "det_device_status": ([vp, c_int, ctypes.POINTER(c_int)], c_int),

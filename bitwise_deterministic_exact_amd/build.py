@@ -9,14 +9,14 @@ import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", f) for f in ("detgemm.hip", "head.hip", "norm.hip", "gated.hip", "int8_block.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("detgemm.hip", "head.hip", "norm.hip", "gated.hip", "int8_block.hip", "policy.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdetgemm.so")
 # the benchmark's LDS-atomic peak probe: its own library, never loaded by the package
 PROBE_SOURCES = [os.path.join(PKG, "csrc", "lds_probe.hip")]
 PROBE_LIB = os.path.join(PKG, "liblds_probe.so")
 # the torch side of the operators (autograd, streams): host code only
-OPS_SOURCES = [os.path.join(PKG, "csrc", f) for f in ("head_ops.cpp", "block_ops.cpp")]
+OPS_SOURCES = [os.path.join(PKG, "csrc", f) for f in ("head_ops.cpp", "block_ops.cpp", "policy_ops.cpp")]
 OPS_LIB = os.path.join(PKG, "_ops.so")
 ARCH = "gfx950"
 

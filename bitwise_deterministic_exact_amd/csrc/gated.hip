@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "elementary.h"
 #include "int8_block.h"
 
 // every fused multiply-add below is written as one: the compiler forms none
@@ -28,16 +29,6 @@ using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------- activations
-
-// e^x to about 2 units: the product with log2 e is carried in two parts, or
-// its rounding would cost |x| units
-__device__ __forceinline__ float exp_of(float x) {
-  x = __builtin_amdgcn_fmed3f(x, -200.0f, 200.0f);            // e^+-200 is inf or 0 in 32 bits all the same
-  const float hi = x * 1.44269502f;
-  const float lo = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -hi));
-  const float e = __builtin_amdgcn_exp2f(hi);
-  return e == INFINITY ? e : fmaf(e, lo * 0.693147182f, e);
-}
 
 // s = 1 / (1 + e^-x) and 1 - s, neither from a difference
 struct Sigmoid {

@@ -9,6 +9,7 @@
 #include "ops_common.h"
 
 void bind_block(py::module_& m);          // block_ops.cpp
+void bind_policy(py::module_& m);         // policy_ops.cpp
 
 namespace {
 
@@ -425,4 +426,5 @@ PYBIND11_MODULE(_ops, m) {
   }, release());
   m.def("distill_backward", &distill_backward, release());
   bind_block(m);
+  bind_policy(m);
 }

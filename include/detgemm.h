@@ -631,6 +631,102 @@ det_status det_int8_pack(det_dtype dt, const void* x, int64_t s_x, int64_t N, in
 det_status det_int8_unpack(const int8_t* codes, int64_t s_codes, const int8_t* exps, int64_t N, int64_t C,
                            det_dtype dt, void* y, void* stream);
 
+typedef enum { DET_REDUCE_NONE = 0, DET_REDUCE_TOKENS = 1, DET_REDUCE_SEQUENCES = 2 } det_reduction;
+typedef enum { DET_PREFER_SIGMOID = 0, DET_PREFER_HINGE = 1, DET_PREFER_IPO = 2 } det_preference;
+
+/*
+ * det_policy_loss -- per token, with d = logprob - old_logprob, r = e^d, A the
+ * advantage and q = ref_logprob - logprob:
+ *   l = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_weight k
+ *   k = e^q - 1 - q   (0 without ref_logprob)
+ * A token is clipped where r A exceeds the clipped product: d > ln(1 +
+ * clip_high) with A > 0, or d < ln(1 - clip_low) with A < 0, decided in 64 bits.
+ *   logprob, old_logprob, ref_logprob (null: none)   [B] rows of T fp32
+ *   advantage         [B] rows of T fp32 (advantage_t 1) or one value to a row,
+ *                     s_advantage apart (advantage_t 0)
+ *   mask              [B] rows of T bytes, 0: the token does not count (what it
+ *                     holds is not looked at); null: all count
+ *   clip_low in [0, 1], clip_high and kl_weight in [0, 1e6)
+ *   reduction         none: l, k and whether clipped (0 or 1) per token, [B][T]
+ *                     contiguous, 0 where a token does not count; tokens: their
+ *                     means over the tokens that count; sequences: the means
+ *                     over the rows that have any of each row's mean; one fp32
+ *                     value each, 0 where nothing counts
+ *   count             [B + 1] int64: the rows' counts and the divisor of the
+ *                     tokens' or the rows' sum, for the gradient; null with none
+ *   workspace         det_policy_loss_workspace_bytes(B, T, reduction), 8-byte
+ *                     aligned
+ * A row's sums are formed in 64 bits in one order per T and rounded to fp32
+ * (for sequences after the division by its count); the rows' values are added
+ * exactly and rounded once, then divided: the results do not depend on the order
+ * of the rows.  A token that counts and whose l is not finite is noted in the
+ * device status ("non-finite"); the sums follow IEEE arithmetic (NaN, or both
+ * infinities: NaN).  B <= 2^22, T <= 2^24, B T <= 2^40.
+ * Returns DET_OK, DET_EINVAL or DET_EHIP.
+ */
+int64_t det_policy_loss_workspace_bytes(int64_t B, int64_t T, det_reduction reduction);
+
+det_status det_policy_loss(const float* logprob, int64_t s_logprob, const float* old_logprob, int64_t s_old,
+                           const float* advantage, int64_t s_advantage, int advantage_t, const uint8_t* mask,
+                           int64_t s_mask, const float* ref_logprob, int64_t s_ref, int64_t B, int64_t T,
+                           double clip_low, double clip_high, double kl_weight, det_reduction reduction, float* loss,
+                           float* kl, float* clipped, int64_t* count, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * det_policy_loss_grad -- dlogprob [B][T] contiguous = w (-r A where the token
+ * is not clipped + kl_weight (1 - e^q)), 0 where a token does not count; w = g
+ * over the token's divisor.
+ *   count             as det_policy_loss wrote it (null with none)
+ *   g                 fp32: one value, or with reduction none [B][T] with
+ *                     strides s_g and s_g_t
+ * The other arguments as for det_policy_loss.
+ */
+det_status det_policy_loss_grad(const float* logprob, int64_t s_logprob, const float* old_logprob, int64_t s_old,
+                                const float* advantage, int64_t s_advantage, int advantage_t, const uint8_t* mask,
+                                int64_t s_mask, const float* ref_logprob, int64_t s_ref, int64_t B, int64_t T,
+                                double clip_low, double clip_high, double kl_weight, det_reduction reduction,
+                                const int64_t* count, const float* g, int64_t s_g, int64_t s_g_t, float* dlogprob,
+                                void* stream);
+
+/*
+ * det_preference_loss -- over P pairs of answers, with s the sum over the tokens
+ * that count of logprob - ref_logprob (by_length: its mean; 0 where none counts)
+ * and z = beta (s_chosen - s_rejected) - margin:
+ *   sigmoid  -(1 - label_smoothing) ln sigma(z) - label_smoothing ln sigma(-z)
+ *   hinge    max(0, 1 - z)
+ *   ipo      (s_chosen - s_rejected - 1 / (2 beta))^2
+ *   chosen, rejected  [P] rows of T_chosen and T_rejected fp32; masks as for
+ *                     det_policy_loss; reference rows for both sides or for none
+ *   beta in (0, 1e6), margin finite (0 for ipo), label_smoothing in [0, 0.5]
+ *                     (0 unless sigmoid)
+ *   loss, chosen_reward, rejected_reward   [P] fp32; reward = beta s
+ *   slope             [P][2] fp32 for the gradient: the derivative of the pair's
+ *                     loss in each token that counts of its two sides
+ * Sums and the loss are formed in 64 bits, in an order that the two lengths
+ * alone decide.  A loss that is not finite is noted in the device status
+ * ("non-finite").  P <= 2^22, lengths <= 2^24, P times a length <= 2^40.
+ * Returns DET_OK, DET_EINVAL or DET_EHIP.
+ */
+det_status det_preference_loss(const float* chosen, int64_t s_chosen, const float* ref_chosen, int64_t s_ref_chosen,
+                               const uint8_t* chosen_mask, int64_t s_chosen_mask, int64_t T_chosen,
+                               const float* rejected, int64_t s_rejected, const float* ref_rejected,
+                               int64_t s_ref_rejected, const uint8_t* rejected_mask, int64_t s_rejected_mask,
+                               int64_t T_rejected, int64_t P, det_preference kind, double beta, double margin,
+                               double label_smoothing, int by_length, float* loss, float* chosen_reward,
+                               float* rejected_reward, float* slope, void* stream);
+
+/*
+ * det_preference_loss_grad -- g slope for the tokens that count, 0 for the
+ * others: dchosen [P][T_chosen] and drejected [P][T_rejected] contiguous (null:
+ * not needed).
+ *   g                 [P] fp32, s_g apart (0 repeats one value)
+ */
+det_status det_preference_loss_grad(const uint8_t* chosen_mask, int64_t s_chosen_mask, int64_t T_chosen,
+                                    const uint8_t* rejected_mask, int64_t s_rejected_mask, int64_t T_rejected,
+                                    int64_t P, const float* slope, const float* g, int64_t s_g, float* dchosen,
+                                    float* drejected, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

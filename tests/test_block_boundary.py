@@ -173,3 +173,140 @@ def test_gated_module():
     assert m.w_gate.shape == m.w_up.shape == (10, 6) and m.w_gate.dtype == torch.bfloat16
     assert not torch.equal(m.w_gate, m.w_up) and m.w_up.abs().max() <= 6 ** -0.5
     assert "gelu" in repr(m) and "int8" in repr(m)
+
+
+# ---------------------------------------------------------------- policy and preference losses
+
+F64 = ctypes.c_double
+
+
+def _policy(lp=A, old=A, adv=A, s=8, adv_t=1, mask=None, s_mask=8, ref=None, Bn=2, T=8, low=0.2, high=0.2, beta=0.0, red=1, loss=B,
+            kl=B, clipped=B, count=B, ws=B, n=1 << 20):
+    return _lib.load().det_policy_loss(lp, s, old, 8, adv, 8, adv_t, mask, s_mask, ref, 8, Bn, T, low, high, beta, red, loss, kl,
+                                       clipped, count, ws, n, None)
+
+
+def _policy_grad(lp=A, red=1, count=A, g=A, s_g=0, s_gt=0, d=B, Bn=2, T=8, low=0.2, ref=None, beta=0.0):
+    return _lib.load().det_policy_loss_grad(lp, 8, A, 8, A, 8, 1, None, 0, ref, 8, Bn, T, low, 0.2, beta, red, count, g, s_g, s_gt,
+                                            d, None)
+
+
+def _prefer(c=A, r=A, rc=None, rr=None, s=8, Tc=8, Tr=8, Pn=2, kind=0, beta=0.1, margin=0.0, smooth=0.0, loss=B, rew=B, slope=B):
+    return _lib.load().det_preference_loss(c, s, rc, 8, None, 0, Tc, r, 8, rr, 8, None, 0, Tr, Pn, kind, beta, margin, smooth, 0,
+                                           loss, rew, B, slope, None)
+
+
+def _prefer_grad(s_m=0, Tc=8, Tr=8, Pn=2, slope=A, g=A, s_g=1, dc=B, dr=B):
+    return _lib.load().det_preference_loss_grad(None, s_m, Tc, None, 0, Tr, Pn, slope, g, s_g, dc, dr, None)
+
+
+O2, O4, N8 = P((1 << 20) + 2), P((1 << 21) + 4), float("nan")
+
+
+@pytest.mark.parametrize("call", [
+    lambda: _policy(Bn=-1), lambda: _policy(T=-1), lambda: _policy(Bn=(1 << 22) + 1), lambda: _policy(T=(1 << 24) + 1),
+    lambda: _policy(Bn=1 << 21, T=1 << 20), lambda: _policy(s=-1), lambda: _policy(s_mask=-8), lambda: _policy(low=-0.1),
+    lambda: _policy(low=1.5), lambda: _policy(low=N8), lambda: _policy(high=-1.0), lambda: _policy(high=N8),
+    lambda: _policy(high=1e6), lambda: _policy(beta=-1.0), lambda: _policy(beta=N8), lambda: _policy(beta=0.1),
+    lambda: _policy(adv_t=2), lambda: _policy(red=3), lambda: _policy(red=-1), lambda: _policy(lp=NULL), lambda: _policy(old=NULL),
+    lambda: _policy(adv=NULL), lambda: _policy(lp=O2), lambda: _policy(ref=O2), lambda: _policy(loss=NULL), lambda: _policy(kl=NULL),
+    lambda: _policy(clipped=NULL), lambda: _policy(count=NULL), lambda: _policy(count=O4), lambda: _policy(loss=O2),
+    lambda: _policy(ws=NULL), lambda: _policy(n=7), lambda: _policy(ws=O4),
+    lambda: _policy_grad(lp=NULL), lambda: _policy_grad(red=7), lambda: _policy_grad(count=NULL), lambda: _policy_grad(g=NULL),
+    lambda: _policy_grad(s_g=-1), lambda: _policy_grad(s_gt=-1), lambda: _policy_grad(d=NULL), lambda: _policy_grad(d=O2),
+    lambda: _policy_grad(low=2.0), lambda: _policy_grad(beta=1.0), lambda: _policy_grad(count=O4),
+    lambda: _prefer(Pn=-1), lambda: _prefer(Tc=-1), lambda: _prefer(Tr=-1), lambda: _prefer(Tr=(1 << 24) + 1), lambda: _prefer(s=-1),
+    lambda: _prefer(kind=3), lambda: _prefer(beta=0.0), lambda: _prefer(beta=N8), lambda: _prefer(margin=N8),
+    lambda: _prefer(margin=0.5, kind=2), lambda: _prefer(smooth=0.6), lambda: _prefer(smooth=-0.1), lambda: _prefer(smooth=0.1, kind=1),
+    lambda: _prefer(rc=A), lambda: _prefer(rr=A), lambda: _prefer(c=NULL), lambda: _prefer(r=NULL), lambda: _prefer(loss=NULL),
+    lambda: _prefer(rew=NULL), lambda: _prefer(slope=NULL), lambda: _prefer(c=O2), lambda: _prefer(slope=O2),
+    lambda: _prefer_grad(Pn=-1), lambda: _prefer_grad(Tc=-1), lambda: _prefer_grad(s_m=-1), lambda: _prefer_grad(slope=NULL),
+    lambda: _prefer_grad(g=NULL), lambda: _prefer_grad(s_g=-1), lambda: _prefer_grad(dc=O2), lambda: _prefer_grad(g=O2),
+])
+def test_loss_entry_points_refuse(call):
+    assert call() == EINVAL and _lib.last_error()
+
+
+def test_empty_losses_are_no_ops():
+    assert _policy(Bn=0, red=0, lp=NULL, loss=NULL) == _lib.DET_OK and _policy(T=0, red=0, loss=NULL) == _lib.DET_OK
+    assert _policy_grad(T=0, d=NULL) == _lib.DET_OK and _prefer(Pn=0, loss=NULL) == _lib.DET_OK
+    assert _prefer_grad(dc=NULL, dr=NULL) == _lib.DET_OK and _prefer_grad(Tc=0, Tr=0) == _lib.DET_OK
+
+
+def test_loss_workspace_sizes():
+    f = _lib.load().det_policy_loss_workspace_bytes
+    # per part of 512 tokens two sums in 64 bits and two counts; per workgroup that joins rows 35 words
+    assert f(3, 512, 1) == 3 * 24 + 35 * 8 and f(3, 513, 2) == 6 * 24 + 35 * 8
+    assert f((1 << 14) + 1, 512, 1) == ((1 << 14) + 1) * 24 + 2 * 35 * 8
+    assert f(3, 512, 0) == 0 and f(0, 512, 1) == 0 and f(3, 0, 1) == 0
+
+
+def _f(*shape, dtype=torch.float32):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+M = lambda *s: _f(*s, dtype=torch.bool)
+
+
+@pytest.mark.parametrize("call,match", [
+    (lambda: det.policy_loss(_f(2, 4, dtype=torch.bfloat16), _f(2, 4), _f(2)), "float32"),
+    (lambda: det.policy_loss(_f(), _f(), _f()), "logprob"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 5), _f(2)), "old_logprob"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(4)), "advantage"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(2, dtype=torch.float64)), "advantage"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(2, 4), _f(2, 4)), "mask"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(2, 4), M(2, 3)), "mask"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(2, 4), ref_logprob=_f(4)), "ref_logprob"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(2, 4), kl_weight=0.1), "ref_logprob"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(2, 4), clip_low=1.1), "clip_low"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(2, 4), clip_high=-0.1), "clip_high"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(2, 4), ref_logprob=_f(2, 4), kl_weight=-1.0), "kl_weight"),
+    (lambda: det.policy_loss(_f(2, 4), _f(2, 4), _f(2, 4), reduction="mean"), "reduction"),
+    (lambda: det.policy_loss(torch.zeros(2, 4), torch.zeros(2, 4), torch.zeros(2)), "GPU"),
+    (lambda: det.policy_loss_backward(_f(2), _f(2, 4), _f(2, 4), _f(2), None, None), "GPU|gradient"),
+    (lambda: det.preference_loss(_f(2, 4, dtype=torch.bfloat16), _f(2, 4)), "chosen_logprob"),
+    (lambda: det.preference_loss(_f(2, 4), _f()), "rejected_logprob"),
+    (lambda: det.preference_loss(_f(2, 4), _f(3, 4)), "leading shape"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 4), _f(2, 4)), "both sides or for none"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 5), _f(2, 4), _f(2, 4)), "ref_rejected"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 5), chosen_mask=M(2, 5)), "chosen_mask"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 5), rejected_mask=_f(2, 5)), "rejected_mask"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 5), kind="dpo"), "kind"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 5), beta=0.0), "beta"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 5), margin=float("inf")), "margin"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 5), margin=1.0, kind="ipo"), "margin"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 5), label_smoothing=0.7), "label_smoothing"),
+    (lambda: det.preference_loss(_f(2, 4), _f(2, 5), label_smoothing=0.1, kind="hinge"), "label_smoothing"),
+    (lambda: det.preference_loss(torch.zeros(2, 4), torch.zeros(2, 4)), "GPU"),
+    (lambda: det.preference_loss_backward(_f(2), _f(3, 2), (2, 4), (2, 5)), "slope"),
+    (lambda: det.preference_loss_backward(_f(3), _f(2, 2), (2, 4), (2, 5)), "gradient"),
+    (lambda: det.preference_loss_backward(_f(2), _f(2, 2), (2, 4), (3, 5)), "leading shape"),
+    (lambda: det.DetLinear(4, 4, checkpoint="bf16"), "checkpoint"),
+])
+def test_loss_python_layer_refuses(call, match):
+    with pytest.raises(ValueError, match=match):
+        call()
+
+
+@pytest.mark.parametrize("i", range(4))
+def test_losses_refuse_forward_mode(i):
+    args = [_f(2, 4) for _ in range(4)]
+    with fw.dual_level():
+        args[i] = fw.make_dual(args[i], _f(2, 4))
+        with pytest.raises(RuntimeError, match="forward-mode"):
+            det.policy_loss(*args[:3], ref_logprob=args[3])
+        with pytest.raises(RuntimeError, match="forward-mode"):
+            det.preference_loss(*args)
+
+
+def test_losses_refuse_traces():
+    z = torch.zeros
+    x = z(2, 4)
+    for call in (lambda x: det.policy_loss(x, z(2, 4), z(2)).loss, lambda x: det.policy_loss_forward(x, z(2, 4), z(2))[0].loss,
+                 lambda x: det.policy_loss_backward(z(()), x, z(2, 4), z(2), None, z(3, dtype=torch.int64)),
+                 lambda x: det.preference_loss(x, z(2, 5)).loss, lambda x: det.preference_loss_forward(x, z(2, 5))[1],
+                 lambda x: det.preference_loss_backward(x[:, 0], z(2, 2), (2, 4), (2, 5))[0]):
+        with pytest.raises(RuntimeError, match="cannot be traced"):
+            torch.jit.trace(call, (x,), check_trace=False)
+        with pytest.raises(RuntimeError, match="cannot be traced"):
+            make_fx(call)(x)

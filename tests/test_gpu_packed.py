@@ -122,3 +122,36 @@ def test_graph_replays():
         torch.cuda.synchronize()
         assert torch.equal(p.codes, q.codes) and torch.equal(p.exponents, q.exponents)
         assert torch.equal(y, det.unpack_int8(q, BF16))
+
+
+@pytest.mark.parametrize("dtype,bias,N,C,F", [(BF16, False, 70, 96, 40), (F32, True, 33, 45, 20), (BF16, True, 300, 513, 64),
+                                              (F32, False, 1, 1, 1)])
+def test_det_linear_reads_its_input_back(dtype, bias, N, C, F):
+    announce(f"DetLinear int8 {dtype} {bias} {N} {C} {F}")
+    torch.manual_seed(2)
+    plain = det.DetLinear(C, F, bias=bias, device=DEV, dtype=dtype)
+    kept = det.DetLinear(C, F, bias=bias, device=DEV, dtype=dtype, checkpoint="int8")
+    kept.load_state_dict(plain.state_dict())
+    assert "int8" in repr(kept)
+    x = torch.randn(2, N, C, device=DEV).to(dtype).requires_grad_(True)
+    # the same results but for dW, which is that of the values read back
+    y, z = plain(x), kept(x)
+    assert torch.equal(y, z)
+    gy = torch.randn_like(y)
+    a, b = (torch.autograd.grad(t, [x, *m.parameters()], gy) for t, m in ((y, plain), (z, kept)))
+    assert torch.equal(a[0], b[0]) and (not bias or torch.equal(a[2], b[2]))
+    back = det.unpack_int8(det.pack_int8(x), dtype).requires_grad_(True)
+    assert torch.equal(torch.autograd.grad(plain(back), plain.weight, gy)[0], b[1])
+    # half a unit of the largest in a block: 1/127 of it
+    assert ((back - x).abs() <= x.abs().amax(-1, keepdim=True) / 127).all()
+    sizes = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (sizes.append((t.dtype, t.numel())), t)[1], lambda t: t):
+        kept(x)
+    assert sorted(n for d, n in sizes if d == torch.int8) == sorted([2 * N * C, 2 * N * ((C + 31) // 32)])
+    assert sum(n for d, n in sizes if d != torch.int8) == F * C
+    # frozen weights: nothing of x is kept
+    kept.requires_grad_(False)
+    sizes.clear()
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (sizes.append(t.dtype), t)[1], lambda t: t):
+        w = kept(x)
+    assert torch.int8 not in sizes and torch.equal(torch.autograd.grad(w, x, gy)[0], a[0])
