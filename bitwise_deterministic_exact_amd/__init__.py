@@ -14,7 +14,7 @@ from .api import (det_combine, det_finalize, det_gemm, det_gemm_noalloc, det_gem
                   exact_dot, exact_dot_digits, exact_sqdiff_digits, exact_sum_squares, gemm_any_k,
                   device_status, gemm_path, get_gemm_path, has_nonfinite, last_gemm_plan, round_f32_to_bf16,
                   set_gemm_path)
-from .gated import (DetGatedLinear, GatedState, gated_linear, gated_linear_backward,  # noqa: F401
+from .gated import (DetGatedLinear, GatedState, ScaledHalf, gated_linear, gated_linear_backward,  # noqa: F401
                     gated_linear_forward)
 from .linear import DetLinear  # noqa: F401
 from .head import (TokenLogProbs, distill_backward, distill_forward, distill_loss, token_logprobs,  # noqa: F401
@@ -34,7 +34,7 @@ __all__ = ["det_gemm", "det_gemm_noalloc", "det_gemm_partial", "det_combine", "d
            "layer_norm", "layer_norm_forward", "layer_norm_backward", "layer_norm_digits", "DetLayerNorm", "NORM_SHARD_ROWS",
            "token_logprobs", "token_logprobs_forward", "token_logprobs_backward", "TokenLogProbs",
            "distill_loss", "distill_forward", "distill_backward",
-           "gated_linear", "gated_linear_forward", "gated_linear_backward", "GatedState", "DetGatedLinear",
+           "gated_linear", "gated_linear_forward", "gated_linear_backward", "GatedState", "ScaledHalf", "DetGatedLinear",
            "pack_int8", "unpack_int8", "PackedInt8",
            "policy_loss", "policy_loss_forward", "policy_loss_backward", "PolicyLoss",
            "preference_loss", "preference_loss_forward", "preference_loss_backward", "PreferenceLoss",

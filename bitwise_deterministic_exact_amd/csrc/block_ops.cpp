@@ -17,7 +17,7 @@ det_activation act_of(const std::string& name, const char* what) {
 }
 
 det_save save_of(const std::optional<std::string>& name, const char* what) {
-  if (!name) return DET_SAVE_BF16;
+  if (!name) return DET_SAVE_HALF;
   if (*name == "int8") return DET_SAVE_INT8;
   refuse(what, ": checkpoint must be None or \"int8\" (got \"", *name, "\")");
 }
@@ -49,7 +49,8 @@ Tensor wide_rows(const Tensor& t) {
   return fits || r.size(0) == 0 ? r : r.clone(at::MemoryFormat::Contiguous);
 }
 
-// what a forward call keeps of both projections: bf16 [.., F], or codes and exponents
+// what a forward call keeps of both projections: fp16 elements or int8 codes
+// [.., F], and the exponents of their blocks
 struct Saved {
   Tensor gate, up, gate_exp, up_exp;
 };
@@ -68,13 +69,11 @@ Tensor gated_forward(const Tensor& x, const Tensor& wg, const Tensor& wu, det_ac
   const std::vector<int64_t> shape = with_last(lead_of(x), F), blocks = with_last(lead_of(x), (F + 31) / 32);
   Tensor h = at::empty(shape, x.options().dtype(ht));
   if (save != DET_SAVE_NONE) {
-    const auto o = x.options().dtype(save == DET_SAVE_INT8 ? at::kChar : at::kBFloat16);
+    const auto o = x.options().dtype(save == DET_SAVE_INT8 ? at::kChar : at::kHalf), e = x.options().dtype(at::kChar);
     kept.gate = at::empty(shape, o);
     kept.up = at::empty(shape, o);
-    if (save == DET_SAVE_INT8) {
-      kept.gate_exp = at::empty(blocks, o);
-      kept.up_exp = at::empty(blocks, o);
-    }
+    kept.gate_exp = at::empty(blocks, e);
+    kept.up_exp = at::empty(blocks, e);
   }
   const int64_t bytes = det_gated_linear_workspace_bytes(N, C, F, save, C % 64 == 0);
   const Tensor ws = bytes > 0 ? at::empty({bytes}, x.options().dtype(at::kByte)) : Tensor();
@@ -103,13 +102,12 @@ GatedGrads gated_backward(const Tensor& dh, const Tensor& x, const OptTensor& x_
   const std::vector<int64_t> shape = with_last(lead_of(x), F), blocks = with_last(lead_of(x), (F + 31) / 32);
   if (dh.sizes() != at::IntArrayRef(shape) || !known(dh.scalar_type()) || dh.device() != x.device())
     refuse(what, ": dh must be float32 or bfloat16 of shape ", shape, " on x's device");
-  const bool int8 = kept.gate_exp.defined();
-  const ScalarType kt = int8 ? at::kChar : at::kBFloat16;
+  const bool int8 = kept.gate.scalar_type() == at::kChar;
   for (const Tensor* t : {&kept.gate, &kept.up})
-    if (t->scalar_type() != kt || t->sizes() != at::IntArrayRef(shape) || t->device() != x.device())
+    if (t->scalar_type() != (int8 ? at::kChar : at::kHalf) || t->sizes() != at::IntArrayRef(shape) || t->device() != x.device())
       refuse(what, ": gate and up must be as gated_linear_forward gives them");
   for (const Tensor* t : {&kept.gate_exp, &kept.up_exp})
-    if (t->defined() != int8 || (int8 && (t->scalar_type() != kt || t->sizes() != at::IntArrayRef(blocks) || t->device() != x.device())))
+    if (t->scalar_type() != at::kChar || t->sizes() != at::IntArrayRef(blocks) || t->device() != x.device())
       refuse(what, ": gate and up must be as gated_linear_forward gives them");
   on_gpu(x, what, "x");
   const c10::DeviceGuard guard(x.device());
@@ -122,17 +120,12 @@ GatedGrads gated_backward(const Tensor& dh, const Tensor& x, const OptTensor& x_
   }
   const Tensor dh2 = rows(dh), x2 = x_exp ? x.contiguous() : rows(x), g2 = rows(wg), u2 = rows(wu);
   const Tensor kg = kept.gate.contiguous(), ku = kept.up.contiguous();
-  Tensor xe, ge, ue;
-  if (x_exp) xe = x_exp->contiguous();
-  if (int8) {
-    ge = kept.gate_exp.contiguous();
-    ue = kept.up_exp.contiguous();
-  }
+  const Tensor xe = x_exp ? x_exp->contiguous() : Tensor(), ge = kept.gate_exp.contiguous(), ue = kept.up_exp.contiguous();
   const int64_t bytes = det_gated_linear_grad_workspace_bytes(N, C, F, need_dx, need_dw);
   const Tensor ws = bytes > 0 ? at::empty({bytes}, x.options().dtype(at::kByte)) : Tensor();
   ok(det_gated_linear_grad(dt_of(dh.scalar_type()), in(dh2), dh2.stride(0), in(x2), x_exp ? C : x2.stride(0),
-                           out<int8_t>(xe), in(g2), g2.stride(0), in(u2), u2.stride(0),
-                           int8 ? DET_SAVE_INT8 : DET_SAVE_BF16, in(kg), in(ku), out<int8_t>(ge), out<int8_t>(ue), N,
+                           static_cast<const int8_t*>(xe.defined() ? xe.const_data_ptr() : nullptr), in(g2), g2.stride(0), in(u2), u2.stride(0),
+                           int8 ? DET_SAVE_INT8 : DET_SAVE_HALF, in(kg), in(ku), static_cast<const int8_t*>(in(ge)), static_cast<const int8_t*>(in(ue)), N,
                            C, F, act, out<void>(g.dx), out<void>(g.dwg), out<void>(g.dwu), out<void>(ws),
                            static_cast<size_t>(bytes), stream_of(x)));
   return g;
@@ -232,15 +225,13 @@ void bind_block(py::module_& m) {
           Saved k;
           const Tensor h = gated_forward(x, wg, wu, act_of(activation, "gated_linear"), dt,
                                          save_of(checkpoint, "gated_linear"), k);
-          return std::make_tuple(h, k.gate, k.up, opt(k.gate_exp), opt(k.up_exp));
+          return std::make_tuple(h, k.gate, k.up, k.gate_exp, k.up_exp);
         }, release());
   m.def("gated_linear_backward",
         [](const Tensor& dh, const Tensor& x, const OptTensor& x_exp, const Tensor& wg, const Tensor& wu,
-           const Tensor& gate, const Tensor& up, const OptTensor& gate_exp, const OptTensor& up_exp,
+           const Tensor& gate, const Tensor& up, const Tensor& gate_exp, const Tensor& up_exp,
            const std::string& activation, bool need_dx, bool need_dw) {
-          const GatedGrads g = gated_backward(dh, x, x_exp, wg, wu,
-                                              {gate, up, gate_exp.value_or(Tensor()), up_exp.value_or(Tensor())},
-                                              act_of(activation, "gated_linear_backward"), need_dx, need_dw);
+          const GatedGrads g = gated_backward(dh, x, x_exp, wg, wu, {gate, up, gate_exp, up_exp}, act_of(activation, "gated_linear_backward"), need_dx, need_dw);
           return std::make_tuple(opt(g.dx), opt(g.dwg), opt(g.dwu));
         }, release());
   m.def("pack_int8", &pack_int8, release());

@@ -263,29 +263,33 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
         float h[4];
         act_times(a.act, g, u, h);
         store4(a.dt, a.out, b * a.na + c, h, in);
-        if (a.save == DET_SAVE_BF16) {
-          store4(DET_BF16, a.gate, b * a.na + c, g, in);
-          store4(DET_BF16, a.up, b * a.na + c, u, in);
-        } else if (a.save == DET_SAVE_INT8) {
+        if (a.save != DET_SAVE_NONE) {
           // 8 lanes hold a block of 32 features; those past the end count as 0
+          const bool int8 = a.save == DET_SAVE_INT8;
           uint32_t tg = 0u, tu = 0u;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (k < n) {
-              tg = max(tg, magnitude(g[k]));
-              tu = max(tu, magnitude(u[k]));
+              tg = max(tg, int8 ? magnitude(g[k]) : finite_magnitude(g[k]));
+              tu = max(tu, int8 ? magnitude(u[k]) : finite_magnitude(u[k]));
             }
           tg = top_of_8(tg);
           tu = top_of_8(tu);
-          const bool bad_g = not_finite(tg), bad_u = not_finite(tu);
-          const int eg = block_exponent(tg), eu = block_exponent(tu);
-          const int64_t blocks = (a.na + 31) / 32;
+          const bool bad_g = not_finite(tg), bad_u = not_finite(tu);        // int8 alone
+          const int eg = int8 ? block_exponent(tg) : half_exponent(tg), eu = int8 ? block_exponent(tu) : half_exponent(tu);
+          const int64_t blocks = (a.na + 31) / 32, at = b * a.na + c;
           if ((lane & 7) == 0 && in > 0) {
             a.gate_exp[b * blocks + c / 32] = static_cast<int8_t>(bad_g ? DET_INT8_NAN : eg);
             a.up_exp[b * blocks + c / 32] = static_cast<int8_t>(bad_u ? DET_INT8_NAN : eu);
           }
-          store_codes(static_cast<int8_t*>(a.gate) + b * a.na + c, codes_of(g, power_of_two(-eg), bad_g), in);
-          store_codes(static_cast<int8_t*>(a.up) + b * a.na + c, codes_of(u, power_of_two(-eu), bad_u), in);
+          const float ig = power_of_two(-eg), iu = power_of_two(-eu);
+          if (int8) {
+            store_codes(static_cast<int8_t*>(a.gate) + at, codes_of(g, ig, bad_g), in);
+            store_codes(static_cast<int8_t*>(a.up) + at, codes_of(u, iu, bad_u), in);
+          } else {
+            store_halves(static_cast<uint16_t*>(a.gate) + at, g, ig, in);
+            store_halves(static_cast<uint16_t*>(a.up) + at, u, iu, in);
+          }
         }
       }
     }
@@ -419,7 +423,7 @@ __device__ __forceinline__ void write_turned(const Tile& t, char* dst, int64_t s
 
 struct GateGradArgs {
   const void* dh; int64_t s_dh; int dh_dt;
-  const void* gate; const void* up;       // [N][F] bf16 or codes
+  const void* gate; const void* up;       // [N][F] halves or codes
   const int8_t* gate_exp; const int8_t* up_exp;
   int64_t N, F, Fp, Np;
   int act, save;
@@ -443,14 +447,14 @@ __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
     const int in = b < a.N ? n : 0;
     float dh[4], g[4], u[4];
     load4(a.dh_dt, a.dh, b * a.s_dh + f, dh, in);
+    const float ug = in > 0 ? unit_of(a.gate_exp[b * blocks + f / 32]) : 0.0f;
+    const float uu = in > 0 ? unit_of(a.up_exp[b * blocks + f / 32]) : 0.0f;
     if (a.save == DET_SAVE_INT8) {
-      const float ug = in > 0 ? unit_of(a.gate_exp[b * blocks + f / 32]) : 0.0f;
-      const float uu = in > 0 ? unit_of(a.up_exp[b * blocks + f / 32]) : 0.0f;
       values_of(load_codes(static_cast<const int8_t*>(a.gate) + b * a.F + f, in), ug, g);
       values_of(load_codes(static_cast<const int8_t*>(a.up) + b * a.F + f, in), uu, u);
     } else {
-      load4(DET_BF16, a.gate, b * a.F + f, g, in);
-      load4(DET_BF16, a.up, b * a.F + f, u, in);
+      load_halves(static_cast<const uint16_t*>(a.gate) + b * a.F + f, ug, g, in);
+      load_halves(static_cast<const uint16_t*>(a.up) + b * a.F + f, uu, u, in);
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -587,7 +591,7 @@ void turn_rows(const void* src, int64_t s_src, const int8_t* exps, int64_t R, in
 }
 
 bool known_act(int act) { return act == DET_ACT_SILU || act == DET_ACT_GELU || act == DET_ACT_GELU_TANH; }
-bool known_save(int save) { return save == DET_SAVE_NONE || save == DET_SAVE_BF16 || save == DET_SAVE_INT8; }
+bool known_save(int save) { return save == DET_SAVE_NONE || save == DET_SAVE_HALF || save == DET_SAVE_INT8; }
 
 det_status check_sizes(int64_t N, int64_t C, int64_t F, int act, int save) {
   if (!known_act(act)) return fail(DET_EINVAL, "unknown activation %d", act);
@@ -631,10 +635,9 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
   if ((st = check_operand(x, s_x, "x")) != DET_OK || (st = check_operand(w_gate, s_gate, "w_gate")) != DET_OK ||
       (st = check_operand(w_up, s_up, "w_up")) != DET_OK)
     return st;
-  if (h == nullptr || (save != DET_SAVE_NONE && (gate == nullptr || up == nullptr)) ||
-      (save == DET_SAVE_INT8 && (gate_exp == nullptr || up_exp == nullptr)))
+  if (h == nullptr || (save != DET_SAVE_NONE && (gate == nullptr || up == nullptr || gate_exp == nullptr || up_exp == nullptr)))
     return fail(DET_EINVAL, "null output");
-  if (!aligned_for(h, h_dt) || (save == DET_SAVE_BF16 && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
+  if (!aligned_for(h, h_dt) || (save == DET_SAVE_HALF && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
     return fail(DET_EINVAL, "outputs must be aligned to their element size");
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (save == DET_SAVE_NONE && N <= FEW) {
@@ -688,10 +691,10 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
     return need_dw ? hip_check(hipGetLastError(), "clearing launch") : DET_OK;
   }
   if (!need_dx && !need_dw) return DET_OK;
-  if (dh == nullptr || gate == nullptr || up == nullptr || (save == DET_SAVE_INT8 && (gate_exp == nullptr || up_exp == nullptr)))
+  if (dh == nullptr || gate == nullptr || up == nullptr || gate_exp == nullptr || up_exp == nullptr)
     return fail(DET_EINVAL, "null pointer");
   if (s_dh < 0) return fail(DET_EINVAL, "negative stride");
-  if (!aligned_for(dh, dh_dt) || (save == DET_SAVE_BF16 && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
+  if (!aligned_for(dh, dh_dt) || (save == DET_SAVE_HALF && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
     return fail(DET_EINVAL, "operands must be aligned to their element size");
   if (need_dx && ((st = check_operand(w_gate, s_gate, "w_gate")) != DET_OK || (st = check_operand(w_up, s_up, "w_up")) != DET_OK))
     return st;

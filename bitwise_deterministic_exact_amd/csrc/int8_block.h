@@ -78,6 +78,53 @@ __device__ __forceinline__ uint32_t load_codes(const int8_t* p, int n) {
   return w;
 }
 
+// The same blocks with fp16 elements, for what is kept in 16 bits: element =
+// half 2^e, e the exponent that brings the block's largest finite magnitude into
+// [2^14, 2^15).  11 bits each over 29 binades below that (bf16: 8 bits, and the
+// gradients that are formed from it would show it), no overflow; infinities and
+// NaN stay themselves.
+__device__ __forceinline__ uint32_t finite_magnitude(float v) {
+  const uint32_t m = magnitude(v);
+  return not_finite(m) ? 0u : m;
+}
+__device__ __forceinline__ int half_exponent(uint32_t m) {
+  const int e = static_cast<int>(m >> 23) - 141;
+  return max(e, -126);
+}
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+using half_words = uint32_t __attribute__((ext_vector_type(2), aligned(2)));
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, f16x2{static_cast<_Float16>(lo), static_cast<_Float16>(hi)});
+}
+// four adjacent elements at p, n of them inside the row
+__device__ __forceinline__ void store_halves(uint16_t* p, const float (&v)[4], float inv, int n) {
+  const half_words w = {pack_half(v[0] * inv, v[1] * inv), pack_half(v[2] * inv, v[3] * inv)};
+  if (n >= 4) {
+    *reinterpret_cast<half_words*>(p) = w;
+  } else {
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+      if (r < n) p[r] = static_cast<uint16_t>(w[r / 2] >> (16 * (r & 1)));
+  }
+}
+__device__ __forceinline__ void load_halves(const uint16_t* p, float unit, float (&v)[4], int n) {
+  half_words w = {0u, 0u};
+  if (n >= 4) {
+    w = *reinterpret_cast<const half_words*>(p);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+      if (r < n) w[r / 2] |= static_cast<uint32_t>(p[r]) << (16 * (r & 1));
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const uint32_t word = w[r];           // a bit cast of w[r] itself takes the vector's first element
+    const f16x2 h = __builtin_bit_cast(f16x2, word);
+    v[2 * r] = static_cast<float>(h[0]) * unit;
+    v[2 * r + 1] = static_cast<float>(h[1]) * unit;
+  }
+}
+
 // four adjacent elements at element i, n of them inside the row (the others 0)
 __device__ __forceinline__ void load4(int dt, const void* p, int64_t i, float (&v)[4], int n) {
   if (n >= 4) {

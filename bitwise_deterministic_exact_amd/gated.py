@@ -11,9 +11,11 @@ not exact as DetLinear's are; a weight gradient is a sum over the call's rows in
 their order).  h is rounded once; the gradients round dg and du to bfloat16 for
 the matrix cores and each sum once.
 
-With ``checkpoint="int8"`` what the backward pass reads again, x and both
-projections, is kept in 8 bits (packed.py), 33/64 of the bytes: the result h is
-the same, the gradients are those at the values that the 8 bits stand for.
+The backward pass reads x and both projections again; these are kept as fp16
+elements of blocks of 32 that share a power of two (11 bits each, no overflow).
+With ``checkpoint="int8"`` x and both projections are kept in 8 bits
+(packed.py), half the bytes: the result h is the same, the gradients are those
+at the values that the 8 bits stand for.
 
 Arguments are checked in the compiled layer (csrc/block_ops.cpp): ValueError for
 a bad shape, dtype, device or value.  Tracing a call (torch.jit.trace, make_fx)
@@ -30,11 +32,18 @@ from . import _lib
 from .packed import PackedInt8
 
 
+class ScaledHalf(NamedTuple):
+    """fp16 values [..., F] and one int8 exponent e for each 32 of them [...,
+    ceil(F / 32)]: an element is value * 2^e."""
+    values: torch.Tensor
+    exponents: torch.Tensor
+
+
 class GatedState(NamedTuple):
     """What gated_linear_backward reads again: both projections of the forward
-    pass, bfloat16 tensors or (checkpoint "int8") PackedInt8."""
-    gate: Union[torch.Tensor, PackedInt8]
-    up: Union[torch.Tensor, PackedInt8]
+    pass, as ScaledHalf or (checkpoint "int8") PackedInt8."""
+    gate: Union[ScaledHalf, PackedInt8]
+    up: Union[ScaledHalf, PackedInt8]
 
 
 def gated_linear_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, activation: str = "silu",
@@ -42,9 +51,8 @@ def gated_linear_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tens
     """(h, GatedState): gated_linear without a graph, and what
     gated_linear_backward needs besides x and the weights."""
     h, gate, up, ge, ue = _lib.ops().gated_linear_forward(x, w_gate, w_up, activation, out_dtype, checkpoint)
-    if ge is not None:
-        gate, up = PackedInt8(gate, ge), PackedInt8(up, ue)
-    return h, GatedState(gate, up)
+    kind = PackedInt8 if checkpoint == "int8" else ScaledHalf
+    return h, GatedState(kind(gate, ge), kind(up, ue))
 
 
 def gated_linear_backward(dh: torch.Tensor, x: Union[torch.Tensor, PackedInt8], w_gate: torch.Tensor,
@@ -53,8 +61,8 @@ def gated_linear_backward(dh: torch.Tensor, x: Union[torch.Tensor, PackedInt8], 
     """(dx, dw_gate, dw_up), bfloat16, each None when not needed, for the
     incoming gradient dh of h (float32 or bfloat16).  x as the forward pass had
     it, or pack_int8 of it; ``state`` comes from gated_linear_forward."""
-    packed = [isinstance(t, PackedInt8) for t in (x, state.gate, state.up)]
-    (x, xe), (gate, ge), (up, ue) = (t if p else (t, None) for t, p in zip((x, state.gate, state.up), packed))
+    x, xe = x if isinstance(x, PackedInt8) else (x, None)
+    (gate, ge), (up, ue) = state
     return _lib.ops().gated_linear_backward(dh, x, xe, w_gate, w_up, gate, up, ge, ue, activation, need_dx, need_dw)
 
 

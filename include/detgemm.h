@@ -555,8 +555,10 @@ det_status det_distill_grad(det_dtype dt, const void* z, int64_t s_row, int64_t 
 #define DET_INT8_NAN (-128)      /* the exponent byte of a block that was not finite */
 
 typedef enum { DET_ACT_SILU = 0, DET_ACT_GELU = 1, DET_ACT_GELU_TANH = 2 } det_activation;
-/* what the forward call keeps of both projections: nothing, bf16, 8-bit blocks */
-typedef enum { DET_SAVE_NONE = 0, DET_SAVE_BF16 = 1, DET_SAVE_INT8 = 2 } det_save;
+/* what the forward call keeps of both projections: nothing, or blocks of 32
+   features that share a power of two 2^e, as fp16 elements (e brings the block's
+   largest finite magnitude into [2^14, 2^15)) or as int8 codes (det_int8_pack) */
+typedef enum { DET_SAVE_NONE = 0, DET_SAVE_HALF = 1, DET_SAVE_INT8 = 2 } det_save;
 
 /*
  * det_gated_linear -- h = act(g) u with g = x w_gate^T and u = x w_up^T.
@@ -566,9 +568,9 @@ typedef enum { DET_SAVE_NONE = 0, DET_SAVE_BF16 = 1, DET_SAVE_INT8 = 2 } det_sav
  *                     0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
  *   h                 [N][F] contiguous of type h_dt
  *   save              what gate and up ([N][F] contiguous) get: nothing (null
- *                     pointers), g and u in bf16, or int8 codes whose blocks'
- *                     exponents go to gate_exp and up_exp [N][ceil(F / 32)]
- *                     (the format of det_int8_pack)
+ *                     pointers), or g and u as fp16 elements or int8 codes, whose
+ *                     blocks' exponents go to gate_exp and up_exp
+ *                     [N][ceil(F / 32)]
  *   workspace         det_gated_linear_workspace_bytes(N, C, F, save, aligned),
  *                     256-byte aligned; `aligned`: x and both weights start at
  *                     multiples of 16 bytes and their strides are multiples of

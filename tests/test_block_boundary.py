@@ -22,7 +22,7 @@ def _gated(x=A, s_x=64, wg=A, s_g=64, wu=A, s_u=64, N=4, C=64, F=8, act=0, dt=1,
     return _lib.load().det_gated_linear(x, s_x, wg, s_g, wu, s_u, N, C, F, act, dt, h, save, gate, up, ge, ue, ws, n, None)
 
 
-def _grad(dt=1, dh=A, s_dh=8, x=A, s_x=64, xe=None, wg=A, s_g=64, wu=A, s_u=64, save=1, gate=A, up=A, ge=None, ue=None, N=4,
+def _grad(dt=1, dh=A, s_dh=8, x=A, s_x=64, xe=None, wg=A, s_g=64, wu=A, s_u=64, save=1, gate=A, up=A, ge=A, ue=A, N=4,
           C=64, F=8, act=0, dx=B, dwg=B, dwu=B, ws=B, n=1 << 30):
     return _lib.load().det_gated_linear_grad(dt, dh, s_dh, x, s_x, xe, wg, s_g, wu, s_u, save, gate, up, ge, ue, N, C, F, act,
                                              dx, dwg, dwu, ws, n, None)
@@ -43,8 +43,8 @@ def _unpack(codes=A, s=8, exps=A, N=2, C=8, dt=0, y=B):
     (lambda: _gated(N=(1 << 22) + 1), EINVAL), (lambda: _gated(x=NULL), EINVAL), (lambda: _gated(wg=NULL), EINVAL),
     (lambda: _gated(wu=NULL), EINVAL), (lambda: _gated(s_x=-64), EINVAL), (lambda: _gated(s_u=-1), EINVAL),
     (lambda: _gated(x=ODD), EINVAL), (lambda: _gated(wu=ODD), EINVAL), (lambda: _gated(h=NULL), EINVAL),
-    (lambda: _gated(h=P((1 << 21) + 2), dt=0), EINVAL), (lambda: _gated(save=1, gate=B), EINVAL),
-    (lambda: _gated(save=1, gate=B, up=ODD), EINVAL), (lambda: _gated(save=2, gate=B, up=B, ge=B), EINVAL),
+    (lambda: _gated(h=P((1 << 21) + 2), dt=0), EINVAL), (lambda: _gated(save=1, gate=B), EINVAL), (lambda: _gated(save=1, gate=B, up=B, ge=B), EINVAL),
+    (lambda: _gated(save=1, gate=B, up=ODD, ge=B, ue=B), EINVAL), (lambda: _gated(save=2, gate=B, up=B, ge=B), EINVAL),
     # an operand that needs a padded copy, and no room for it
     (lambda: _gated(N=100, C=65, s_x=65, s_g=65, s_u=65, ws=NULL, n=0), EINVAL),
     (lambda: _gated(N=100, s_x=65, n=8), EINVAL), (lambda: _gated(N=100, x=P((1 << 20) + 2), ws=NULL), EINVAL),
@@ -52,7 +52,7 @@ def _unpack(codes=A, s=8, exps=A, N=2, C=8, dt=0, y=B):
     (lambda: _grad(dt=5), EDTYPE), (lambda: _grad(act=9), EINVAL), (lambda: _grad(save=0), EINVAL),
     (lambda: _grad(save=3), EINVAL), (lambda: _grad(dwu=None), EINVAL), (lambda: _grad(dwg=None), EINVAL),
     (lambda: _grad(dh=NULL), EINVAL), (lambda: _grad(gate=NULL), EINVAL), (lambda: _grad(up=NULL), EINVAL),
-    (lambda: _grad(save=2, ge=A), EINVAL), (lambda: _grad(s_dh=-8), EINVAL), (lambda: _grad(dt=0, dh=P((1 << 20) + 2)), EINVAL),
+    (lambda: _grad(save=2, ue=None), EINVAL), (lambda: _grad(ge=None), EINVAL), (lambda: _grad(s_dh=-8), EINVAL), (lambda: _grad(dt=0, dh=P((1 << 20) + 2)), EINVAL),
     (lambda: _grad(gate=ODD), EINVAL), (lambda: _grad(dx=ODD), EINVAL), (lambda: _grad(dwg=ODD), EINVAL),
     (lambda: _grad(x=NULL), EINVAL), (lambda: _grad(x=ODD), EINVAL), (lambda: _grad(s_x=-1), EINVAL),
     (lambda: _grad(wg=NULL), EINVAL), (lambda: _grad(s_u=-64), EINVAL), (lambda: _grad(ws=NULL), EINVAL),
@@ -100,7 +100,11 @@ def _i8(*shape):
     return _m(*shape, dtype=torch.int8)
 
 
-S = det.GatedState(_m(2, 6), _m(2, 6))
+def _half(*shape):
+    return det.ScaledHalf(_m(*shape, dtype=torch.float16), _i8(*shape[:-1], (shape[-1] + 31) // 32))
+
+
+S = det.GatedState(_half(2, 6), _half(2, 6))
 
 
 @pytest.mark.parametrize("call,match", [
@@ -120,10 +124,11 @@ S = det.GatedState(_m(2, 6), _m(2, 6))
     (lambda: det.gated_linear(*(torch.zeros(s, dtype=torch.bfloat16) for s in ((2, 4), (6, 4), (6, 4)))), "GPU"),
     (lambda: det.gated_linear_backward(_m(2, 5), _m(2, 4), _m(6, 4), _m(6, 4), S), "dh"),
     (lambda: det.gated_linear_backward(_m(2, 6, dtype=torch.float16), _m(2, 4), _m(6, 4), _m(6, 4), S), "dh"),
-    (lambda: det.gated_linear_backward(_m(2, 6), _m(2, 4), _m(6, 4), _m(6, 4), det.GatedState(_m(2, 6), _m(2, 5))), "gate and up"),
-    (lambda: det.gated_linear_backward(_m(2, 6), _m(2, 4), _m(6, 4), _m(6, 4), det.GatedState(_i8(2, 6), _i8(2, 6))), "gate and up"),
+    (lambda: det.gated_linear_backward(_m(2, 6), _m(2, 4), _m(6, 4), _m(6, 4), det.GatedState(_half(2, 6), _half(2, 5))), "gate and up"),
     (lambda: det.gated_linear_backward(_m(2, 6), _m(2, 4), _m(6, 4), _m(6, 4), det.GatedState(
-        det.PackedInt8(_i8(2, 6), _i8(2, 1)), _m(2, 6))), "gate and up"),
+        det.ScaledHalf(_m(2, 6), _i8(2, 1)), _half(2, 6))), "gate and up"),
+    (lambda: det.gated_linear_backward(_m(2, 6), _m(2, 4), _m(6, 4), _m(6, 4), det.GatedState(
+        det.PackedInt8(_i8(2, 6), _i8(2, 1)), _half(2, 6))), "gate and up"),
     (lambda: det.gated_linear_backward(_m(2, 6), _m(2, 4), _m(6, 4), _m(6, 4), det.GatedState(
         det.PackedInt8(_i8(2, 6), _i8(2, 2)), det.PackedInt8(_i8(2, 6), _i8(2, 1)))), "gate and up"),
     (lambda: det.gated_linear_backward(_m(2, 6), det.PackedInt8(_i8(2, 4), _i8(2, 2)), _m(6, 4), _m(6, 4), S), "packed x"),
@@ -160,7 +165,8 @@ def test_traces_are_refused():
     x = z(2, 4)
     i8 = lambda *s: torch.zeros(s, dtype=torch.int8)
     for call in (lambda x: det.gated_linear(x, z(6, 4), z(6, 4)), lambda x: det.gated_linear_forward(x, z(6, 4), z(6, 4))[0],
-                 lambda x: det.gated_linear_backward(z(2, 6), x, z(6, 4), z(6, 4), det.GatedState(z(2, 6), z(2, 6)))[0],
+                 lambda x: det.gated_linear_backward(z(2, 6), x, z(6, 4), z(6, 4), det.GatedState(
+                     *[det.ScaledHalf(z(2, 6).half(), i8(2, 1))] * 2))[0],
                  lambda x: det.pack_int8(x)[0], lambda x: det.unpack_int8(det.PackedInt8(i8(2, 4), i8(2, 1))) + x):
         with pytest.raises(RuntimeError, match="cannot be traced"):
             torch.jit.trace(call, (x,), check_trace=False)

@@ -51,6 +51,29 @@ def slope64(kind, g):
     return torch.autograd.grad(act64(kind, g).sum(), g)[0]
 
 
+def two(e):
+    """2^e from its bits (pow is off by a unit of 64 bits)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def value(t):
+    """What a kept projection stands for, in 64 bits."""
+    if isinstance(t, det.PackedInt8):
+        return det.unpack_int8(t).double()
+    return t.values.double() * two(t.exponents).repeat_interleave(32, -1)[..., :t.values.shape[-1]]
+
+
+def half64(v):
+    """v (64 bits) as fp16 elements of blocks of 32: (values, exponents)."""
+    N, F = v.shape
+    b = torch.nn.functional.pad(v, (0, -F % 32)).reshape(N, -1, 32)
+    top = torch.where(torch.isfinite(b), b.abs(), 0.0).amax(-1)
+    e = (torch.frexp(top)[1].long() - 15).clamp(min=-126)
+    e = torch.where(top == 0, -126, e)
+    h = (b * two(-e)[..., None]).to(torch.float16)     # a sum of few bits: rounded once
+    return h.reshape(N, -1)[:, :F], e.to(torch.int8)
+
+
 def within(got, want, bound, what):
     bad = ~((got.double() - want).abs() <= bound)
     assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, worst "
@@ -64,8 +87,8 @@ def test_products_are_exact_on_integers(N, C, F):
     x, wg, wu = operands(1, N, C, F, normal=False)
     _, s = det.gated_linear_forward(x, wg, wu)
     for got, w in ((s.gate, wg), (s.up, wu)):
-        want = (x.double() @ w.double().t()).to(F32)           # an integer below 2^24: exact
-        assert torch.equal(got, want.to(BF16))
+        values, exps = half64(x.double() @ w.double().t())
+        assert torch.equal(got.values, values) and torch.equal(got.exponents, exps)
     # the same products where nothing is kept (few tokens take another kernel): act(g) ~ g from 32 on is g
     one = torch.zeros(F, C, device=DEV, dtype=BF16)
     one[:, 0] = 64.0
@@ -122,7 +145,7 @@ def test_gradients_against_64_bits(N, C, F, act, dtype):
     dh = torch.randn(N, F, device=DEV, generator=torch.Generator(device=DEV).manual_seed(4)).to(dtype)
     h, s = det.gated_linear_forward(x, wg, wu, activation=act, out_dtype=dtype)
     got = det.gated_linear_backward(dh, x, wg, wu, s, activation=act)
-    want = reference_grads(act, dh, x, wg, wu, s.gate.double(), s.up.double())
+    want = reference_grads(act, dh, x, wg, wu, value(s.gate), value(s.up))
     for name, t, (v, b) in zip(("dx", "dw_gate", "dw_up"), got, want):
         assert t.dtype == BF16
         within(t, v, b + 1e-37, name)
@@ -166,7 +189,7 @@ def test_int8_checkpoint(N, C, F):
     assert sum(n for d, n in sizes if d != torch.int8) == 2 * F * C        # the weights
     for a, b in zip(torch.autograd.grad(again, leaves, dh), got):
         assert torch.equal(a, b)
-    # a packed x with bfloat16 projections, too
+    # a packed x with projections in 16 bits, too
     _, sb = det.gated_linear_forward(x, wg, wu)
     mixed = det.gated_linear_backward(dh, px, wg, wu, sb)
     plain = det.gated_linear_backward(dh, x, wg, wu, sb)
@@ -238,6 +261,18 @@ def test_rows_that_are_not_finite_stay_by_themselves():
     assert torch.equal(h[rows], clean[rows]) and torch.isnan(h[3]).all() and not torch.isfinite(h[70]).any()
     assert torch.equal(s.gate.codes[rows], s0.gate.codes[rows])
     assert (s.gate.exponents[~rows] == -128).all() and (s.up.exponents[~rows] == -128).all()
+    # in 16 bits an element that is not finite stays by itself
+    wide = wg.clone()
+    wide[7] = float("inf")
+    kept = det.gated_linear_forward(x, wide, wu)[1]
+    fine = det.gated_linear_forward(x, wg, wu)[1]
+    cols = torch.arange(130, device=DEV) != 7
+    assert not torch.isfinite(value(kept.gate)[:, 7]).any()
+    assert ((value(kept.gate) - value(fine.gate)).abs()[:, cols] <= 2.0 ** -10 * value(fine.gate).abs()[:, cols]).all()
+    # sizes that fp16 alone would lose
+    for scale in (2.0 ** 40, 2.0 ** -60):
+        big = det.gated_linear_forward((x.double() * scale).to(BF16), wg, wu)[1]
+        assert torch.equal(big.gate.values, fine.gate.values)
     # large arguments: the activations reach their limits
     wide = torch.full((70, 1), 3.0e4, device=DEV, dtype=BF16)
     one = torch.ones(8, 1, device=DEV, dtype=BF16)
