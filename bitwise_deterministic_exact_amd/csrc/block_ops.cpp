@@ -118,10 +118,15 @@ GatedGrads gated_backward(const Tensor& dh, const Tensor& x, const OptTensor& x_
     g.dwg = at::empty(wg.sizes(), bf16);
     g.dwu = at::empty(wu.sizes(), bf16);
   }
-  const Tensor dh2 = rows(dh), x2 = x_exp ? x.contiguous() : rows(x), g2 = rows(wg), u2 = rows(wu);
+  const Tensor dh2 = rows(dh), x2 = x_exp ? x.contiguous() : wide_rows(x);
+  Tensor g2 = wide_rows(wg), u2 = wide_rows(wu);
+  if (g2.stride(0) != u2.stride(0)) {     // dx runs over both with one stride
+    g2 = g2.contiguous();
+    u2 = u2.contiguous();
+  }
   const Tensor kg = kept.gate.contiguous(), ku = kept.up.contiguous();
   const Tensor xe = x_exp ? x_exp->contiguous() : Tensor(), ge = kept.gate_exp.contiguous(), ue = kept.up_exp.contiguous();
-  const int64_t bytes = det_gated_linear_grad_workspace_bytes(N, C, F, need_dx, need_dw);
+  const int64_t bytes = det_gated_linear_grad_workspace_bytes(N, C, F, need_dx, need_dw, C % 64 == 0, x_exp.has_value());
   const Tensor ws = bytes > 0 ? at::empty({bytes}, x.options().dtype(at::kByte)) : Tensor();
   ok(det_gated_linear_grad(dt_of(dh.scalar_type()), in(dh2), dh2.stride(0), in(x2), x_exp ? C : x2.stride(0),
                            static_cast<const int8_t*>(xe.defined() ? xe.const_data_ptr() : nullptr), in(g2), g2.stride(0), in(u2), u2.stride(0),

@@ -76,29 +76,36 @@ __device__ __forceinline__ void act_times(int act, const float (&g)[4], const fl
 
 // ---------------------------------------------------------------- the matrix product
 //
-// D[b][a] = sum_k A[a][k] B[b][k], both operands with adjacent k and K a
-// multiple of 64.  A workgroup of WA x WB waves owns TA x TB outputs, a wave
-// FA x FB blocks of 16 x 16.  Per step of 64 k the TA + TB rows (128 bytes
-// each) are copied into one of two LDS buffers with 16-byte copies that need
-// no registers, while the other buffer is read.  A row's eight 16-byte pieces
-// lie in its LDS row in the order piece ^ (row & 7), so that the 8 lanes that
-// read a piece of 8 rows at a time hit different banks.
+// D[b][a] = sum_k A[k, a] B[k, b].  An operand lies with adjacent k (rows of A
+// or B, "by row") or with adjacent a or b (rows of k, "by k"): the gradients read
+// x, the weights, dg and du as they lie, with no transposed copy.
 //
-// A step is two halves of one MFMA per block: while a half's MFMAs run, the
-// next half's fragments are read.
-
-enum { MM_GATED, MM_ROWS };
-
+// A workgroup of WA x WB waves owns TA x TB outputs, a wave FA x FB blocks of 16
+// x 16.  A ring of BUFS stages of KS k (32 or 64) in LDS is filled with 16-byte
+// copies that need no registers, BUFS - 1 stages ahead; while the MFMAs of 32 k
+// run (one per block), the next 32's fragments are read.  One barrier per stage.
+//
+// By row: KS k per row, whose 16-byte pieces lie in the order piece ^ swap_row(row),
+// so that the lanes that read one piece of 16 rows hit all banks alike.  A
+// fragment is one 16-byte read.
+// By k: T elements per row of k; a fragment's 16 columns are 32 bytes of 8 rows
+// per lane group, read by two transposing reads of 4 rows each (16 lanes give
+// the addresses of 4 x 16 elements and get 4 of a column each).  The 32-byte
+// pieces lie in the order piece ^ swap(k), again all banks once.
+struct Operand {
+  const void* p; int64_t stride;          // elements between rows (of k, or of a or b)
+  int64_t n;                              // its a or b
+};
 struct MmArgs {
-  const void* A; int64_t s_a;             // MM_GATED: the gate's weights
-  const void* A1; int64_t s_a1;           // MM_GATED: the up projection's
-  const void* B; int64_t s_b;
-  int64_t na, nb;                         // rows of A (MM_GATED: of each half) and of B
-  int K;
+  // a second operand A1 of the same size: the gate's rows are A's, the up
+  // projection's A1's (gated); or k goes over A and then, from `turn` on, over A1
+  Operand A, A1, B;
+  int64_t K;                              // a multiple of 64: what lies past the rows of k is 0
+  int64_t ka, kb, turn;                   // by k: rows of k of A (and of A1), of B
   int64_t tiles_a, tiles_b;
-  // MM_GATED: out is h [nb][na]; MM_ROWS: D itself, rows from `split` on in out1
-  void* out; void* out1; int64_t split;
-  // what the gradients read again (null: nothing)
+  // gated: h [n of B][n of A]; else D, rows [0, split0) in out, [split1, split1 + split0) in out1
+  void* out; void* out1; int64_t split0, split1;
+  // what the gradients read again
   void* gate; void* up;
   int8_t* gate_exp; int8_t* up_exp;
   int dt, act, save;                      // type of out, activation, what gate and up hold
@@ -115,12 +122,6 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("" ::: "memory");
 }
 
-#ifdef __HIP_DEVICE_COMPILE__              // buffer descriptors are a type of the device's alone
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00020000);
-}
-#endif
-
 // Tiles in ranges, one per XCD (workgroups go to the XCDs in turn), and in
 // groups of 8 rows of tiles within: the 32 workgroups that are resident on an
 // XCD cover about 8 x 4 tiles and share their operands in its L2.
@@ -132,13 +133,104 @@ __device__ __forceinline__ void tile_of(int64_t id, int64_t tiles_a, int64_t til
   ta = in / rows;
 }
 
-template <int MODE, int WA, int WB, int FA, int FB>
-__global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__              // buffer descriptors are a type of the device's alone
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00020000);
+}
+using s16x4 = short __attribute__((ext_vector_type(4)));
+using lds_s16x4 = __attribute__((address_space(3))) s16x4;
+
+// One operand's share of a step: T of its a or b, copied by NW waves, read as
+// fragments of 16.
+template <bool BY_K, int T, int NW, int KS>
+struct Tile {
+  static constexpr int COPIES = T * KS / 512 / NW;            // of 1 KiB, per wave and stage
+  static constexpr int BYTES = T * KS * 2;
+  static constexpr int ROWS = 512 / KS, PIECES = KS / 8;      // by row: rows of a copy, pieces of 16 bytes in one
+  static constexpr int LINE = T / 8;                          // by k: pieces of 16 bytes in a row of k
+  // which 32-byte piece of a row of k lies where; 8 rows that are read at once differ in it
+  static __device__ __forceinline__ int swap(int k) {
+    const int s = (k & 3) | ((k >> 1) & 4);
+    return T >= 128 ? s : ((k >> 1) & 1) | ((k >> 2) & 2);
+  }
+  // by row: what a row's pieces are swapped with
+  static __device__ __forceinline__ int swap_row(int r) { return KS == 64 ? r & 7 : (r >> 2) & 3; }
+  int64_t stride;                         // bytes
+  __amdgpu_buffer_rsrc_t buf;             // by row: of the tile
+  int at;                                 // by row: bytes of k before the next stage
+  const char* next;                       // by k: the next stage's first row
+  int left, cols;                         // by k: rows from there on, bytes of a row
+  int from[COPIES];                       // by row: rows past the end are the last one again
+  // `limit` of its a or b from `first` on are the tile's
+  __device__ __forceinline__ void init(const Operand& o, int64_t first, int limit, int64_t K, int64_t rows, int wave, int lane) {
+    stride = o.stride * 2;
+    const int n = static_cast<int>(min<int64_t>(limit, o.n - first));
+    if constexpr (BY_K) {
+      next = static_cast<const char*>(o.p) + first * 2;
+      left = static_cast<int>(rows);
+      cols = (n * 2 + 15) & ~15;          // whole pieces: strides are multiples of 16 bytes
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) {
+        const int at = (wave * COPIES + j) * 64 + lane, k = at / LINE, slot = at % LINE;
+        const int piece = (((slot >> 1) ^ swap(k)) << 1) | (slot & 1);
+        from[j] = k * static_cast<int>(stride) + min(piece, cols / 16 - 1) * 16;         // columns past the end: the last ones
+      }
+    } else {
+      buf = buffer_of(static_cast<const char*>(o.p) + first * stride, (n - 1) * stride + K * 2);
+      at = 0;
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) {
+        const int r = (wave * COPIES + j) * ROWS + lane / PIECES;
+        from[j] = min(r, n - 1) * static_cast<int>(stride) + (((lane % PIECES) ^ swap_row(lane / PIECES)) * 16);
+      }
+    }
+  }
+  // The next stage into LDS at `to`.  By k: rows past the end lie past the end of
+  // the buffer and come as 0.  By row: K is whole; stages past it, which no MFMA
+  // takes, get the next rows' elements or 0.
+  __device__ __forceinline__ void copy(char* to, int wave) {
+    if constexpr (BY_K) {
+      // no branch: one would keep the copies from going between the MFMAs
+      const __amdgpu_buffer_rsrc_t b = buffer_of(next, max(0, (min(left, KS) - 1) * static_cast<int>(stride) + cols));
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b, to + (wave * COPIES + j) * 1024, 16, from[j], 0, 0, 0);
+      next += KS * stride;
+      left -= KS;
+    } else {
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, to + (wave * COPIES + j) * 1024, 16, from[j], at, 0, 0);
+      at += KS * 2;
+    }
+  }
+  // a lane's address of fragment 0, and the fragment that starts at a or b = 16 f
+  static __device__ __forceinline__ int lane_at(int lane) {
+    const int i = lane & 15, q = lane >> 4;
+    if constexpr (BY_K) return (8 * q + (i >> 2)) * T * 2 + swap(8 * q + (i >> 2)) * 32 + (i & 3) * 8;
+    else return i * KS * 2 + ((q ^ swap_row(i)) * 16);
+  }
+  static __device__ __forceinline__ bf16x8 fragment(const char* __restrict__ tile, int at, int f, int half) {
+    if constexpr (BY_K) {
+      const char* const p = tile + half * 32 * T * 2 + (at ^ (f * 32));     // a row of k is a power of two: the bits do not meet
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * T * 2));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *reinterpret_cast<const bf16x8*>(tile + (at ^ (half * 64)) + f * 16 * KS * 2);
+    }
+  }
+};
+#endif
+
+template <bool GATED, bool A_BY_K, bool B_BY_K, int WA, int WB, int FA, int FB, int KS, int BUFS, bool SPREAD>
+__global__ __launch_bounds__(64 * WA * WB, FA * FB > 32 ? 1 : 2) void k_mm(MmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
-  constexpr int NW = WA * WB, TA = WA * FA * 16, TB = WB * FB * 16, TH = MODE == MM_GATED ? TA / 2 : TA;
-  constexpr int CA = TA / 8 / NW, CB = TB / 8 / NW;           // copies (8 rows each) of a wave and step
-  constexpr int BUF = (TA + TB) * 128;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * BUF];
+  constexpr int NW = WA * WB, TA = WA * FA * 16, TB = WB * FB * 16, TH = GATED ? TA / 2 : TA;
+  using TileA = Tile<A_BY_K, TA, NW, KS>;
+  using TileB = Tile<B_BY_K, TB, NW, KS>;
+  constexpr int BUF = TileA::BYTES + TileB::BYTES, COPIES = TileA::COPIES + TileB::COPIES;
+  __shared__ __attribute__((aligned(1024))) char lds[BUFS * BUF];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wa = wave / WB, wb = wave % WB;
@@ -146,51 +238,47 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
   tile_of(blockIdx.x, a.tiles_a, a.tiles_b, ta, tb);
   const int64_t row_a = ta * TH, row_b = tb * TB;
 
-  // where this wave's copies come from: rows past the end are the last one again
-  const bool second = MODE == MM_GATED && wave * CA * 8 >= TH;            // uniform: the up projection's rows
-  const int64_t s_a = second ? a.s_a1 : a.s_a;
-  const char* const pa = static_cast<const char*>(second ? a.A1 : a.A) + row_a * s_a * 2;
-  const char* const pb = static_cast<const char*>(a.B) + row_b * a.s_b * 2;
-  const int rows_a = static_cast<int>(min<int64_t>(TH, a.na - row_a)), rows_b = static_cast<int>(min<int64_t>(TB, a.nb - row_b));
-  const __amdgpu_buffer_rsrc_t ra = buffer_of(pa, (rows_a - 1) * s_a * 2 + static_cast<int64_t>(a.K) * 2);
-  const __amdgpu_buffer_rsrc_t rb = buffer_of(pb, (rows_b - 1) * a.s_b * 2 + static_cast<int64_t>(a.K) * 2);
-  const int piece = ((lane & 7) ^ (lane >> 3)) * 16;
-  int from_a[CA], from_b[CB];
-#pragma unroll
-  for (int j = 0; j < CA; ++j) {
-    const int r = (wave * CA + j) * 8 + (lane >> 3) - (second ? TH : 0);
-    from_a[j] = min(r, rows_a - 1) * static_cast<int>(s_a * 2) + piece;
+  TileA A;
+  TileB B;
+  B.init(a.B, row_b, TB, a.K, a.kb, wave, lane);
+  if constexpr (GATED) {
+    // the tile's first half is the gate's, its second the up projection's: each wave copies rows of one of them
+    static_assert(!A_BY_K && TH % (TileA::ROWS * TileA::COPIES) == 0, "a wave's copies lie in one half");
+    constexpr int HALF = NW / 2;
+    A.init(wave < HALF ? a.A : a.A1, row_a, TH, a.K, 0, wave % HALF, lane);
+  } else {
+    A.init(a.A, row_a, TA, a.K, a.ka, wave, lane);
   }
-#pragma unroll
-  for (int j = 0; j < CB; ++j) {
-    const int r = (wave * CB + j) * 8 + (lane >> 3);
-    from_b[j] = min(r, rows_b - 1) * static_cast<int>(a.s_b * 2) + piece;
-  }
-  auto copy = [&](int k, int buf) {
+  const int stages = static_cast<int>(a.K / KS);
+  int turn_at = static_cast<int>(a.turn / KS);                // stages until A1 follows
+  const char* const second = static_cast<const char*>(a.A1.p) + row_a * 2;
+  // the next stage of both operands
+  auto copy = [&](int buf) {
     char* const to = lds + buf * BUF;
-#pragma unroll
-    for (int j = 0; j < CA; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to + (wave * CA + j) * 1024, 16, from_a[j], k * 2, 0, 0);
-#pragma unroll
-    for (int j = 0; j < CB; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to + TA * 128 + (wave * CB + j) * 1024, 16, from_b[j], k * 2, 0, 0);
+    if constexpr (A_BY_K) {
+      const bool now = turn_at == 0;
+      A.next = now ? second : A.next;
+      A.left = now ? static_cast<int>(a.ka) : A.left;
+      --turn_at;
+    }
+    A.copy(to, wave);
+    B.copy(to + TileA::BYTES, wave);
   };
-
-  // the first LDS row of fragment i of A (of this wave)
+  // the first row of A's tile of fragment i of this wave
   auto frag_row = [&](int i) {
-    if constexpr (MODE == MM_GATED) return (i < FA / 2 ? 0 : TH) + wa * FA * 8 + (i % (FA / 2)) * 16;
+    if constexpr (GATED) return (i < FA / 2 ? 0 : TH) + wa * FA * 8 + (i % (FA / 2)) * 16;
     else return (wa * FA + i) * 16;
   };
-  const int in_row = (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) * 16);   // the second half: ^ 64
+  const int at_a = TileA::lane_at(lane), at_b = TileB::lane_at(lane);
   struct Frags {
     bf16x8 fa[FA], fb[FB];
   };
   auto read = [&](Frags& f, int buf, int half) {
-    const char* const at = lds + buf * BUF + (in_row ^ (half * 64));
+    const char* const tile = lds + buf * BUF;
 #pragma unroll
-    for (int j = 0; j < FB; ++j) f.fb[j] = *reinterpret_cast<const bf16x8*>(at + TA * 128 + (wb * FB + j) * 2048);
+    for (int j = 0; j < FB; ++j) f.fb[j] = TileB::fragment(tile + TileA::BYTES, at_b, wb * FB + j, half);
 #pragma unroll
-    for (int i = 0; i < FA; ++i) f.fa[i] = *reinterpret_cast<const bf16x8*>(at + frag_row(i) * 128);
+    for (int i = 0; i < FA; ++i) f.fa[i] = TileA::fragment(tile, at_a, frag_row(i) / 16, half);
   };
   f32x4 acc[FA][FB];
 #pragma unroll
@@ -204,29 +292,62 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
       for (int j = 0; j < FB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.fa[i], f.fb[j], acc[i][j], 0, 0, 0);
   };
 
-  const int steps = a.K / 64;
   Frags f0, f1;
-  copy(0, 0);
-  __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));
+#pragma unroll
+  for (int s = 0; s < BUFS; ++s) copy(s);
+  __builtin_amdgcn_s_waitcnt(waitcnt((BUFS - 1) * COPIES, 15));
   step_barrier();
   read(f0, 0, 0);
-  copy(min(1, steps - 1) * 64, 1);
-  __builtin_amdgcn_sched_barrier(0);
-  for (int s = 0; s < steps; ++s) {
-    const int buf = s & 1;
-    read(f1, buf, 1);
+  // SPREAD: the reads and copies go between the MFMAs.  Else they go before them:
+  // then one of a SIMD's two waves reads while the other multiplies.
+  constexpr int MFMAS = FA * FB, READS = FA * (A_BY_K ? 2 : 1) + FB * (B_BY_K ? 2 : 1);
+  auto run = [&](const Frags& now, auto copies) {
+    if constexpr (SPREAD) {
+      constexpr int C = decltype(copies)::value, PER = MFMAS - C > READS ? (MFMAS - C) / READS : 1;
+      multiply(now);
+#pragma unroll
+      for (int r = 0; r < READS; ++r) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // a read of the LDS
+        __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);  // MFMAs
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);    // a copy, behind the reads: both are LDS accesses
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+    } else {
+      __builtin_amdgcn_sched_barrier(0);
+      //PRIO1
+      multiply(now);
+      //PRIO0
+    }
     __builtin_amdgcn_sched_barrier(0);
-    multiply(f0);
-    __builtin_amdgcn_sched_barrier(0);
-    // this buffer's reads are done and the other buffer's copies have landed, for every wave
-    __builtin_amdgcn_s_waitcnt(waitcnt(0, 0));
+  };
+  int buf = 0;                            // of the stage whose last MFMAs run
+  // the last MFMAs of a stage, while the next one's first fragments are read
+  auto turn = [&](const Frags& now, Frags& then) {
+    // this wave's reads of the stage are done and its copies of the next one have landed; then every wave's
+    __builtin_amdgcn_s_waitcnt(waitcnt((BUFS - 2) * COPIES, 0));
     step_barrier();
-    read(f0, buf ^ 1, 0);                 // after the last step: read again, not used
+    const int next = buf + 1 == BUFS ? 0 : buf + 1;
     __builtin_amdgcn_sched_barrier(0);
-    copy(min(s + 2, steps - 1) * 64, buf);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(f1);
-    __builtin_amdgcn_sched_barrier(0);
+    read(then, next, 0);                  // after the last stage: not used
+    copy(buf);
+    run(now, std::integral_constant<int, COPIES>{});
+    buf = next;
+  };
+  if constexpr (KS == 32) {
+    for (int s = 0; s < stages; s += 2) { // K is a multiple of 64
+      turn(f0, f1);
+      turn(f1, f0);
+    }
+  } else {
+    for (int s = 0; s < stages; ++s) {
+      __builtin_amdgcn_sched_barrier(0);
+      read(f1, buf, 1);
+      run(f0, std::integral_constant<int, 0>{});
+      turn(f1, f0);
+    }
   }
   __builtin_amdgcn_s_waitcnt(waitcnt(0, 0));                  // no copy or read of these buffers is left
   step_barrier();
@@ -243,26 +364,28 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
     for (int i = 0; i < FA; ++i)
       *reinterpret_cast<f32x4*>(own + (lane & 15) * ROW + i * 16 + 4 * (lane >> 4)) = acc[i][j];
     wave_sync();
-    constexpr int LANES = (MODE == MM_GATED ? FA / 2 : FA) * 4;           // lanes to a row
+    constexpr int LANES = (GATED ? FA / 2 : FA) * 4;           // lanes to a row
     const int64_t c = row_a + wa * (LANES * 4) + (lane % LANES) * 4;
-    const int n = static_cast<int>(min<int64_t>(4, a.na - c));
+    const int64_t na = a.A.n;
+    const int n = static_cast<int>(min<int64_t>(4, na - c));
 #pragma unroll 1
     for (int r0 = 0; r0 < 16; r0 += 64 / LANES) {
       const int r = r0 + lane / LANES;
       const int64_t b = row_b + (wb * FB + j) * 16 + r;
-      const int in = b < a.nb ? n : 0;
+      const int in = b < a.B.n ? n : 0;
       const float* const from = own + r * ROW + (lane % LANES) * 4;
       const f32x4 first = *reinterpret_cast<const f32x4*>(from);
-      if constexpr (MODE == MM_ROWS) {
+      if constexpr (!GATED) {
         const float v[4] = {first[0], first[1], first[2], first[3]};
-        const bool hi = b >= a.split;
-        store4(a.dt, hi ? a.out1 : a.out, (hi ? b - a.split : b) * a.na + c, v, in);
+        const bool hi = b >= a.split1;
+        const int64_t row = hi ? b - a.split1 : b;
+        store4(a.dt, hi ? a.out1 : a.out, row * na + c, v, row < a.split0 ? in : 0);
       } else {
         const f32x4 upper = *reinterpret_cast<const f32x4*>(from + FA * 8);
         const float g[4] = {first[0], first[1], first[2], first[3]}, u[4] = {upper[0], upper[1], upper[2], upper[3]};
         float h[4];
         act_times(a.act, g, u, h);
-        store4(a.dt, a.out, b * a.na + c, h, in);
+        store4(a.dt, a.out, b * na + c, h, in);
         if (a.save != DET_SAVE_NONE) {
           // 8 lanes hold a block of 32 features; those past the end count as 0
           const bool int8 = a.save == DET_SAVE_INT8;
@@ -277,7 +400,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
           tu = top_of_8(tu);
           const bool bad_g = not_finite(tg), bad_u = not_finite(tu);        // int8 alone
           const int eg = int8 ? block_exponent(tg) : half_exponent(tg), eu = int8 ? block_exponent(tu) : half_exponent(tu);
-          const int64_t blocks = (a.na + 31) / 32, at = b * a.na + c;
+          const int64_t blocks = (na + 31) / 32, at = b * na + c;
           if ((lane & 7) == 0 && in > 0) {
             a.gate_exp[b * blocks + c / 32] = static_cast<int8_t>(bad_g ? DET_INT8_NAN : eg);
             a.up_exp[b * blocks + c / 32] = static_cast<int8_t>(bad_u ? DET_INT8_NAN : eu);
@@ -394,130 +517,84 @@ __global__ __launch_bounds__(64, 2) void k_few(FewArgs a) {
 }
 
 // ---------------------------------------------------------------- the gradients' operands
-//
-// Tiles of 64 x 64, 4 x 4 elements to a thread; what is needed with the other
-// index adjacent goes through LDS (68 elements to a row: 8-byte accesses of 16
-// rows fall in different banks).
 
-constexpr int TILE = 64, TILE_ROW = 68;
-
-struct Tile {
-  uint16_t v[TILE][TILE_ROW];
-};
-// element (r, c) of the thread's 4 x 4, from (4 tr, 4 tc) of the tile, into row c, column r
-__device__ __forceinline__ void turn(Tile& t, int tr, int tc, const float (&v)[4][4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<u32x2*>(&t.v[4 * tc + c][4 * tr]) = u32x2{pack_bf16(v[0][c], v[1][c]), pack_bf16(v[2][c], v[3][c])};
-}
-// the turned tile's rows [0, rows) at dst (element (0, 0)), `cols` of each
-__device__ __forceinline__ void write_turned(const Tile& t, char* dst, int64_t stride, int rows, int cols) {
-  const int c = (threadIdx.x & 15) * 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 16 + (threadIdx.x >> 4);
-    if (r < rows && c < cols)             // cols is a multiple of 4
-      *reinterpret_cast<u32x2_a2*>(dst + (r * stride + c) * 2) = *reinterpret_cast<const u32x2*>(&t.v[r][c]);
-  }
+// i / per where both fit 32 bits (a division in 64 costs tens of instructions)
+__device__ __forceinline__ int64_t row_of(int64_t i, int64_t per) {
+  return i <= 0xFFFFFFFFll ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per) : i / per;
 }
 
 struct GateGradArgs {
   const void* dh; int64_t s_dh; int dh_dt;
   const void* gate; const void* up;       // [N][F] halves or codes
   const int8_t* gate_exp; const int8_t* up_exp;
-  int64_t N, F, Fp, Np;
+  int64_t N, F, Fp;
   int act, save;
-  char* rows;                             // [N][2 Fp]: dg and du, zeros from F to Fp; null: not needed
-  char* turned;                           // [2 F][Np]: the same by feature, zeros from N to Np
+  uint16_t* rows;                         // [N][2 Fp]: dg and du, zeros from F to Fp
 };
 
 // dg and du, rounded to bf16 for the matrix cores (each off by at most half a
-// unit; the sums they enter are fp32)
+// unit; the sums they enter are fp32).  A thread takes 8 adjacent features.
+template <int ACT>
 __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
-  __shared__ Tile tg, tu;
-  const int64_t f0 = static_cast<int64_t>(blockIdx.y) * TILE, b0 = static_cast<int64_t>(blockIdx.x) * TILE;
-  const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
-  const int64_t f = f0 + 4 * tc;
-  const int n = static_cast<int>(min<int64_t>(4, a.F - f));
-  const int64_t blocks = (a.F + 31) / 32;
-  float dg[4][4], du[4][4];
+  const int64_t per = a.Fp / 8, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= a.N * per) return;
+  const int64_t b = row_of(i, per), f0 = (i - b * per) * 8, blocks = (a.F + 31) / 32;
+  const float ug = f0 < a.F ? unit_of(a.gate_exp[b * blocks + f0 / 32]) : 0.0f;
+  const float uu = f0 < a.F ? unit_of(a.up_exp[b * blocks + f0 / 32]) : 0.0f;
+  float dh[2][4], g[2][4], u[2][4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t b = b0 + 4 * tr + r;
-    const int in = b < a.N ? n : 0;
-    float dh[4], g[4], u[4];
-    load4(a.dh_dt, a.dh, b * a.s_dh + f, dh, in);
-    const float ug = in > 0 ? unit_of(a.gate_exp[b * blocks + f / 32]) : 0.0f;
-    const float uu = in > 0 ? unit_of(a.up_exp[b * blocks + f / 32]) : 0.0f;
+  for (int h = 0; h < 2; ++h) {
+    const int64_t f = f0 + 4 * h, at = b * a.F + f;
+    const int in = static_cast<int>(min<int64_t>(4, a.F - f));
+    load4(a.dh_dt, a.dh, b * a.s_dh + f, dh[h], in);
     if (a.save == DET_SAVE_INT8) {
-      values_of(load_codes(static_cast<const int8_t*>(a.gate) + b * a.F + f, in), ug, g);
-      values_of(load_codes(static_cast<const int8_t*>(a.up) + b * a.F + f, in), uu, u);
+      values_of(load_codes(static_cast<const int8_t*>(a.gate) + at, in), ug, g[h]);
+      values_of(load_codes(static_cast<const int8_t*>(a.up) + at, in), uu, u[h]);
     } else {
-      load_halves(static_cast<const uint16_t*>(a.gate) + b * a.F + f, ug, g, in);
-      load_halves(static_cast<const uint16_t*>(a.up) + b * a.F + f, uu, u, in);
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      Act t;
-      if (a.act == DET_ACT_SILU) t = act_of<DET_ACT_SILU>(g[c]);
-      else if (a.act == DET_ACT_GELU_TANH) t = act_of<DET_ACT_GELU_TANH>(g[c]);
-      else t = act_of<DET_ACT_GELU>(g[c]);
-      const bool inside = c < in;
-      dg[r][c] = inside ? dh[c] * u[c] * t.d : 0.0f;
-      du[r][c] = inside ? dh[c] * t.a : 0.0f;
-    }
-    if (a.rows != nullptr && b < a.N && f < a.Fp) {           // Fp is a multiple of 4
-      store_vec<DET_BF16, 4>(a.rows, b * 2 * a.Fp + f, dg[r]);
-      store_vec<DET_BF16, 4>(a.rows, b * 2 * a.Fp + a.Fp + f, du[r]);
+      load_halves(static_cast<const uint16_t*>(a.gate) + at, ug, g[h], in);
+      load_halves(static_cast<const uint16_t*>(a.up) + at, uu, u[h], in);
     }
   }
-  if (a.turned == nullptr) return;        // uniform
-  turn(tg, tr, tc, dg);
-  turn(tu, tr, tc, du);
-  __syncthreads();
-  const int rows = static_cast<int>(min<int64_t>(TILE, a.F - f0)), cols = static_cast<int>(min<int64_t>(TILE, a.Np - b0));
-  write_turned(tg, a.turned + (f0 * a.Np + b0) * 2, a.Np, rows, cols);
-  write_turned(tu, a.turned + ((a.F + f0) * a.Np + b0) * 2, a.Np, rows, cols);
-}
-
-struct TurnArgs {
-  const void* src; int64_t s_src;         // [R][C], bf16 or codes with exponents
-  const int8_t* exps;
-  int64_t R, C, Rp;
-  char* dst; int64_t s_dst;               // [C][Rp]: zeros from R to Rp, a multiple of 4
-};
-__global__ __launch_bounds__(256) void k_turn(TurnArgs a) {
-  __shared__ Tile t;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * TILE, r0 = static_cast<int64_t>(blockIdx.x) * TILE;
-  const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
-  const int64_t c = c0 + 4 * tc;
-  const int n = static_cast<int>(min<int64_t>(4, a.C - c));
-  float v[4][4];
+  float dg[8], du[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = r0 + 4 * tr + i;
-    const int in = r < a.R ? n : 0;
-    if (a.exps != nullptr) {
-      const float unit = in > 0 ? unit_of(a.exps[r * ((a.C + 31) / 32) + c / 32]) : 0.0f;
-      values_of(load_codes(static_cast<const int8_t*>(a.src) + r * a.s_src + c, in), unit, v[i]);
-    } else {
-      load4(DET_BF16, a.src, r * a.s_src + c, v[i], in);
-    }
+  for (int c = 0; c < 8; ++c) {
+    const Act t = act_of<ACT>(g[c / 4][c % 4]);
+    const bool inside = f0 + c < a.F;
+    dg[c] = inside ? dh[c / 4][c % 4] * u[c / 4][c % 4] * t.d : 0.0f;
+    du[c] = inside ? dh[c / 4][c % 4] * t.a : 0.0f;
   }
-  turn(t, tr, tc, v);
-  __syncthreads();
-  write_turned(t, a.dst + (c0 * a.s_dst + r0) * 2, a.s_dst, static_cast<int>(min<int64_t>(TILE, a.C - c0)),
-               static_cast<int>(min<int64_t>(TILE, a.Rp - r0)));
+  store_vec<DET_BF16, 8>(a.rows, b * 2 * a.Fp + f0, dg);
+  store_vec<DET_BF16, 8>(a.rows, b * 2 * a.Fp + a.Fp + f0, du);
 }
 
 // rows of C elements as rows of Cp, the rest zeros
 __global__ __launch_bounds__(256) void k_pad(const void* src, int64_t s_src, int64_t R, int64_t C, int64_t Cp, void* dst) {
   const int64_t per = Cp / 8, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= R * per) return;
-  const int64_t r = i / per;
-  const int c = static_cast<int>(i % per) * 8;
+  const int64_t r = row_of(i, per);
+  const int c = static_cast<int>(i - r * per) * 8;
   const bf16x8 v = fragment(static_cast<const char*>(src) + r * s_src * 2, c, static_cast<int>(C));
   *reinterpret_cast<bf16x8*>(static_cast<char*>(dst) + i * 16) = v;
+}
+
+// the same from codes
+__global__ __launch_bounds__(256) void k_unpack_pad(const int8_t* src, int64_t s_src, const int8_t* exps, int64_t R, int64_t C,
+                                                    int64_t Cp, void* dst) {
+  const int64_t per = Cp / 8, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= R * per) return;
+  const int64_t r = row_of(i, per);
+  const int c = static_cast<int>(i - r * per) * 8;
+  const float unit = c < C ? unit_of(exps[r * ((C + 31) / 32) + c / 32]) : 0.0f;
+  float v[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int in = static_cast<int>(min<int64_t>(4, C - c - 4 * h));
+    float q[4];
+    values_of(load_codes(src + r * s_src + c + 4 * h, in), unit, q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * h + e] = e < in ? q[e] : 0.0f;
+  }
+  store_vec<DET_BF16, 8>(dst, i * 8, v);
 }
 
 __global__ __launch_bounds__(256) void k_clear(uint16_t* p, int64_t n) {
@@ -533,61 +610,45 @@ constexpr int64_t STRIDE_MAX = 1 << 22;   // 256 rows lie within 2^31 bytes: off
 int64_t up_to(int64_t v, int64_t m) { return ceil_div(v, m) * m; }
 int64_t room(int64_t bytes) { return up_to(bytes, 256); }
 
-// whether the copies of the matrix product can take this operand as it lies
+// whether the copies of the matrix product can take rows of K elements as they lie
 bool direct(const void* p, int64_t stride, int64_t K) {
   return K % 64 == 0 && stride % 8 == 0 && stride >= K && stride <= STRIDE_MAX && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-template <int MODE>
-void launch_mm(MmArgs a, hipStream_t s) {
-  constexpr int half = MODE == MM_GATED ? 2 : 1;
-  // tiles of 256 x 256 (one workgroup per CU) where they fill the chip, else of 128 x 128
-  const int64_t large = ceil_div(a.na * half, 256) * ceil_div(a.nb, 256);
-  if (large >= 256) {
-    a.tiles_a = ceil_div(a.na * half, 256);
-    a.tiles_b = ceil_div(a.nb, 256);
-    hipLaunchKernelGGL((k_mm<MODE, 2, 4, 8, 4>), dim3(static_cast<unsigned>(a.tiles_a * a.tiles_b)), dim3(512), 0, s, a);
+template <bool GATED, bool A_BY_K, bool B_BY_K, int WA, int WB, int FA, int FB, int KS, int BUFS, bool SPREAD>
+void launch_tiles(MmArgs a, hipStream_t s) {
+  a.tiles_a = ceil_div(a.A.n, WA * FA * 16 / (GATED ? 2 : 1));
+  a.tiles_b = ceil_div(a.B.n, WB * FB * 16);
+  hipLaunchKernelGGL((k_mm<GATED, A_BY_K, B_BY_K, WA, WB, FA, FB, KS, BUFS, SPREAD>), dim3(static_cast<unsigned>(a.tiles_a * a.tiles_b)),
+                     dim3(64 * WA * WB), 0, s, a);
+}
+template <bool GATED, bool A_BY_K, bool B_BY_K>
+void launch_mm(const MmArgs& a, hipStream_t s) {
+  const int64_t na = a.A.n * (GATED ? 2 : 1), nb = a.B.n;
+  if (ceil_div(na, 256) * ceil_div(nb, 256) >= 128) {
+    if constexpr (A_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 32, 5, true>(a, s); //BIGK
+    else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 64, 2, false>(a, s); //BIGR
+  } else if (ceil_div(na, 128) * ceil_div(nb, 128) >= 256) {
+    launch_tiles<GATED, A_BY_K, B_BY_K, 2, 2, 4, 4, 32, 5, true>(a, s); //MID
   } else {
-    a.tiles_a = ceil_div(a.na * half, 128);
-    a.tiles_b = ceil_div(a.nb, 128);
-    hipLaunchKernelGGL((k_mm<MODE, 2, 2, 4, 4>), dim3(static_cast<unsigned>(a.tiles_a * a.tiles_b)), dim3(256), 0, s, a);
+    launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 32, 5, true>(a, s); //SMALL
   }
 }
 
-// p as an operand of the matrix product: itself, or a padded copy at ws (which advances)
-const void* operand(const void* p, int64_t& stride, int64_t R, int64_t K, char*& ws, hipStream_t s) {
-  if (direct(p, stride, K)) return p;
+unsigned blocks_for(int64_t threads) { return static_cast<unsigned>(ceil_div(threads, 256)); }
+
+// a padded copy of R rows of K elements at ws (which advances)
+const void* padded(const void* p, int64_t& stride, int64_t R, int64_t K, char*& ws, hipStream_t s) {
   const int64_t Kp = up_to(K, 64);
   void* const to = ws;
   ws += room(R * Kp * 2);
-  hipLaunchKernelGGL(k_pad, dim3(static_cast<unsigned>(ceil_div(R * (Kp / 8), 256))), dim3(256), 0, s, p, stride, R, K, Kp, to);
+  hipLaunchKernelGGL(k_pad, dim3(blocks_for(R * (Kp / 8))), dim3(256), 0, s, p, stride, R, K, Kp, to);
   stride = Kp;
   return to;
 }
-
-struct GradRoom {
-  int64_t rows, turned, x, w, total;
-};
-GradRoom grad_room(int64_t N, int64_t C, int64_t F, bool need_dx, bool need_dw) {
-  const int64_t Fp = up_to(F, 32), Np = up_to(N, 64);
-  GradRoom r{};
-  if (need_dx) {
-    r.rows = room(N * 2 * Fp * 2);
-    r.w = room(C * 2 * Fp * 2);
-  }
-  if (need_dw) {
-    r.turned = room(2 * F * Np * 2);
-    r.x = room(C * Np * 2);
-  }
-  r.total = r.rows + r.turned + r.x + r.w;
-  return r;
-}
-
-void turn_rows(const void* src, int64_t s_src, const int8_t* exps, int64_t R, int64_t C, int64_t Rp, char* dst,
-               int64_t s_dst, hipStream_t s) {
-  TurnArgs a{src, s_src, exps, R, C, Rp, dst, s_dst};
-  hipLaunchKernelGGL(k_turn, dim3(static_cast<unsigned>(ceil_div(Rp, TILE)), static_cast<unsigned>(ceil_div(C, TILE))),
-                     dim3(256), 0, s, a);
+// p as an operand of the matrix product: itself, or a padded copy
+const void* operand(const void* p, int64_t& stride, int64_t R, int64_t K, char*& ws, hipStream_t s) {
+  return direct(p, stride, K) ? p : padded(p, stride, R, K, ws, s);
 }
 
 bool known_act(int act) { return act == DET_ACT_SILU || act == DET_ACT_GELU || act == DET_ACT_GELU_TANH; }
@@ -654,20 +715,24 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
   if ((st = check_workspace(workspace, workspace_bytes, need)) != DET_OK) return st;
   char* ws = static_cast<char*>(workspace);
   MmArgs a{};
-  a.s_a = s_gate; a.s_a1 = s_up; a.s_b = s_x;
-  a.A = operand(w_gate, a.s_a, F, C, ws, s);
-  a.A1 = operand(w_up, a.s_a1, F, C, ws, s);
-  a.B = operand(x, a.s_b, N, C, ws, s);
-  a.na = F; a.nb = N; a.K = static_cast<int>(Cp);
+  a.A = {w_gate, s_gate, F};
+  a.A1 = {w_up, s_up, F};
+  a.B = {x, s_x, N};
+  for (Operand* o : {&a.A, &a.A1, &a.B}) o->p = operand(o->p, o->stride, o->n, C, ws, s);
+  a.K = Cp;
   a.out = h; a.dt = h_dt; a.act = act; a.save = save;
   a.gate = gate; a.up = up; a.gate_exp = gate_exp; a.up_exp = up_exp;
-  launch_mm<MM_GATED>(a, s);
+  launch_mm<true, false, false>(a, s);
   return hip_check(hipGetLastError(), "gated projection launch");
 }
 
-int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, int need_dx, int need_dw) {
-  if (N <= 0 || C <= 0 || F <= 0 || N > DET_ROWS_MAX || C > DET_GATED_MAX || F > DET_GATED_MAX) return 0;
-  return grad_room(N, C, F, need_dx != 0, need_dw != 0).total;
+int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, int need_dx, int need_dw, int aligned,
+                                              int packed) {
+  if (N <= 0 || C <= 0 || F <= 0 || N > DET_ROWS_MAX || C > DET_GATED_MAX || F > DET_GATED_MAX || (!need_dx && !need_dw)) return 0;
+  const int64_t Cp = up_to(C, 64);
+  const bool as_is = C % 64 == 0 && aligned;
+  return room(N * 2 * up_to(F, 64) * 2) + (need_dx && !as_is ? 2 * room(F * Cp * 2) : 0) +
+         (need_dw && (packed || !as_is) ? room(N * Cp * 2) : 0);
 }
 
 det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, const void* x, int64_t s_x,
@@ -702,38 +767,49 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
     if (x == nullptr || s_x < 0) return fail(DET_EINVAL, "null x or negative stride");
     if (x_exp == nullptr && !aligned_for(x, DET_BF16)) return fail(DET_EINVAL, "x must be aligned to its element size");
   }
-  const GradRoom r = grad_room(N, C, F, need_dx, need_dw);
-  if ((st = check_workspace(workspace, workspace_bytes, r.total)) != DET_OK) return st;
-  char* const ws = static_cast<char*>(workspace);
-  const int64_t Fp = up_to(F, 32), Np = up_to(N, 64);
+  const int64_t Cp = up_to(C, 64), Fp = up_to(F, 64), rows = room(N * 2 * Fp * 2);
+  const bool codes = need_dw && x_exp != nullptr;
+  // k runs over both weights with one stride
+  const bool copy_w = !direct(w_gate, s_gate, C) || !direct(w_up, s_up, C) || s_gate != s_up;
+  const int64_t need = rows + (need_dx && copy_w ? 2 * room(F * Cp * 2) : 0) +
+                       (need_dw && (codes || !direct(x, s_x, C)) ? room(N * Cp * 2) : 0);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != DET_OK) return st;
+  char* ws = static_cast<char*>(workspace) + rows;
   GateGradArgs g{};
   g.dh = dh; g.s_dh = s_dh; g.dh_dt = dh_dt;
   g.gate = gate; g.up = up; g.gate_exp = gate_exp; g.up_exp = up_exp;
-  g.N = N; g.F = F; g.Fp = Fp; g.Np = Np; g.act = act; g.save = save;
-  g.rows = need_dx ? ws : nullptr;
-  g.turned = need_dw ? ws + r.rows : nullptr;
-  hipLaunchKernelGGL(k_gate_grad, dim3(static_cast<unsigned>(ceil_div(Np, TILE)), static_cast<unsigned>(ceil_div(Fp, TILE))),
-                     dim3(256), 0, s, g);
-  if (need_dx) {
-    char* const wt = ws + r.rows + r.turned + r.x;
-    turn_rows(w_gate, s_gate, nullptr, F, C, Fp, wt, 2 * Fp, s);
-    turn_rows(w_up, s_up, nullptr, F, C, Fp, wt + Fp * 2, 2 * Fp, s);
+  g.N = N; g.F = F; g.Fp = Fp; g.save = save;
+  g.rows = static_cast<uint16_t*>(workspace);
+  const dim3 grid(blocks_for(N * (Fp / 8)));
+  if (act == DET_ACT_SILU) hipLaunchKernelGGL(k_gate_grad<DET_ACT_SILU>, grid, dim3(256), 0, s, g);
+  else if (act == DET_ACT_GELU_TANH) hipLaunchKernelGGL(k_gate_grad<DET_ACT_GELU_TANH>, grid, dim3(256), 0, s, g);
+  else hipLaunchKernelGGL(k_gate_grad<DET_ACT_GELU>, grid, dim3(256), 0, s, g);
+  if (need_dx) {                          // dx [N][C]: k over the gate's features, then over the up projection's
     MmArgs a{};
-    a.A = wt; a.s_a = 2 * Fp; a.na = C;
-    a.B = ws; a.s_b = 2 * Fp; a.nb = N;
-    a.K = static_cast<int>(2 * Fp);
-    a.out = dx; a.split = N; a.dt = DET_BF16;
-    launch_mm<MM_ROWS>(a, s);
+    a.A = {w_gate, s_gate, C};
+    a.A1 = {w_up, s_up, C};
+    if (copy_w)
+      for (Operand* o : {&a.A, &a.A1}) o->p = padded(o->p, o->stride, F, C, ws, s);
+    a.B = {workspace, 2 * Fp, N};
+    a.K = 2 * Fp; a.ka = F; a.turn = Fp;
+    a.out = dx; a.split0 = a.split1 = N; a.dt = DET_BF16;
+    launch_mm<false, true, false>(a, s);
   }
-  if (need_dw) {
-    char* const xt = ws + r.rows + r.turned;
-    turn_rows(x, s_x, x_exp, N, C, Np, xt, Np, s);
+  if (need_dw) {                          // dw [2 F][C]: k over the rows
     MmArgs a{};
-    a.A = xt; a.s_a = Np; a.na = C;
-    a.B = ws + r.rows; a.s_b = Np; a.nb = 2 * F;
-    a.K = static_cast<int>(Np);
-    a.out = dw_gate; a.out1 = dw_up; a.split = F; a.dt = DET_BF16;
-    launch_mm<MM_ROWS>(a, s);
+    a.A = {x, s_x, C};
+    if (codes) {
+      hipLaunchKernelGGL(k_unpack_pad, dim3(blocks_for(N * (Cp / 8))), dim3(256), 0, s, static_cast<const int8_t*>(x), s_x, x_exp,
+                         N, C, Cp, static_cast<void*>(ws));
+      a.A = {ws, Cp, C};
+    } else {
+      a.A.p = operand(x, a.A.stride, N, C, ws, s);
+    }
+    a.A1 = a.A;
+    a.B = {workspace, 2 * Fp, 2 * Fp};
+    a.K = a.turn = up_to(N, 64); a.ka = a.kb = N;
+    a.out = dw_gate; a.out1 = dw_up; a.split0 = F; a.split1 = Fp; a.dt = DET_BF16;
+    launch_mm<false, true, true>(a, s);
   }
   return hip_check(hipGetLastError(), "gated projection gradient launch");
 }

@@ -599,12 +599,15 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
  *   dx                [N][C] bf16 contiguous; null: not needed
  *   dw_gate, dw_up    [F][C] bf16 contiguous; both null: not needed
  *   workspace         det_gated_linear_grad_workspace_bytes(N, C, F, dx != null,
- *                     dw_gate != null), 256-byte aligned
+ *                     dw_gate != null, aligned, x_exp != null), 256-byte
+ *                     aligned; `aligned` as above, and both weights have one
+ *                     stride
  * Each gradient is an fp32 sum in one fixed order, rounded once: dx over the
  * features of the gate, then of up; the weights' over the rows in ascending
  * order, so these depend on how rows are cut into calls.
  */
-int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, int need_dx, int need_dw);
+int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, int need_dx, int need_dw, int aligned,
+                                              int packed);
 
 det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, const void* x, int64_t s_x,
                                  const int8_t* x_exp, const void* w_gate, int64_t s_gate, const void* w_up,

@@ -86,10 +86,13 @@ def test_workspace_sizes():
     assert fwd(65, 100, 96, 0, 1) == 65 * 128 * 2 + 2 * 96 * 128 * 2
     assert fwd(64, 100, 96, 1, 1) == 64 * 128 * 2 + 2 * 96 * 128 * 2
     assert fwd(1000, 128, 96, 0, 0) == 1000 * 256 + 2 * 96 * 256
-    # dg and du by token and by feature, x and the weights by feature
-    assert grad(64, 128, 96, 1, 0) == 64 * 192 * 2 + 128 * 192 * 2
-    assert grad(65, 128, 100, 0, 1) == 200 * 128 * 2 + 128 * 128 * 2
-    assert grad(0, 128, 96, 1, 1) == 0 and fwd(10, 0, 8, 0, 0) == 0 and grad(10, 8, 1 << 17, 1, 1) == 0
+    # dg and du with rows of a multiple of 64 each, copies where an operand does not lie as wanted, x where it is packed
+    assert grad(64, 128, 96, 1, 1, 1, 0) == 64 * 2 * 128 * 2
+    assert grad(64, 128, 96, 1, 1, 0, 0) == 64 * 2 * 128 * 2 + 2 * 96 * 256 + 64 * 256
+    assert grad(65, 100, 128, 0, 1, 1, 0) == 65 * 2 * 128 * 2 + 65 * 128 * 2
+    assert grad(64, 128, 96, 1, 1, 1, 1) == 64 * 2 * 128 * 2 + 64 * 256
+    assert grad(0, 128, 96, 1, 1, 1, 0) == 0 and fwd(10, 0, 8, 0, 0) == 0 and grad(10, 8, 1 << 17, 1, 1, 1, 0) == 0
+    assert grad(10, 8, 8, 0, 0, 0, 0) == 0
 
 
 def _m(*shape, dtype=torch.bfloat16):
