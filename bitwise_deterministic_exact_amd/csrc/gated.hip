@@ -422,10 +422,12 @@ __global__ __launch_bounds__(64 * WA * WB, FA * FB > 32 ? 1 : 2) void k_mm(MmArg
 
 // ---------------------------------------------------------------- few tokens
 //
-// Up to 64 tokens: the weights' bytes bound it.  A wave owns 16 features, reads
-// their gate and up rows straight into fragments (16 bytes to a lane, UN steps
-// of 32 k ahead) and multiplies them with up to four blocks of 16 tokens: the
-// same chain of MFMAs per output as above.
+// The weights' bytes bound it.  A wave owns 16 features, reads their gate and up
+// rows straight into fragments (16 bytes to a lane, UN steps of 32 k at a time
+// and the next UN ahead, at any alignment) and multiplies them with up to four
+// blocks of 16 tokens: the same chain of MFMAs per output as above.  (Four waves
+// to the same features, taking the batches of a chain in turn, had more in
+// flight but waited for each other: 1 x 2048 x 5461 11.9 -> 16.1 us.)
 
 struct FewArgs {
   const void* x; int64_t s_x;
@@ -567,14 +569,23 @@ __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
   store_vec<DET_BF16, 8>(a.rows, b * 2 * a.Fp + a.Fp + f0, du);
 }
 
-// rows of C elements as rows of Cp, the rest zeros
-__global__ __launch_bounds__(256) void k_pad(const void* src, int64_t s_src, int64_t R, int64_t C, int64_t Cp, void* dst) {
-  const int64_t per = Cp / 8, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= R * per) return;
+// rows of C elements as rows of Cp, the rest zeros: up to three operands at once
+struct PadArgs {
+  const void* src[3]; int64_t stride[3], R[3];
+  void* dst[3];
+  unsigned first[3];                      // blocks of the operands before
+  int n;
+  int64_t C, Cp;
+};
+__global__ __launch_bounds__(256) void k_pad(PadArgs a) {
+  int o = 0;                              // uniform
+  while (o + 1 < a.n && blockIdx.x >= a.first[o + 1]) ++o;
+  const int64_t per = a.Cp / 8, i = static_cast<int64_t>(blockIdx.x - a.first[o]) * 256 + threadIdx.x;
+  if (i >= a.R[o] * per) return;
   const int64_t r = row_of(i, per);
   const int c = static_cast<int>(i - r * per) * 8;
-  const bf16x8 v = fragment(static_cast<const char*>(src) + r * s_src * 2, c, static_cast<int>(C));
-  *reinterpret_cast<bf16x8*>(static_cast<char*>(dst) + i * 16) = v;
+  const bf16x8 v = fragment(static_cast<const char*>(a.src[o]) + r * a.stride[o] * 2, c, static_cast<int>(a.C));
+  *reinterpret_cast<bf16x8*>(static_cast<char*>(a.dst[o]) + i * 16) = v;
 }
 
 // the same from codes
@@ -604,7 +615,10 @@ __global__ __launch_bounds__(256) void k_clear(uint16_t* p, int64_t n) {
 
 // ---------------------------------------------------------------- host side
 
-constexpr int64_t FEW = 64;               // tokens
+// Tokens that go without tiles: up to 16, or 64 where the operands would have to
+// be copied first.  64 x 4096 x 11008: 94 us against 45 with tiles, 48 x 2048 x
+// 5461 22 against 10.5, with rows of 2047 22 against 30; one token 34 us.
+constexpr int64_t FEW = 16, FEW_COPIED = 64;
 constexpr int64_t STRIDE_MAX = 1 << 22;   // 256 rows lie within 2^31 bytes: offsets fit a buffer's 32 bits
 
 int64_t up_to(int64_t v, int64_t m) { return ceil_div(v, m) * m; }
@@ -622,34 +636,87 @@ void launch_tiles(MmArgs a, hipStream_t s) {
   hipLaunchKernelGGL((k_mm<GATED, A_BY_K, B_BY_K, WA, WB, FA, FB, KS, BUFS, SPREAD>), dim3(static_cast<unsigned>(a.tiles_a * a.tiles_b)),
                      dim3(64 * WA * WB), 0, s, a);
 }
+// Tiles of 64 x 64, 128 x 128, 128 x 256 or 256 x 256 (A x B): large ones move
+// fewer bytes per product, small ones fill the chip.  The rule takes the least of
+// what each would take, rounds (stages t + end), from what was measured (us per
+// stage of 64 k where half the CUs have a tile and where all have, and for a
+// tile's end; 64 x 64 fits twice on a CU).  4096 features of either weight, k
+// 4096, by tokens: 256: 17 us (28, 52, 87 for the larger tiles), 512: 28 28 52
+// 87, 1024: 53 35 52 88, 2048: 103 69 65 89, 4096: 202 135 124 106.  The result's
+// bits are the same for all.
+struct TileCost {
+  int a, b, slots;
+  double half, full, end;
+};
+constexpr TileCost TILES[4] = {{64, 64, 512, 0.30, 0.50, 1.0}, {128, 128, 256, 0.50, 0.55, 2.0}, {128, 256, 256, 0.82, 0.95, 4.0},
+                               {256, 256, 256, 1.3, 1.6, 8.0}};
+int tile_choice(int64_t na, int64_t nb, int64_t K) {
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < 4; ++i) {
+    const TileCost& t = TILES[i];
+    const int64_t tiles = ceil_div(na, t.a) * ceil_div(nb, t.b);
+    const double time = static_cast<double>(ceil_div(tiles, t.slots)) *
+                        (static_cast<double>(K) / 64.0 * (2 * tiles <= t.slots ? t.half : t.full) + t.end);
+    if (i == 0 || time < least) {
+      best = i;
+      least = time;
+    }
+  }
+  return best;
+}
+
+// By row 64 k to a stage (whole lines of memory), its reads before its MFMAs;
+// by k 32 and 64, spread: 8192 x 4096 x 11008 forward 1187 us so, 1204 spread,
+// 1306 with 32; dx and its dg and du 1287 against 1387 and 1362, dw 1349 against 1500.
 template <bool GATED, bool A_BY_K, bool B_BY_K>
 void launch_mm(const MmArgs& a, hipStream_t s) {
-  const int64_t na = a.A.n * (GATED ? 2 : 1), nb = a.B.n;
-  if (ceil_div(na, 256) * ceil_div(nb, 256) >= 128) {
-    if constexpr (A_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 32, 5, true>(a, s); //BIGK
-    else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 64, 2, false>(a, s); //BIGR
-  } else if (ceil_div(na, 128) * ceil_div(nb, 128) >= 256) {
-    launch_tiles<GATED, A_BY_K, B_BY_K, 2, 2, 4, 4, 32, 5, true>(a, s); //MID
-  } else {
-    launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 32, 5, true>(a, s); //SMALL
+  switch (tile_choice(a.A.n * (GATED ? 2 : 1), a.B.n, a.K)) {
+    case 0:
+      if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 64, 5, false>(a, s);
+      else if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 2, 1, 64, 5, true>(a, s);
+      else launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 32, 5, true>(a, s);
+      break;
+    case 1:
+      if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 2, 64, 5, true>(a, s);
+      else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 2, 4, 4, 32, 5, true>(a, s);
+      break;
+    case 2:
+      if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 64, 3, !GATED>(a, s);
+      else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 32, 5, true>(a, s);
+      break;
+    default:
+      if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 64, 2, false>(a, s);
+      else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 32, 5, true>(a, s);
   }
 }
 
 unsigned blocks_for(int64_t threads) { return static_cast<unsigned>(ceil_div(threads, 256)); }
 
-// a padded copy of R rows of K elements at ws (which advances)
-const void* padded(const void* p, int64_t& stride, int64_t R, int64_t K, char*& ws, hipStream_t s) {
-  const int64_t Kp = up_to(K, 64);
-  void* const to = ws;
-  ws += room(R * Kp * 2);
-  hipLaunchKernelGGL(k_pad, dim3(blocks_for(R * (Kp / 8))), dim3(256), 0, s, p, stride, R, K, Kp, to);
-  stride = Kp;
-  return to;
-}
-// p as an operand of the matrix product: itself, or a padded copy
-const void* operand(const void* p, int64_t& stride, int64_t R, int64_t K, char*& ws, hipStream_t s) {
-  return direct(p, stride, K) ? p : padded(p, stride, R, K, ws, s);
-}
+// padded copies of operands, made by one launch
+struct Pads {
+  PadArgs a{};
+  unsigned blocks = 0;
+  char* ws;
+  Pads(int64_t C, void* workspace) : ws(static_cast<char*>(workspace)) {
+    a.C = C;
+    a.Cp = up_to(C, 64);
+  }
+  void copy(const void*& p, int64_t& stride, int64_t R) {
+    a.src[a.n] = p;
+    a.stride[a.n] = stride;
+    a.R[a.n] = R;
+    a.dst[a.n] = ws;
+    a.first[a.n++] = blocks;
+    blocks += blocks_for(R * (a.Cp / 8));
+    p = ws;
+    stride = a.Cp;
+    ws += room(R * a.Cp * 2);
+  }
+  void launch(hipStream_t s) const {
+    if (a.n > 0) hipLaunchKernelGGL(k_pad, dim3(blocks), dim3(256), 0, s, a);
+  }
+};
 
 bool known_act(int act) { return act == DET_ACT_SILU || act == DET_ACT_GELU || act == DET_ACT_GELU_TANH; }
 bool known_save(int save) { return save == DET_SAVE_NONE || save == DET_SAVE_HALF || save == DET_SAVE_INT8; }
@@ -681,7 +748,7 @@ extern "C" {
 
 int64_t det_gated_linear_workspace_bytes(int64_t N, int64_t C, int64_t F, det_save save, int aligned) {
   if (N <= 0 || C <= 0 || F <= 0 || N > DET_ROWS_MAX || C > DET_GATED_MAX || F > DET_GATED_MAX) return 0;
-  if ((save == DET_SAVE_NONE && N <= FEW) || (C % 64 == 0 && aligned)) return 0;
+  if ((save == DET_SAVE_NONE && N <= FEW_COPIED) || (C % 64 == 0 && aligned)) return 0;
   const int64_t Cp = up_to(C, 64);
   return room(N * Cp * 2) + 2 * room(F * Cp * 2);
 }
@@ -701,7 +768,8 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
   if (!aligned_for(h, h_dt) || (save == DET_SAVE_HALF && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
     return fail(DET_EINVAL, "outputs must be aligned to their element size");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (save == DET_SAVE_NONE && N <= FEW) {
+  const bool copies = !direct(x, s_x, C) || !direct(w_gate, s_gate, C) || !direct(w_up, s_up, C);
+  if (save == DET_SAVE_NONE && N <= (copies ? FEW_COPIED : FEW)) {
     FewArgs a{x, s_x, {w_gate, w_up}, {s_gate, s_up}, N, F, static_cast<int>(C), h, h_dt, act};
     const dim3 grid(static_cast<unsigned>(ceil_div(F, 16)));
     if (N <= 16) hipLaunchKernelGGL((k_few<1, 8>), grid, dim3(64), 0, s, a);
@@ -713,12 +781,14 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
   const int64_t need = (direct(x, s_x, C) ? 0 : room(N * Cp * 2)) + (direct(w_gate, s_gate, C) ? 0 : room(F * Cp * 2)) +
                        (direct(w_up, s_up, C) ? 0 : room(F * Cp * 2));
   if ((st = check_workspace(workspace, workspace_bytes, need)) != DET_OK) return st;
-  char* ws = static_cast<char*>(workspace);
   MmArgs a{};
   a.A = {w_gate, s_gate, F};
   a.A1 = {w_up, s_up, F};
   a.B = {x, s_x, N};
-  for (Operand* o : {&a.A, &a.A1, &a.B}) o->p = operand(o->p, o->stride, o->n, C, ws, s);
+  Pads pads(C, workspace);
+  for (Operand* o : {&a.A, &a.A1, &a.B})
+    if (!direct(o->p, o->stride, C)) pads.copy(o->p, o->stride, o->n);
+  pads.launch(s);
   a.K = Cp;
   a.out = h; a.dt = h_dt; a.act = act; a.save = save;
   a.gate = gate; a.up = up; a.gate_exp = gate_exp; a.up_exp = up_exp;
@@ -774,7 +844,6 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
   const int64_t need = rows + (need_dx && copy_w ? 2 * room(F * Cp * 2) : 0) +
                        (need_dw && (codes || !direct(x, s_x, C)) ? room(N * Cp * 2) : 0);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != DET_OK) return st;
-  char* ws = static_cast<char*>(workspace) + rows;
   GateGradArgs g{};
   g.dh = dh; g.s_dh = s_dh; g.dh_dt = dh_dt;
   g.gate = gate; g.up = up; g.gate_exp = gate_exp; g.up_exp = up_exp;
@@ -784,12 +853,24 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
   if (act == DET_ACT_SILU) hipLaunchKernelGGL(k_gate_grad<DET_ACT_SILU>, grid, dim3(256), 0, s, g);
   else if (act == DET_ACT_GELU_TANH) hipLaunchKernelGGL(k_gate_grad<DET_ACT_GELU_TANH>, grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL(k_gate_grad<DET_ACT_GELU>, grid, dim3(256), 0, s, g);
+  Operand gates{w_gate, s_gate, C}, ups{w_up, s_up, C}, xs{x, s_x, C};
+  Pads pads(C, static_cast<char*>(workspace) + rows);
+  if (need_dx && copy_w) {
+    pads.copy(gates.p, gates.stride, F);
+    pads.copy(ups.p, ups.stride, F);
+  }
+  if (need_dw && codes) {
+    hipLaunchKernelGGL(k_unpack_pad, dim3(blocks_for(N * (Cp / 8))), dim3(256), 0, s, static_cast<const int8_t*>(x), s_x, x_exp, N,
+                       C, Cp, static_cast<void*>(pads.ws));
+    xs = {pads.ws, Cp, C};
+  } else if (need_dw && !direct(x, s_x, C)) {
+    pads.copy(xs.p, xs.stride, N);
+  }
+  pads.launch(s);
   if (need_dx) {                          // dx [N][C]: k over the gate's features, then over the up projection's
     MmArgs a{};
-    a.A = {w_gate, s_gate, C};
-    a.A1 = {w_up, s_up, C};
-    if (copy_w)
-      for (Operand* o : {&a.A, &a.A1}) o->p = padded(o->p, o->stride, F, C, ws, s);
+    a.A = gates;
+    a.A1 = ups;
     a.B = {workspace, 2 * Fp, N};
     a.K = 2 * Fp; a.ka = F; a.turn = Fp;
     a.out = dx; a.split0 = a.split1 = N; a.dt = DET_BF16;
@@ -797,15 +878,7 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
   }
   if (need_dw) {                          // dw [2 F][C]: k over the rows
     MmArgs a{};
-    a.A = {x, s_x, C};
-    if (codes) {
-      hipLaunchKernelGGL(k_unpack_pad, dim3(blocks_for(N * (Cp / 8))), dim3(256), 0, s, static_cast<const int8_t*>(x), s_x, x_exp,
-                         N, C, Cp, static_cast<void*>(ws));
-      a.A = {ws, Cp, C};
-    } else {
-      a.A.p = operand(x, a.A.stride, N, C, ws, s);
-    }
-    a.A1 = a.A;
+    a.A = a.A1 = xs;
     a.B = {workspace, 2 * Fp, 2 * Fp};
     a.K = a.turn = up_to(N, 64); a.ka = a.kb = N;
     a.out = dw_gate; a.out1 = dw_up; a.split0 = F; a.split1 = Fp; a.dt = DET_BF16;
