@@ -74,10 +74,10 @@ def load() -> ctypes.CDLL:
         "det_distill_grad": ([c_int, vp, i64, i64, i64, ctypes.c_double, vp, i64, i64, vp, vp, vp, i64, vp, i64, vp],
                              c_int),
         "det_gated_linear_workspace_bytes": ([i64, i64, i64, c_int, c_int], i64),
-        "det_gated_linear": ([vp, i64, vp, i64, vp, i64, i64, i64, i64, c_int, c_int, vp, c_int, vp, vp, vp, vp, vp,
+        "det_gated_linear": ([vp, i64, vp, i64, vp, i64, i64, i64, i64, c_int, c_int, vp, c_int, vp, vp, i64, vp, vp, vp,
                               ctypes.c_size_t, vp], c_int),
         "det_gated_linear_grad_workspace_bytes": ([i64, i64, i64, c_int, c_int, c_int, c_int], i64),
-        "det_gated_linear_grad": ([c_int, vp, i64, vp, i64, vp, vp, i64, vp, i64, c_int, vp, vp, vp, vp, i64, i64,
+        "det_gated_linear_grad": ([c_int, vp, i64, vp, i64, vp, vp, i64, vp, i64, c_int, vp, vp, i64, vp, vp, i64, i64,
                                    i64, c_int, vp, vp, vp, vp, ctypes.c_size_t, vp], c_int),
         "det_int8_pack": ([c_int, vp, i64, i64, i64, vp, vp, vp], c_int),
         "det_int8_unpack": ([vp, i64, vp, i64, i64, c_int, vp, vp], c_int),

@@ -70,15 +70,17 @@ Tensor gated_forward(const Tensor& x, const Tensor& wg, const Tensor& wu, det_ac
   Tensor h = at::empty(shape, x.options().dtype(ht));
   if (save != DET_SAVE_NONE) {
     const auto o = x.options().dtype(save == DET_SAVE_INT8 ? at::kChar : at::kHalf), e = x.options().dtype(at::kChar);
-    kept.gate = at::empty(shape, o);
-    kept.up = at::empty(shape, o);
+    // rows of a multiple of 32, so that every row is written and read in aligned words
+    const int64_t Fs = (F + 31) / 32 * 32;
+    kept.gate = at::empty(with_last(lead_of(x), Fs), o).narrow(-1, 0, F);
+    kept.up = at::empty(with_last(lead_of(x), Fs), o).narrow(-1, 0, F);
     kept.gate_exp = at::empty(blocks, e);
     kept.up_exp = at::empty(blocks, e);
   }
   const int64_t bytes = det_gated_linear_workspace_bytes(N, C, F, save, C % 64 == 0);
   const Tensor ws = bytes > 0 ? at::empty({bytes}, x.options().dtype(at::kByte)) : Tensor();
   ok(det_gated_linear(in(x2), x2.stride(0), in(g2), g2.stride(0), in(u2), u2.stride(0), N, C, F, act,
-                      dt_of(ht), out<void>(h), save, out<void>(kept.gate), out<void>(kept.up),
+                      dt_of(ht), out<void>(h), save, out<void>(kept.gate), out<void>(kept.up), (F + 31) / 32 * 32,
                       out<int8_t>(kept.gate_exp), out<int8_t>(kept.up_exp), out<void>(ws),
                       static_cast<size_t>(bytes), stream_of(x)));
   return h;
@@ -124,13 +126,17 @@ GatedGrads gated_backward(const Tensor& dh, const Tensor& x, const OptTensor& x_
     g2 = g2.contiguous();
     u2 = u2.contiguous();
   }
-  const Tensor kg = kept.gate.contiguous(), ku = kept.up.contiguous();
+  Tensor kg = rows(kept.gate), ku = rows(kept.up);
+  if (kg.stride(0) != ku.stride(0)) {
+    kg = kg.contiguous();
+    ku = ku.contiguous();
+  }
   const Tensor xe = x_exp ? x_exp->contiguous() : Tensor(), ge = kept.gate_exp.contiguous(), ue = kept.up_exp.contiguous();
   const int64_t bytes = det_gated_linear_grad_workspace_bytes(N, C, F, need_dx, need_dw, C % 64 == 0, x_exp.has_value());
   const Tensor ws = bytes > 0 ? at::empty({bytes}, x.options().dtype(at::kByte)) : Tensor();
   ok(det_gated_linear_grad(dt_of(dh.scalar_type()), in(dh2), dh2.stride(0), in(x2), x_exp ? C : x2.stride(0),
                            static_cast<const int8_t*>(xe.defined() ? xe.const_data_ptr() : nullptr), in(g2), g2.stride(0), in(u2), u2.stride(0),
-                           int8 ? DET_SAVE_INT8 : DET_SAVE_HALF, in(kg), in(ku), static_cast<const int8_t*>(in(ge)), static_cast<const int8_t*>(in(ue)), N,
+                           int8 ? DET_SAVE_INT8 : DET_SAVE_HALF, in(kg), in(ku), kg.stride(0), static_cast<const int8_t*>(in(ge)), static_cast<const int8_t*>(in(ue)), N,
                            C, F, act, out<void>(g.dx), out<void>(g.dwg), out<void>(g.dwu), out<void>(ws),
                            static_cast<size_t>(bytes), stream_of(x)));
   return g;
@@ -177,17 +183,15 @@ Tensor unpack_int8(const Tensor& codes, const Tensor& exps, ScalarType dtype) {
 
 // ---------------------------------------------------------------- autograd
 
-// tie: x, or with 8-bit checkpoints, which do not keep x, an empty tensor that
-// hangs on x in the graph: what refuses second derivatives has to reach x
 struct GatedFn : torch::autograd::Function<GatedFn> {
-  static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& wg, const Tensor& wu, const Tensor& tie,
-                        int64_t act, std::optional<ScalarType> out_dtype, int64_t save) {
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& wg, const Tensor& wu, int64_t act,
+                        std::optional<ScalarType> out_dtype, int64_t save) {
     Saved kept;
     Tensor h = gated_forward(x, wg, wu, static_cast<det_activation>(act), out_dtype, static_cast<det_save>(save), kept);
-    // x enters the weights' gradients only
+    // x enters the weights' gradients only; its shape is asked for in any case
     Tensor kx = x, xe;
     if (save == DET_SAVE_INT8) std::tie(kx, xe) = pack_int8(x);
-    ctx->save_for_backward({kx, xe, wg, wu, kept.gate, kept.up, kept.gate_exp, kept.up_exp, tie});
+    ctx->save_for_backward({kx, xe, wg, wu, kept.gate, kept.up, kept.gate_exp, kept.up_exp});
     ctx->saved_data["act"] = act;
     return h;
   }
@@ -201,9 +205,9 @@ struct GatedFn : torch::autograd::Function<GatedFn> {
                          static_cast<det_activation>(ctx->saved_data["act"].toInt()), ctx->needs_input_grad(0),
                          ctx->needs_input_grad(1) || ctx->needs_input_grad(2));
     }
-    variable_list r = once({g.dx, ctx->needs_input_grad(1) ? g.dwg : Tensor(), ctx->needs_input_grad(2) ? g.dwu : Tensor()},
-                           {s[8], s[2], s[3], grads[0]}, "gated_linear");
-    r.resize(7);
+    variable_list r = once_at_node({g.dx, ctx->needs_input_grad(1) ? g.dwg : Tensor(), ctx->needs_input_grad(2) ? g.dwu : Tensor()},
+                                   grads, "gated_linear");
+    r.resize(6);
     return r;
   }
 };
@@ -214,7 +218,7 @@ Tensor gated_linear(const Tensor& x, const Tensor& wg, const Tensor& wu, const s
   const det_activation act = act_of(activation, "gated_linear");
   const det_save save = save_of(checkpoint, "gated_linear");
   if (at::GradMode::is_enabled() && (wants_grad(x) || wants_grad(wg) || wants_grad(wu)))
-    return GatedFn::apply(x, wg, wu, save == DET_SAVE_INT8 && x.dim() > 0 ? x.narrow(0, 0, 0).clone() : x, static_cast<int64_t>(act), out_dtype, static_cast<int64_t>(save));
+    return GatedFn::apply(x, wg, wu, static_cast<int64_t>(act), out_dtype, static_cast<int64_t>(save));
   Saved none;
   return gated_forward(x, wg, wu, act, out_dtype, DET_SAVE_NONE, none);
 }

@@ -106,7 +106,7 @@ struct MmArgs {
   // gated: h [n of B][n of A]; else D, rows [0, split0) in out, [split1, split1 + split0) in out1
   void* out; void* out1; int64_t split0, split1;
   // what the gradients read again
-  void* gate; void* up;
+  void* gate; void* up; int64_t s_kept;
   int8_t* gate_exp; int8_t* up_exp;
   int dt, act, save;                      // type of out, activation, what gate and up hold
 };
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(64 * WA * WB, FA * FB > 32 ? 1 : 2) void k_mm(MmArg
           tu = top_of_8(tu);
           const bool bad_g = not_finite(tg), bad_u = not_finite(tu);        // int8 alone
           const int eg = int8 ? block_exponent(tg) : half_exponent(tg), eu = int8 ? block_exponent(tu) : half_exponent(tu);
-          const int64_t blocks = (na + 31) / 32, at = b * na + c;
+          const int64_t blocks = (na + 31) / 32, at = b * a.s_kept + c;
           if ((lane & 7) == 0 && in > 0) {
             a.gate_exp[b * blocks + c / 32] = static_cast<int8_t>(bad_g ? DET_INT8_NAN : eg);
             a.up_exp[b * blocks + c / 32] = static_cast<int8_t>(bad_u ? DET_INT8_NAN : eu);
@@ -527,7 +527,8 @@ __device__ __forceinline__ int64_t row_of(int64_t i, int64_t per) {
 
 struct GateGradArgs {
   const void* dh; int64_t s_dh; int dh_dt;
-  const void* gate; const void* up;       // [N][F] halves or codes
+  const void* gate; const void* up;       // [N] rows of F halves or codes
+  int64_t s_kept;
   const int8_t* gate_exp; const int8_t* up_exp;
   int64_t N, F, Fp;
   int act, save;
@@ -546,7 +547,7 @@ __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
   float dh[2][4], g[2][4], u[2][4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int64_t f = f0 + 4 * h, at = b * a.F + f;
+    const int64_t f = f0 + 4 * h, at = b * a.s_kept + f;
     const int in = static_cast<int>(min<int64_t>(4, a.F - f));
     load4(a.dh_dt, a.dh, b * a.s_dh + f, dh[h], in);
     if (a.save == DET_SAVE_INT8) {
@@ -755,7 +756,7 @@ int64_t det_gated_linear_workspace_bytes(int64_t N, int64_t C, int64_t F, det_sa
 
 det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int64_t s_gate, const void* w_up,
                             int64_t s_up, int64_t N, int64_t C, int64_t F, det_activation act, det_dtype h_dt, void* h,
-                            det_save save, void* gate, void* up, int8_t* gate_exp, int8_t* up_exp, void* workspace,
+                            det_save save, void* gate, void* up, int64_t s_kept, int8_t* gate_exp, int8_t* up_exp, void* workspace,
                             size_t workspace_bytes, void* stream) {
   if (!known_dtype(h_dt)) return fail(DET_EDTYPE, "unknown dtype %d", h_dt);
   det_status st = check_sizes(N, C, F, act, save);
@@ -765,6 +766,7 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
     return st;
   if (h == nullptr || (save != DET_SAVE_NONE && (gate == nullptr || up == nullptr || gate_exp == nullptr || up_exp == nullptr)))
     return fail(DET_EINVAL, "null output");
+  if (save != DET_SAVE_NONE && s_kept < F) return fail(DET_EINVAL, "rows of gate and up overlap: stride %lld", (long long)s_kept);
   if (!aligned_for(h, h_dt) || (save == DET_SAVE_HALF && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
     return fail(DET_EINVAL, "outputs must be aligned to their element size");
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -791,7 +793,7 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
   pads.launch(s);
   a.K = Cp;
   a.out = h; a.dt = h_dt; a.act = act; a.save = save;
-  a.gate = gate; a.up = up; a.gate_exp = gate_exp; a.up_exp = up_exp;
+  a.gate = gate; a.up = up; a.s_kept = s_kept; a.gate_exp = gate_exp; a.up_exp = up_exp;
   launch_mm<true, false, false>(a, s);
   return hip_check(hipGetLastError(), "gated projection launch");
 }
@@ -807,7 +809,8 @@ int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, i
 
 det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, const void* x, int64_t s_x,
                                  const int8_t* x_exp, const void* w_gate, int64_t s_gate, const void* w_up,
-                                 int64_t s_up, det_save save, const void* gate, const void* up, const int8_t* gate_exp,
+                                 int64_t s_up, det_save save, const void* gate, const void* up, int64_t s_kept,
+                                 const int8_t* gate_exp,
                                  const int8_t* up_exp, int64_t N, int64_t C, int64_t F, det_activation act, void* dx,
                                  void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes, void* stream) {
   if (!known_dtype(dh_dt)) return fail(DET_EDTYPE, "unknown dtype %d", dh_dt);
@@ -828,7 +831,7 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
   if (!need_dx && !need_dw) return DET_OK;
   if (dh == nullptr || gate == nullptr || up == nullptr || gate_exp == nullptr || up_exp == nullptr)
     return fail(DET_EINVAL, "null pointer");
-  if (s_dh < 0) return fail(DET_EINVAL, "negative stride");
+  if (s_dh < 0 || s_kept < 0) return fail(DET_EINVAL, "negative stride");
   if (!aligned_for(dh, dh_dt) || (save == DET_SAVE_HALF && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
     return fail(DET_EINVAL, "operands must be aligned to their element size");
   if (need_dx && ((st = check_operand(w_gate, s_gate, "w_gate")) != DET_OK || (st = check_operand(w_up, s_up, "w_up")) != DET_OK))
@@ -846,7 +849,7 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
   if ((st = check_workspace(workspace, workspace_bytes, need)) != DET_OK) return st;
   GateGradArgs g{};
   g.dh = dh; g.s_dh = s_dh; g.dh_dt = dh_dt;
-  g.gate = gate; g.up = up; g.gate_exp = gate_exp; g.up_exp = up_exp;
+  g.gate = gate; g.up = up; g.s_kept = s_kept; g.gate_exp = gate_exp; g.up_exp = up_exp;
   g.N = N; g.F = F; g.Fp = Fp; g.save = save;
   g.rows = static_cast<uint16_t*>(workspace);
   const dim3 grid(blocks_for(N * (Fp / 8)));

@@ -86,14 +86,26 @@ inline Tensor rows(const Tensor& t) {
 // it is asked for one input alone.  Torch's own DelayedError hangs on the
 // results only: grad(loss + g.pow(2).sum(), x) would leave it out and return
 // the first-order terms.
-inline variable_list once(variable_list grads, const variable_list& sources, const char* name) {
-  if (!at::GradMode::is_enabled()) return grads;
-  const auto refusal = std::make_shared<torch::autograd::Error>(
-      std::string(name) + " is differentiable once",
-      torch::autograd::collect_next_edges(at::ArrayRef<Tensor>(sources)));
+inline variable_list refuse_more(variable_list grads, torch::autograd::edge_list&& edges, const char* name) {
+  const auto refusal = std::make_shared<torch::autograd::Error>(std::string(name) + " is differentiable once",
+                                                                std::move(edges));
   for (auto& g : grads)
     if (g.defined()) torch::autograd::set_history(g, refusal);
   return grads;
+}
+inline variable_list once(variable_list grads, const variable_list& sources, const char* name) {
+  if (!at::GradMode::is_enabled()) return grads;
+  return refuse_more(std::move(grads), torch::autograd::collect_next_edges(at::ArrayRef<Tensor>(sources)), name);
+}
+// the same for a backward pass that does not keep its inputs: their edges are
+// those of the node that is running
+inline variable_list once_at_node(variable_list grads, const variable_list& incoming, const char* name) {
+  if (!at::GradMode::is_enabled()) return grads;
+  torch::autograd::edge_list edges = torch::autograd::collect_next_edges(at::ArrayRef<Tensor>(incoming));
+  if (const auto node = torch::autograd::get_current_node())
+    for (const auto& e : node->next_edges())
+      if (e.is_valid()) edges.push_back(e);
+  return refuse_more(std::move(grads), std::move(edges), name);
 }
 
 // A trace (torch.jit.trace, make_fx) sees the allocations of the results but

@@ -20,8 +20,10 @@ namespace {
 
 using namespace rowops;
 
-// A wave takes 512 tokens of a row at a time: two vectors of 4 per lane.
-constexpr int PART = 512, VECS = 2;
+// A wave takes 512 tokens of a row at a time: two vectors of 4 per lane.  In the
+// policy loss a workgroup of four takes a piece of 2048 tokens, or four rows of
+// up to 512.
+constexpr int PART = 512, VECS = 2, PIECE = 4 * PART;
 
 struct __attribute__((packed, aligned(1))) MaskWord {
   uint32_t w;
@@ -81,14 +83,14 @@ struct PolicyArgs {
   const float* adv; int64_t s_adv; int adv_t;                 // adv_t: 1 per token, 0 one to a row
   const uint8_t* mask; int64_t s_mask;
   const float* ref; int64_t s_ref;        // null: no KL term
-  int64_t B, T, parts;
+  int64_t B, T, pieces;
   double low, high;                       // ln(1 - clip_low), ln(1 + clip_high)
   float bound_low, bound_high, kl_weight;
   int reduction;
   // reduction none: per token; else one value each
   float* loss; float* kl; float* clipped;
-  // what the parts of rows leave: [parts][B]
-  double* part_loss; double* part_kl; int32_t* part_clipped; int32_t* part_count;
+  // what the pieces of rows leave, [pieces][B]: sums of loss and KL, tokens clipped and that count
+  double2* piece_sums; int2* piece_counts;
   int64_t* count;                         // [B] tokens of a row that count, [B + 0] their divisor
   int64_t* joined; int groups;            // groups > 1: [groups][JOINED] of the workgroups that join rows
   int32_t* status;
@@ -138,19 +140,30 @@ __device__ __forceinline__ Token token_of(const PolicyArgs& a, float lp, float o
   return t;
 }
 
-// the parts of rows, one to a wave
+// the row of a wave, its piece and the wave's first token
+struct Place {
+  int64_t b, piece, t;
+};
+__device__ __forceinline__ Place place_of(const PolicyArgs& a, int wave) {
+  if (a.T <= PART) return {static_cast<int64_t>(blockIdx.x) * 4 + wave, 0, 0};
+  const int64_t b = static_cast<int64_t>(blockIdx.x) / a.pieces, piece = static_cast<int64_t>(blockIdx.x) - b * a.pieces;
+  return {b, piece, piece * PIECE + wave * PART};
+}
+
 __global__ __launch_bounds__(256) void k_policy(PolicyArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (id >= a.B * a.parts) return;
-  const int64_t b = id / a.parts, part = id % a.parts;
+  __shared__ double sums[4][2];
+  __shared__ int counts[4][2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place at = place_of(a, wave);
+  const int64_t b = at.b;
+  if (b >= a.B) return;                   // short rows alone: no barrier follows there
   const float adv_b = a.adv_t == 0 ? a.adv[b * a.s_adv] : 0.0f;
   double loss = 0.0, kl = 0.0;
   int clipped = 0, count = 0;
   bool bad = false;
 #pragma unroll
   for (int v = 0; v < VECS; ++v) {
-    const int64_t t = part * PART + v * 256 + lane * 4;
+    const int64_t t = at.t + v * 256 + lane * 4;
     const int n = static_cast<int>(max<int64_t>(0, min<int64_t>(4, a.T - t)));
     float lp[4], old[4], adv[4], ref[4], l[4], k[4], c[4];
     bool m[4];
@@ -184,20 +197,34 @@ __global__ __launch_bounds__(256) void k_policy(PolicyArgs a) {
   kl = wave_sum(kl);
   clipped = wave_count(clipped);
   count = wave_count(count);
+  if (a.T > PART) {                       // the piece's four waves, in order
+    if (lane == 0) {
+      sums[wave][0] = loss;
+      sums[wave][1] = kl;
+      counts[wave][0] = clipped;
+      counts[wave][1] = count;
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      loss += sums[w][0];
+      kl += sums[w][1];
+      clipped += counts[w][0];
+      count += counts[w][1];
+    }
+  }
   if (lane == 0) {
-    const int64_t at = part * a.B + b;
-    a.part_loss[at] = loss;
-    a.part_kl[at] = kl;
-    a.part_clipped[at] = clipped;
-    a.part_count[at] = count;
+    a.piece_sums[at.piece * a.B + b] = double2{loss, kl};
+    a.piece_counts[at.piece * a.B + b] = int2{clipped, count};
   }
 }
 
-// Rows joined: a row's parts are added in 64 bits, in ascending order (up to 16
+// Rows joined: a row's pieces are added in 64 bits, in ascending order (up to 16
 // of them) or over the lanes of a wave; the rows' values, rounded to fp32, are
 // added exactly.  Three sums (loss, KL, clipped) of NDIG digits, their values
 // that are not finite by kind, and two counts.
-constexpr int SUMS = 3, JOINED = SUMS * NDIG + SUMS + 2, SERIAL = 16, JOIN_THREADS = 1024;
+constexpr int SUMS = 3, JOINED = SUMS * NDIG + SUMS + 2, SERIAL = 16, AHEAD = 8, JOIN_THREADS = 1024;
 
 struct JoinTotals {
   unsigned long long digits[SUMS][NDIG][64];                  // a lane's own, or all would wait for one address
@@ -229,7 +256,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_policy_join(PolicyArgs a) {
   if (threadIdx.x < SUMS) s.kinds[threadIdx.x] = 0;
   if (threadIdx.x == 0) s.tokens = s.rows = 0ull;
   __syncthreads();
-  const bool serial = a.parts <= SERIAL;
+  const bool serial = a.pieces <= SERIAL;
   const int64_t at_once = static_cast<int64_t>(a.groups) * (serial ? JOIN_THREADS : JOIN_THREADS / 64);
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (serial ? JOIN_THREADS : JOIN_THREADS / 64) +
                         (serial ? threadIdx.x : threadIdx.x >> 6);
@@ -237,12 +264,24 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_policy_join(PolicyArgs a) {
   for (int64_t b = first; b < a.B; b += at_once) {
     double sum[SUMS] = {0.0, 0.0, 0.0};
     int64_t clipped = 0, count = 0;
-    for (int64_t p = serial ? 0 : lane; p < a.parts; p += serial ? 1 : 64) {
-      const int64_t at = p * a.B + b;
-      sum[0] += a.part_loss[at];
-      sum[1] += a.part_kl[at];
-      clipped += a.part_clipped[at];
-      count += a.part_count[at];
+    const int stride = serial ? 1 : 64;
+    for (int64_t p0 = serial ? 0 : lane; p0 < a.pieces; p0 += AHEAD * stride) {
+      double2 v[AHEAD];                   // all in flight before the first is added; past the end: row b's first, not added
+      int2 n[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int64_t p = p0 + i * stride, at = (p < a.pieces ? p : 0) * a.B + b;
+        v[i] = a.piece_sums[at];
+        n[i] = a.piece_counts[at];
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (p0 + i * stride < a.pieces) {
+          sum[0] += v[i].x;
+          sum[1] += v[i].y;
+          clipped += n[i].x;
+          count += n[i].y;
+        }
     }
     if (!serial) {
       sum[0] = wave_sum(sum[0]);
@@ -263,8 +302,15 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_policy_join(PolicyArgs a) {
       else add_digits(__float_as_uint(v), [&](int j, int64_t x) { atomicAdd(&s.digits[k][j][lane], static_cast<unsigned long long>(x)); });
     }
   }
-  if (tokens != 0) atomicAdd(&s.tokens, tokens);
-  if (rows != 0) atomicAdd(&s.rows, rows);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {      // one address each: a thousand adds in a row would take 9 us
+    tokens += __shfl_xor(tokens, o);
+    rows += __shfl_xor(rows, o);
+  }
+  if (lane == 0 && rows != 0) {
+    atomicAdd(&s.tokens, tokens);
+    atomicAdd(&s.rows, rows);
+  }
   __syncthreads();
   if (threadIdx.x < SUMS * NDIG) {
     unsigned long long t = 0;
@@ -312,9 +358,9 @@ __global__ __launch_bounds__(64) void k_policy_total(PolicyArgs a) {
 
 __global__ __launch_bounds__(256) void k_policy_grad(PolicyArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (id >= a.B * a.parts) return;
-  const int64_t b = id / a.parts, part = id % a.parts;
+  const Place at = place_of(a, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+  const int64_t b = at.b;
+  if (b >= a.B) return;
   const float adv_b = a.adv_t == 0 ? a.adv[b * a.s_adv] : 0.0f;
   float w_b = 0.0f;                       // this row's weight: g over the count it was divided by
   if (a.reduction != DET_REDUCE_NONE) {
@@ -324,7 +370,7 @@ __global__ __launch_bounds__(256) void k_policy_grad(PolicyArgs a) {
   }
 #pragma unroll
   for (int v = 0; v < VECS; ++v) {
-    const int64_t t = part * PART + v * 256 + lane * 4;
+    const int64_t t = at.t + v * 256 + lane * 4;
     const int n = static_cast<int>(max<int64_t>(0, min<int64_t>(4, a.T - t)));
     float lp[4], old[4], adv[4], ref[4], w[4], out[4];
     bool m[4];
@@ -473,22 +519,22 @@ __global__ __launch_bounds__(256) void k_preference_grad(PreferenceArgs a, int64
 constexpr int64_t T_MAX = int64_t{1} << 24;
 
 int64_t parts_of(int64_t T) { return ceil_div(T, PART); }
-// workgroups that join rows: one up to 2^14 parts of rows (up to 16 loads to a thread of its 1024)
-int groups_of(int64_t B, int64_t parts) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, ceil_div(B * parts, 1 << 14))));
+int64_t pieces_of(int64_t T) { return T <= PART ? std::min<int64_t>(T, 1) : ceil_div(T, PIECE); }
+unsigned policy_blocks(int64_t B, int64_t T) { return static_cast<unsigned>(T <= PART ? ceil_div(B, 4) : B * pieces_of(T)); }
+// workgroups that join rows: one up to 2^13 pieces of rows (up to 8 to a thread of its 1024)
+int groups_of(int64_t B, int64_t pieces) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, ceil_div(B * pieces, 1 << 13))));
 }
 struct PolicyRoom {
-  int64_t loss, kl, clipped, count, joined, total;
+  int64_t sums, joined, counts, total;
 };
 PolicyRoom policy_room(int64_t B, int64_t T) {
-  const int64_t n = B * parts_of(T);
+  const int64_t n = B * pieces_of(T);
   PolicyRoom r;
-  r.loss = 0;
-  r.kl = n * 8;
-  r.joined = 2 * n * 8;
-  r.clipped = r.joined + groups_of(B, parts_of(T)) * JOINED * 8;
-  r.count = r.clipped + n * 4;
-  r.total = r.count + n * 4;
+  r.sums = 0;
+  r.joined = n * 16;
+  r.counts = r.joined + groups_of(B, pieces_of(T)) * JOINED * 8;
+  r.total = r.counts + n * 8;
   return r;
 }
 
@@ -526,7 +572,7 @@ PolicyArgs policy_args(const float* lp, int64_t s_lp, const float* old, int64_t 
   PolicyArgs a{};
   a.lp = lp; a.s_lp = s_lp; a.old = old; a.s_old = s_old; a.adv = adv; a.s_adv = s_adv; a.adv_t = adv_t;
   a.mask = mask; a.s_mask = s_mask; a.ref = ref; a.s_ref = s_ref;
-  a.B = B; a.T = T; a.parts = parts_of(T);
+  a.B = B; a.T = T; a.pieces = pieces_of(T);
   a.low = log1p(-low); a.high = log1p(high);
   a.bound_low = static_cast<float>(1.0 - low); a.bound_high = static_cast<float>(1.0 + high);
   a.kl_weight = static_cast<float>(kl_weight);
@@ -561,24 +607,22 @@ det_status det_policy_loss(const float* logprob, int64_t s_logprob, const float*
   if (!aligned4(loss) || !aligned4(kl) || !aligned4(clipped) || !aligned8(count))
     return fail(DET_EINVAL, "outputs must be aligned to their element size");
   const int64_t need = det_policy_loss_workspace_bytes(B, T, reduction);
-  if (need > 0 && (workspace == nullptr || !aligned8(workspace) || workspace_bytes < static_cast<size_t>(need)))
-    return fail(DET_EINVAL, "workspace: %lld bytes, 8-byte aligned, are needed", (long long)need);
+  if (need > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < static_cast<size_t>(need)))
+    return fail(DET_EINVAL, "workspace: %lld bytes, 16-byte aligned, are needed", (long long)need);
   a.loss = loss; a.kl = kl; a.clipped = clipped; a.count = count;
   a.status = det_device_status_word();
   if (a.status == nullptr) return DET_EHIP;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  a.groups = groups_of(B, a.parts);
+  a.groups = groups_of(B, a.pieces);
   if (need > 0) {
     const PolicyRoom r = policy_room(B, T);
     char* const ws = static_cast<char*>(workspace);
-    a.part_loss = reinterpret_cast<double*>(ws + r.loss);
-    a.part_kl = reinterpret_cast<double*>(ws + r.kl);
+    a.piece_sums = reinterpret_cast<double2*>(ws + r.sums);
     a.joined = reinterpret_cast<int64_t*>(ws + r.joined);
-    a.part_clipped = reinterpret_cast<int32_t*>(ws + r.clipped);
-    a.part_count = reinterpret_cast<int32_t*>(ws + r.count);
+    a.piece_counts = reinterpret_cast<int2*>(ws + r.counts);
   }
   if (B * T > 0)
-    hipLaunchKernelGGL(k_policy, dim3(static_cast<unsigned>(ceil_div(B * a.parts, 4))), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_policy, dim3(policy_blocks(B, T)), dim3(256), 0, s, a);
   if (!none) {                            // without tokens: every sum is empty
     hipLaunchKernelGGL(k_policy_join, dim3(a.groups), dim3(JOIN_THREADS), 0, s, a);
     if (a.groups > 1) hipLaunchKernelGGL(k_policy_total, dim3(1), dim3(64), 0, s, a);
@@ -602,7 +646,7 @@ det_status det_policy_loss_grad(const float* logprob, int64_t s_logprob, const f
   if (!aligned4(g) || !aligned4(dlogprob) || !aligned8(count)) return fail(DET_EINVAL, "operands must be aligned to their element size");
   a.count = const_cast<int64_t*>(count);
   a.g = g; a.s_g = s_g; a.s_g_t = s_g_t; a.dlp = dlogprob;
-  hipLaunchKernelGGL(k_policy_grad, dim3(static_cast<unsigned>(ceil_div(B * a.parts, 4))), dim3(256), 0,
+  hipLaunchKernelGGL(k_policy_grad, dim3(policy_blocks(B, T)), dim3(256), 0,
                      static_cast<hipStream_t>(stream), a);
   return hip_check(hipGetLastError(), "policy loss gradient launch");
 }

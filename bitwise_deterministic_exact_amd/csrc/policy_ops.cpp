@@ -27,6 +27,10 @@ int64_t stride_of(const Tensor& t) { return t.defined() ? t.stride(0) : 0; }
 template <class T>
 const T* ptr(const Tensor& t) { return t.defined() ? static_cast<const T*>(t.const_data_ptr()) : nullptr; }
 
+// an input without a gradient
+Tensor constant(const Tensor& t) { return t.requires_grad() ? t.detach() : t; }
+OptTensor constant(const OptTensor& t) { return wants_grad(t) ? OptTensor(t->detach()) : t; }
+
 // ---------------------------------------------------------------- policy loss
 
 struct PolicyOptions {
@@ -156,8 +160,8 @@ std::tuple<Tensor, Tensor, Tensor> policy_loss(const Tensor& lp, const Tensor& o
   for (const OptTensor& t : {OptTensor(lp), OptTensor(old), OptTensor(adv), ref}) no_tangent(t, "policy_loss");
   const det_reduction red = reduction_of(reduction, "policy_loss");
   if (at::GradMode::is_enabled() && wants_grad(lp)) {
-    const OptTensor r = ref ? OptTensor(ref->detach()) : ref;
-    const variable_list v = PolicyFn::apply(lp, old.detach(), adv.detach(), mask, r, low, high, kl_weight, static_cast<int64_t>(red));
+    const variable_list v = PolicyFn::apply(lp, constant(old), constant(adv), mask, constant(ref), low, high, kl_weight,
+                                            static_cast<int64_t>(red));
     return {v[0], v[1], v[2]};
   }
   const Policy p = policy_forward(lp, old, adv, mask, ref, {low, high, kl_weight, red});
@@ -283,7 +287,6 @@ std::tuple<Tensor, Tensor, Tensor> preference_loss(const Tensor& chosen, const T
   for (const OptTensor& t : {OptTensor(chosen), OptTensor(rejected), ref_chosen, ref_rejected}) no_tangent(t, "preference_loss");
   const det_preference k = kind_of(kind, "preference_loss");
   if (at::GradMode::is_enabled() && (wants_grad(chosen) || wants_grad(rejected))) {
-    auto constant = [](const OptTensor& t) { return t ? OptTensor(t->detach()) : t; };
     const variable_list v = PreferenceFn::apply(chosen, rejected, constant(ref_chosen), constant(ref_rejected), mask_chosen,
                                                 mask_rejected, static_cast<int64_t>(k), beta, margin, smooth, by_length);
     return {v[0], v[1], v[2]};

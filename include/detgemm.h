@@ -567,8 +567,8 @@ typedef enum { DET_SAVE_NONE = 0, DET_SAVE_HALF = 1, DET_SAVE_INT8 = 2 } det_sav
  *   act               silu g / (1 + e^-g); gelu g Phi(g); gelu_tanh
  *                     0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
  *   h                 [N][F] contiguous of type h_dt
- *   save              what gate and up ([N][F] contiguous) get: nothing (null
- *                     pointers), or g and u as fp16 elements or int8 codes, whose
+ *   save              what gate and up ([N] rows of F, s_kept >= F apart; a
+ *                     multiple of 4 is faster) get: nothing (null pointers), or g and u as fp16 elements or int8 codes, whose
  *                     blocks' exponents go to gate_exp and up_exp
  *                     [N][ceil(F / 32)]
  *   workspace         det_gated_linear_workspace_bytes(N, C, F, save, aligned),
@@ -584,8 +584,8 @@ int64_t det_gated_linear_workspace_bytes(int64_t N, int64_t C, int64_t F, det_sa
 
 det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int64_t s_gate, const void* w_up,
                             int64_t s_up, int64_t N, int64_t C, int64_t F, det_activation act, det_dtype h_dt, void* h,
-                            det_save save, void* gate, void* up, int8_t* gate_exp, int8_t* up_exp, void* workspace,
-                            size_t workspace_bytes, void* stream);
+                            det_save save, void* gate, void* up, int64_t s_kept, int8_t* gate_exp, int8_t* up_exp,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * det_gated_linear_grad -- the gradients of det_gated_linear.  With dg = dh u
@@ -611,8 +611,8 @@ int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, i
 
 det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, const void* x, int64_t s_x,
                                  const int8_t* x_exp, const void* w_gate, int64_t s_gate, const void* w_up,
-                                 int64_t s_up, det_save save, const void* gate, const void* up, const int8_t* gate_exp,
-                                 const int8_t* up_exp, int64_t N, int64_t C, int64_t F, det_activation act, void* dx,
+                                 int64_t s_up, det_save save, const void* gate, const void* up, int64_t s_kept,
+                                 const int8_t* gate_exp, const int8_t* up_exp, int64_t N, int64_t C, int64_t F, det_activation act, void* dx,
                                  void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
@@ -659,7 +659,7 @@ typedef enum { DET_PREFER_SIGMOID = 0, DET_PREFER_HINGE = 1, DET_PREFER_IPO = 2 
  *                     value each, 0 where nothing counts
  *   count             [B + 1] int64: the rows' counts and the divisor of the
  *                     tokens' or the rows' sum, for the gradient; null with none
- *   workspace         det_policy_loss_workspace_bytes(B, T, reduction), 8-byte
+ *   workspace         det_policy_loss_workspace_bytes(B, T, reduction), 16-byte
  *                     aligned
  * A row's sums are formed in 64 bits in one order per T and rounded to fp32
  * (for sequences after the division by its count); the rows' values are added

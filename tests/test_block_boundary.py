@@ -18,13 +18,14 @@ EINVAL, EDTYPE = _lib.DET_EINVAL, _lib.DET_EDTYPE
 
 
 def _gated(x=A, s_x=64, wg=A, s_g=64, wu=A, s_u=64, N=4, C=64, F=8, act=0, dt=1, h=B, save=0, gate=None, up=None, ge=None,
-           ue=None, ws=B, n=1 << 30):
-    return _lib.load().det_gated_linear(x, s_x, wg, s_g, wu, s_u, N, C, F, act, dt, h, save, gate, up, ge, ue, ws, n, None)
+           ue=None, ws=B, n=1 << 30, s_k=8):
+    return _lib.load().det_gated_linear(x, s_x, wg, s_g, wu, s_u, N, C, F, act, dt, h, save, gate, up, s_k, ge, ue, ws, n, None)
 
 
 def _grad(dt=1, dh=A, s_dh=8, x=A, s_x=64, xe=None, wg=A, s_g=64, wu=A, s_u=64, save=1, gate=A, up=A, ge=A, ue=A, N=4,
-          C=64, F=8, act=0, dx=B, dwg=B, dwu=B, ws=B, n=1 << 30):
-    return _lib.load().det_gated_linear_grad(dt, dh, s_dh, x, s_x, xe, wg, s_g, wu, s_u, save, gate, up, ge, ue, N, C, F, act,
+          C=64, F=8, act=0, dx=B, dwg=B, dwu=B, ws=B, n=1 << 30,
+          s_k=8):
+    return _lib.load().det_gated_linear_grad(dt, dh, s_dh, x, s_x, xe, wg, s_g, wu, s_u, save, gate, up, s_k, ge, ue, N, C, F, act,
                                              dx, dwg, dwu, ws, n, None)
 
 
@@ -43,7 +44,8 @@ def _unpack(codes=A, s=8, exps=A, N=2, C=8, dt=0, y=B):
     (lambda: _gated(N=(1 << 22) + 1), EINVAL), (lambda: _gated(x=NULL), EINVAL), (lambda: _gated(wg=NULL), EINVAL),
     (lambda: _gated(wu=NULL), EINVAL), (lambda: _gated(s_x=-64), EINVAL), (lambda: _gated(s_u=-1), EINVAL),
     (lambda: _gated(x=ODD), EINVAL), (lambda: _gated(wu=ODD), EINVAL), (lambda: _gated(h=NULL), EINVAL),
-    (lambda: _gated(h=P((1 << 21) + 2), dt=0), EINVAL), (lambda: _gated(save=1, gate=B), EINVAL), (lambda: _gated(save=1, gate=B, up=B, ge=B), EINVAL),
+    (lambda: _gated(h=P((1 << 21) + 2), dt=0), EINVAL), (lambda: _gated(save=1, gate=B), EINVAL), (lambda: _gated(save=1, gate=B, up=B, ge=B, ue=B, s_k=7), EINVAL),
+    (lambda: _grad(s_k=-8), EINVAL), (lambda: _gated(save=1, gate=B, up=B, ge=B), EINVAL),
     (lambda: _gated(save=1, gate=B, up=ODD, ge=B, ue=B), EINVAL), (lambda: _gated(save=2, gate=B, up=B, ge=B), EINVAL),
     # an operand that needs a padded copy, and no room for it
     (lambda: _gated(N=100, C=65, s_x=65, s_g=65, s_u=65, ws=NULL, n=0), EINVAL),
@@ -220,7 +222,7 @@ O2, O4, N8 = P((1 << 20) + 2), P((1 << 21) + 4), float("nan")
     lambda: _policy(adv_t=2), lambda: _policy(red=3), lambda: _policy(red=-1), lambda: _policy(lp=NULL), lambda: _policy(old=NULL),
     lambda: _policy(adv=NULL), lambda: _policy(lp=O2), lambda: _policy(ref=O2), lambda: _policy(loss=NULL), lambda: _policy(kl=NULL),
     lambda: _policy(clipped=NULL), lambda: _policy(count=NULL), lambda: _policy(count=O4), lambda: _policy(loss=O2),
-    lambda: _policy(ws=NULL), lambda: _policy(n=7), lambda: _policy(ws=O4),
+    lambda: _policy(ws=NULL), lambda: _policy(n=7), lambda: _policy(ws=P((1 << 21) + 8)),
     lambda: _policy_grad(lp=NULL), lambda: _policy_grad(red=7), lambda: _policy_grad(count=NULL), lambda: _policy_grad(g=NULL),
     lambda: _policy_grad(s_g=-1), lambda: _policy_grad(s_gt=-1), lambda: _policy_grad(d=NULL), lambda: _policy_grad(d=O2),
     lambda: _policy_grad(low=2.0), lambda: _policy_grad(beta=1.0), lambda: _policy_grad(count=O4),
@@ -244,9 +246,9 @@ def test_empty_losses_are_no_ops():
 
 def test_loss_workspace_sizes():
     f = _lib.load().det_policy_loss_workspace_bytes
-    # per part of 512 tokens two sums in 64 bits and two counts; per workgroup that joins rows 35 words
-    assert f(3, 512, 1) == 3 * 24 + 35 * 8 and f(3, 513, 2) == 6 * 24 + 35 * 8
-    assert f((1 << 14) + 1, 512, 1) == ((1 << 14) + 1) * 24 + 2 * 35 * 8
+    # per piece (2048 tokens, or a row of up to 512) two sums in 64 bits and two counts; per workgroup that joins rows 35 words
+    assert f(3, 512, 1) == 3 * 24 + 35 * 8 and f(3, 513, 2) == 3 * 24 + 35 * 8 and f(3, 2049, 2) == 6 * 24 + 35 * 8
+    assert f((1 << 13) + 1, 512, 1) == ((1 << 13) + 1) * 24 + 2 * 35 * 8
     assert f(3, 512, 0) == 0 and f(0, 512, 1) == 0 and f(3, 0, 1) == 0
 
 

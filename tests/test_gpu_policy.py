@@ -13,9 +13,9 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 U = 2.0 ** -24                                      # half a step of fp32
 NAN, INF = float("nan"), float("inf")
-# one token, ragged vectors, one and several parts of 512, more parts than one thread adds, more rows than one
-# workgroup joins
-SIZES = [(1, 1), (3, 7), (8, 300), (5, 512), (4, 513), (2, 5000), (3, 9000), (700, 33), (17000, 3)]
+# one token, ragged vectors, rows of one wave and of one and several workgroups, more pieces than one thread adds,
+# more rows than one workgroup joins
+SIZES = [(1, 1), (3, 7), (8, 300), (5, 512), (4, 513), (2, 5000), (3, 9000), (1, 40000), (700, 33), (17000, 3)]
 
 
 def answers(seed, B, T, per_token=True, ref=True, masked=True):
