@@ -647,7 +647,7 @@ __global__ __launch_bounds__(64 * COL_WAVES) void k_norm_columns(ColArgs a) {
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         const uint32_t u = k0 + i * STEP < end ? __float_as_uint(v[i]) : 0u;
-        if ((u & 0x7F800000u) == 0x7F800000u) bad[lane] = 1;
+        if (((u >> 23) & 0xFFu) == 0xFFu) bad[lane] = 1;
         else add_digits(u, [&](int j, int64_t v) { atomicAdd(&dg[j][lane], static_cast<unsigned long long>(v)); });
       }
     }

@@ -221,7 +221,7 @@ __global__ __launch_bounds__(256) void k_policy(PolicyArgs a) {
 }
 
 // Rows joined: a row's pieces are added in 64 bits, in ascending order (up to 16
-// of them) or over the lanes of a wave; the rows' values, rounded to fp32, are
+// of them) or over the lanes of a wave; the rows' values, to 48 bits, are
 // added exactly.  Three sums (loss, KL, clipped) of NDIG digits, their values
 // that are not finite by kind, and two counts.
 constexpr int SUMS = 3, JOINED = SUMS * NDIG + SUMS + 2, SERIAL = 16, AHEAD = 8, JOIN_THREADS = 1024;
@@ -297,9 +297,15 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_policy_join(PolicyArgs a) {
 #pragma unroll
     for (int k = 0; k < SUMS; ++k) {
       if (a.reduction == DET_REDUCE_SEQUENCES) sum[k] /= static_cast<double>(max<int64_t>(count, 1));
-      const float v = static_cast<float>(sum[k]);
-      if (!(fabsf(v) < INFINITY)) atomicOr(&s.kinds[k], v != v ? 1 : v > 0.0f ? 2 : 4);
-      else add_digits(__float_as_uint(v), [&](int j, int64_t x) { atomicAdd(&s.digits[k][j][lane], static_cast<unsigned long long>(x)); });
+      // two fp32 parts, 48 bits: what a row's rounding to one would leave shows where rows cancel
+      const float hi = static_cast<float>(sum[k]), lo = static_cast<float>(sum[k] - static_cast<double>(hi));
+      auto add = [&](int j, int64_t x) { atomicAdd(&s.digits[k][j][lane], static_cast<unsigned long long>(x)); };
+      if (!(fabsf(hi) < INFINITY)) {
+        atomicOr(&s.kinds[k], hi != hi ? 1 : hi > 0.0f ? 2 : 4);
+      } else {
+        add_digits(__float_as_uint(hi), add);
+        add_digits(__float_as_uint(lo), add);
+      }
     }
   }
 #pragma unroll

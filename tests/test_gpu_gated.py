@@ -357,3 +357,22 @@ def test_module_and_a_feed_forward_block():
     assert all(torch.isfinite(g).all() and g.dtype == BF16 for g in grads)
     again = torch.autograd.grad(det.exact_mse_loss(down(up(x))), [x, *up.parameters(), *down.parameters()])
     assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+def test_rows_past_32_bits():
+    # h, what is kept and dg and du pass 2^32 bytes; the last rows are those of a small batch
+    N, C, F = 560000, 64, 4160
+    g = torch.Generator(device=DEV).manual_seed(16)
+    x = torch.randn(N, C, generator=g, device=DEV).to(BF16)
+    wg, wu = (torch.randn(F, C, generator=g, device=DEV).to(BF16) / 8 for _ in range(2))
+    h, s = det.gated_linear_forward(x, wg, wu)
+    part, t = det.gated_linear_forward(x[-70:], wg, wu)
+    assert torch.equal(h[-70:], part) and torch.equal(s.up.values[-70:], t.up.values)
+    assert torch.equal(s.gate.exponents[-70:], t.gate.exponents)
+    # a gradient of the last rows alone: dx is theirs, dw is that of these rows after rows of zeros
+    dh = torch.zeros(N, F, device=DEV, dtype=BF16)
+    dh[-64:] = torch.randn(64, F, generator=g, device=DEV).to(BF16)
+    dx, dwg, dwu = det.gated_linear_backward(dh, x, wg, wu, s)
+    small = det.gated_linear_backward(dh[-64:], x[-64:], wg, wu, det.gated_linear_forward(x[-64:], wg, wu)[1])
+    assert torch.equal(dx[-64:], small[0]) and (dx[:-64] == 0).all()
+    assert torch.equal(dwg, small[1]) and torch.equal(dwu, small[2])

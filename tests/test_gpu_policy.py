@@ -470,3 +470,17 @@ def test_rows_past_32_bits():
     one = torch.ones((), device=DEV)
     d = det.policy_loss_backward(one, lp, old, adv, mask, count)
     assert torch.equal(d[-1:], det.policy_loss_backward(one, lp[-1:], old[-1:], adv[-1:], mask[-1:], c2)) and (d[:-1] == 0).all()
+
+
+def test_rows_that_cancel_are_added_exactly():
+    # with r = 1 a token's loss is -A, exactly; a row of two has a sum of at most 48 bits
+    g = torch.Generator().manual_seed(12)
+    for B, T in ((5000, 1), (20001, 2)):
+        adv = torch.randn(B, T, generator=g) * torch.exp(2 * torch.randn(B, 1, generator=g))
+        adv[B // 2:2 * (B // 2)] = -adv[:B // 2]                  # what is left is the last row, and a trace
+        adv[3, 0] += 2.0 ** -20
+        lp = -torch.rand(B, T, generator=g)
+        total = torch.tensor(math.fsum((-adv.double()).flatten().tolist()), dtype=torch.float64).float()
+        want = (total.double() / (B * T)).float()
+        got = det.policy_loss(lp.to(DEV), lp.to(DEV), adv.to(DEV)).loss
+        assert got.item() == want.item()
