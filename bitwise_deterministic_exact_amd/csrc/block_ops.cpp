@@ -90,55 +90,61 @@ struct GatedGrads {
   Tensor dx, dwg, dwu;
 };
 
-// x: bfloat16 with no exponents, or its codes with them
+// x: bfloat16 with no exponents, or its codes with them; undefined where the
+// weights' gradients are not needed
 GatedGrads gated_backward(const Tensor& dh, const Tensor& x, const OptTensor& x_exp, const Tensor& wg,
                           const Tensor& wu, const Saved& kept, det_activation act, bool need_dx, bool need_dw) {
   const char* const what = "gated_linear_backward";
   not_traced(what);
-  check_gated(x.sizes(), x_exp ? at::kBFloat16 : x.scalar_type(), wg, wg, wu, what);
-  const int64_t C = x.size(-1), N = x.numel() / C, F = wg.size(0);
-  if (x.device() != wg.device()) refuse(what, ": x and the weights must share a device");
-  if (x_exp && (x.scalar_type() != at::kChar || x_exp->scalar_type() != at::kChar || x_exp->device() != x.device() ||
-                x_exp->sizes() != at::IntArrayRef(with_last(lead_of(x), (C + 31) / 32))))
-    refuse(what, ": a packed x needs int8 codes and one int8 exponent for each 32 of them");
-  const std::vector<int64_t> shape = with_last(lead_of(x), F), blocks = with_last(lead_of(x), (F + 31) / 32);
-  if (dh.sizes() != at::IntArrayRef(shape) || !known(dh.scalar_type()) || dh.device() != x.device())
-    refuse(what, ": dh must be float32 or bfloat16 of shape ", shape, " on x's device");
+  if (kept.gate.dim() < 1 || wg.dim() != 2) refuse(what, ": gate must be [..., F], w_gate [F, C]");
+  const at::IntArrayRef lead = lead_of(kept.gate);
+  const int64_t C = wg.size(1), F = wg.size(0);
+  const std::vector<int64_t> xs = with_last(lead, C), hs = with_last(lead, F), blocks = with_last(lead, (F + 31) / 32);
+  check_gated(xs, x.defined() && !x_exp ? x.scalar_type() : at::kBFloat16, wg, wg, wu, what);
+  auto has = [&](const Tensor& t, ScalarType type, const std::vector<int64_t>& shape) {
+    return t.scalar_type() == type && t.sizes() == at::IntArrayRef(shape) && t.device() == wg.device();
+  };
+  if (!has(dh, dh.scalar_type(), hs) || !known(dh.scalar_type()))
+    refuse(what, ": dh must be float32 or bfloat16 of shape ", hs, " on the weights' device");
   const bool int8 = kept.gate.scalar_type() == at::kChar;
   for (const Tensor* t : {&kept.gate, &kept.up})
-    if (t->scalar_type() != (int8 ? at::kChar : at::kHalf) || t->sizes() != at::IntArrayRef(shape) || t->device() != x.device())
-      refuse(what, ": gate and up must be as gated_linear_forward gives them");
+    if (!has(*t, int8 ? at::kChar : at::kHalf, hs)) refuse(what, ": gate and up must be as gated_linear_forward gives them");
   for (const Tensor* t : {&kept.gate_exp, &kept.up_exp})
-    if (t->scalar_type() != at::kChar || t->sizes() != at::IntArrayRef(blocks) || t->device() != x.device())
-      refuse(what, ": gate and up must be as gated_linear_forward gives them");
-  on_gpu(x, what, "x");
-  const c10::DeviceGuard guard(x.device());
+    if (!has(*t, at::kChar, blocks)) refuse(what, ": gate and up must be as gated_linear_forward gives them");
+  if (x_exp && (!has(x, at::kChar, xs) || !has(*x_exp, at::kChar, with_last(lead, (C + 31) / 32))))
+    refuse(what, ": a packed x needs int8 codes of shape ", xs, " and one int8 exponent for each 32 of them");
+  if (!x_exp && x.defined() && !has(x, at::kBFloat16, xs)) refuse(what, ": x must be of shape ", xs, " on the weights' device");
+  if (need_dw && !x.defined()) refuse(what, ": the weights' gradients need x");
+  on_gpu(wg, what, "w_gate");
+  const c10::DeviceGuard guard(wg.device());
   GatedGrads g;
   const auto bf16 = wg.options().dtype(at::kBFloat16);
-  if (need_dx) g.dx = at::empty(x.sizes(), bf16);
+  if (need_dx) g.dx = at::empty(xs, bf16);
   if (need_dw) {
     g.dwg = at::empty(wg.sizes(), bf16);
     g.dwu = at::empty(wu.sizes(), bf16);
   }
-  const Tensor dh2 = rows(dh), x2 = x_exp ? x.contiguous() : wide_rows(x);
-  Tensor g2 = wide_rows(wg), u2 = wide_rows(wu);
+  const Tensor dh2 = rows(dh), x2 = !need_dw ? Tensor() : x_exp ? x.contiguous() : wide_rows(x);
+  const Tensor xe = need_dw && x_exp ? x_exp->contiguous() : Tensor();
+  const Tensor ge = kept.gate_exp.contiguous(), ue = kept.up_exp.contiguous();
+  Tensor g2 = wide_rows(wg), u2 = wide_rows(wu), kg = rows(kept.gate), ku = rows(kept.up);
   if (g2.stride(0) != u2.stride(0)) {     // dx runs over both with one stride
     g2 = g2.contiguous();
     u2 = u2.contiguous();
   }
-  Tensor kg = rows(kept.gate), ku = rows(kept.up);
   if (kg.stride(0) != ku.stride(0)) {
     kg = kg.contiguous();
     ku = ku.contiguous();
   }
-  const Tensor xe = x_exp ? x_exp->contiguous() : Tensor(), ge = kept.gate_exp.contiguous(), ue = kept.up_exp.contiguous();
-  const int64_t bytes = det_gated_linear_grad_workspace_bytes(N, C, F, need_dx, need_dw, C % 64 == 0, x_exp.has_value());
-  const Tensor ws = bytes > 0 ? at::empty({bytes}, x.options().dtype(at::kByte)) : Tensor();
-  ok(det_gated_linear_grad(dt_of(dh.scalar_type()), in(dh2), dh2.stride(0), in(x2), x_exp ? C : x2.stride(0),
-                           static_cast<const int8_t*>(xe.defined() ? xe.const_data_ptr() : nullptr), in(g2), g2.stride(0), in(u2), u2.stride(0),
-                           int8 ? DET_SAVE_INT8 : DET_SAVE_HALF, in(kg), in(ku), kg.stride(0), static_cast<const int8_t*>(in(ge)), static_cast<const int8_t*>(in(ue)), N,
-                           C, F, act, out<void>(g.dx), out<void>(g.dwg), out<void>(g.dwu), out<void>(ws),
-                           static_cast<size_t>(bytes), stream_of(x)));
+  auto bytes_of = [](const Tensor& t) { return t.defined() ? static_cast<const int8_t*>(t.const_data_ptr()) : nullptr; };
+  const int64_t N = kg.size(0);
+  const int64_t bytes = det_gated_linear_grad_workspace_bytes(N, C, F, need_dx, need_dw, C % 64 == 0, xe.defined());
+  const Tensor ws = bytes > 0 ? at::empty({bytes}, wg.options().dtype(at::kByte)) : Tensor();
+  ok(det_gated_linear_grad(dt_of(dh.scalar_type()), in(dh2), dh2.stride(0), bytes_of(x2),
+                           xe.defined() || !x2.defined() ? C : x2.stride(0), bytes_of(xe), in(g2), g2.stride(0), in(u2),
+                           u2.stride(0), int8 ? DET_SAVE_INT8 : DET_SAVE_HALF, in(kg), in(ku), kg.stride(0), bytes_of(ge),
+                           bytes_of(ue), N, C, F, act, out<void>(g.dx), out<void>(g.dwg), out<void>(g.dwu), out<void>(ws),
+                           static_cast<size_t>(bytes), stream_of(wg)));
   return g;
 }
 
@@ -188,9 +194,12 @@ struct GatedFn : torch::autograd::Function<GatedFn> {
                         std::optional<ScalarType> out_dtype, int64_t save) {
     Saved kept;
     Tensor h = gated_forward(x, wg, wu, static_cast<det_activation>(act), out_dtype, static_cast<det_save>(save), kept);
-    // x enters the weights' gradients only; its shape is asked for in any case
-    Tensor kx = x, xe;
-    if (save == DET_SAVE_INT8) std::tie(kx, xe) = pack_int8(x);
+    // x enters the weights' gradients only
+    Tensor kx, xe;
+    if (wants_grad(wg) || wants_grad(wu)) {
+      if (save == DET_SAVE_INT8) std::tie(kx, xe) = pack_int8(x);
+      else kx = x;
+    }
     ctx->save_for_backward({kx, xe, wg, wu, kept.gate, kept.up, kept.gate_exp, kept.up_exp});
     ctx->saved_data["act"] = act;
     return h;
@@ -237,10 +246,10 @@ void bind_block(py::module_& m) {
           return std::make_tuple(h, k.gate, k.up, k.gate_exp, k.up_exp);
         }, release());
   m.def("gated_linear_backward",
-        [](const Tensor& dh, const Tensor& x, const OptTensor& x_exp, const Tensor& wg, const Tensor& wu,
+        [](const Tensor& dh, const OptTensor& x, const OptTensor& x_exp, const Tensor& wg, const Tensor& wu,
            const Tensor& gate, const Tensor& up, const Tensor& gate_exp, const Tensor& up_exp,
            const std::string& activation, bool need_dx, bool need_dw) {
-          const GatedGrads g = gated_backward(dh, x, x_exp, wg, wu, {gate, up, gate_exp, up_exp}, act_of(activation, "gated_linear_backward"), need_dx, need_dw);
+          const GatedGrads g = gated_backward(dh, x.value_or(Tensor()), x_exp, wg, wu, {gate, up, gate_exp, up_exp}, act_of(activation, "gated_linear_backward"), need_dx, need_dw);
           return std::make_tuple(opt(g.dx), opt(g.dwg), opt(g.dwu));
         }, release());
   m.def("pack_int8", &pack_int8, release());

@@ -55,12 +55,13 @@ def gated_linear_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tens
     return h, GatedState(kind(gate, ge), kind(up, ue))
 
 
-def gated_linear_backward(dh: torch.Tensor, x: Union[torch.Tensor, PackedInt8], w_gate: torch.Tensor,
+def gated_linear_backward(dh: torch.Tensor, x: Union[torch.Tensor, PackedInt8, None], w_gate: torch.Tensor,
                           w_up: torch.Tensor, state: GatedState, *, activation: str = "silu", need_dx: bool = True,
                           need_dw: bool = True):
     """(dx, dw_gate, dw_up), bfloat16, each None when not needed, for the
     incoming gradient dh of h (float32 or bfloat16).  x as the forward pass had
-    it, or pack_int8 of it; ``state`` comes from gated_linear_forward."""
+    it, or pack_int8 of it (None without need_dw); ``state`` comes from
+    gated_linear_forward."""
     x, xe = x if isinstance(x, PackedInt8) else (x, None)
     (gate, ge), (up, ue) = state
     return _lib.ops().gated_linear_backward(dh, x, xe, w_gate, w_up, gate, up, ge, ue, activation, need_dx, need_dw)

@@ -138,6 +138,9 @@ S = det.GatedState(_half(2, 6), _half(2, 6))
         det.PackedInt8(_i8(2, 6), _i8(2, 2)), det.PackedInt8(_i8(2, 6), _i8(2, 1)))), "gate and up"),
     (lambda: det.gated_linear_backward(_m(2, 6), det.PackedInt8(_i8(2, 4), _i8(2, 2)), _m(6, 4), _m(6, 4), S), "packed x"),
     (lambda: det.gated_linear_backward(_m(2, 6), det.PackedInt8(_m(2, 4), _i8(2, 1)), _m(6, 4), _m(6, 4), S), "packed x"),
+    (lambda: det.gated_linear_backward(_m(2, 6), _m(3, 4), _m(6, 4), _m(6, 4), S), "x must be"),
+    (lambda: det.gated_linear_backward(_m(2, 6), None, _m(6, 4), _m(6, 4), S), "need x"),
+    (lambda: det.gated_linear_backward(_m(2, 6), _m(2, 4), _m(6), _m(6, 4), S), "w_gate"),
     (lambda: det.DetGatedLinear(0, 4), "features"), (lambda: det.DetGatedLinear(4, 65537), "features"),
     (lambda: det.DetGatedLinear(4, 4, activation="tanh"), "activation"),
     (lambda: det.DetGatedLinear(4, 4, out_dtype=torch.float16), "out_dtype"),

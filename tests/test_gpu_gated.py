@@ -359,6 +359,26 @@ def test_module_and_a_feed_forward_block():
     assert all(torch.equal(a, b) for a, b in zip(grads, again))
 
 
+@pytest.mark.parametrize("ck", [None, "int8"])
+def test_frozen_weights_keep_nothing_of_x(ck):
+    x, wg, wu = operands(17, 70, 100, 65)
+    dh = torch.randn(70, 65, device=DEV).to(BF16)
+    _, s = det.gated_linear_forward(x, wg, wu, checkpoint=ck)
+    x.requires_grad_(True)
+    sizes = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (sizes.append(tuple(t.shape)), t)[1], lambda t: t):
+        h = det.gated_linear(x, wg, wu, checkpoint=ck)
+    assert (70, 100) not in sizes and (70, 4) not in sizes
+    dx, = torch.autograd.grad(h, x, dh)
+    assert torch.equal(dx, det.gated_linear_backward(dh, None, wg, wu, s, need_dw=False)[0])
+    # one weight alone, no gradient of x
+    for i in (1, 2):
+        leaves = [t.detach().clone().requires_grad_(j == i) for j, t in enumerate((x, wg, wu))]
+        kx = det.pack_int8(x) if ck else x.detach()
+        g, = torch.autograd.grad(det.gated_linear(*leaves, checkpoint=ck), leaves[i], dh)
+        assert torch.equal(g, det.gated_linear_backward(dh, kx, wg, wu, s, need_dx=False)[i])
+
+
 def test_rows_past_32_bits():
     # h, what is kept and dg and du pass 2^32 bytes; the last rows are those of a small batch
     N, C, F = 560000, 64, 4160
