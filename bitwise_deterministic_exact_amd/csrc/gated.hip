@@ -102,7 +102,7 @@ struct MmArgs {
   Operand A, A1, B;
   int64_t K;                              // a multiple of 64: what lies past the rows of k is 0
   int64_t ka, kb, turn;                   // by k: rows of k of A (and of A1), of B
-  int64_t tiles_a, tiles_b;
+  int64_t begin_a, begin_b, tiles_a, tiles_b;                // this launch's tiles
   // gated: h [n of B][n of A]; else D, rows [0, split0) in out, [split1, split1 + split0) in out1
   void* out; void* out1; int64_t split0, split1;
   // what the gradients read again
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(64 * WA * WB, FA * FB > 32 ? 1 : 2) void k_mm(MmArg
   const int wa = wave / WB, wb = wave % WB;
   int64_t ta, tb;
   tile_of(blockIdx.x, a.tiles_a, a.tiles_b, ta, tb);
-  const int64_t row_a = ta * TH, row_b = tb * TB;
+  const int64_t row_a = a.begin_a + ta * TH, row_b = a.begin_b + tb * TB;
 
   TileA A;
   TileB B;
@@ -630,18 +630,11 @@ bool direct(const void* p, int64_t stride, int64_t K) {
   return K % 64 == 0 && stride % 8 == 0 && stride >= K && stride <= STRIDE_MAX && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-template <bool GATED, bool A_BY_K, bool B_BY_K, int WA, int WB, int FA, int FB, int KS, int BUFS, bool SPREAD>
-void launch_tiles(MmArgs a, hipStream_t s) {
-  a.tiles_a = ceil_div(a.A.n, WA * FA * 16 / (GATED ? 2 : 1));
-  a.tiles_b = ceil_div(a.B.n, WB * FB * 16);
-  hipLaunchKernelGGL((k_mm<GATED, A_BY_K, B_BY_K, WA, WB, FA, FB, KS, BUFS, SPREAD>), dim3(static_cast<unsigned>(a.tiles_a * a.tiles_b)),
-                     dim3(64 * WA * WB), 0, s, a);
-}
 // Tiles of 64 x 64, 128 x 128, 128 x 256 or 256 x 256 (A x B): large ones move
 // fewer bytes per product, small ones fill the chip.  The rule takes the least of
 // what each would take, rounds (stages t + end), from what was measured (us per
-// stage of 64 k where half the CUs have a tile and where all have, and for a
-// tile's end; 64 x 64 fits twice on a CU).  4096 features of either weight, k
+// stage of 64 k where up to half the CUs have a tile and where all have, a last
+// round in between, and for a tile's end; 64 x 64 fits twice on a CU).  4096 features of either weight, k
 // 4096, by tokens: 256: 17 us (28, 52, 87 for the larger tiles), 512: 28 28 52
 // 87, 1024: 53 35 52 88, 2048: 103 69 65 89, 4096: 202 135 124 106.  The result's
 // bits are the same for all.
@@ -651,45 +644,95 @@ struct TileCost {
 };
 constexpr TileCost TILES[4] = {{64, 64, 512, 0.30, 0.50, 1.0}, {128, 128, 256, 0.50, 0.55, 2.0}, {128, 256, 256, 0.82, 0.95, 4.0},
                                {256, 256, 256, 1.3, 1.6, 8.0}};
-int tile_choice(int64_t na, int64_t nb, int64_t K) {
-  int best = 0;
+double tile_time(const TileCost& t, int64_t na, int64_t nb, int64_t K) {
+  const int64_t tiles = ceil_div(na, t.a) * ceil_div(nb, t.b), whole = tiles / t.slots, last = tiles % t.slots;
+  const double stages = static_cast<double>(K) / 64.0, share = static_cast<double>(last) / t.slots;
+  const double partly = t.half + (t.full - t.half) * std::max(0.0, 2.0 * share - 1.0);
+  return static_cast<double>(whole) * (stages * t.full + t.end) + (last > 0 ? stages * partly + t.end : 0.0);
+}
+struct Part {
+  int tile;
+  int64_t a0, a1, b0, b1;                 // of A (gated: of both halves together) and B
+};
+double best_tile(int64_t a0, int64_t a1, int64_t b0, int64_t b1, int64_t K, Part& p) {
   double least = 0.0;
   for (int i = 0; i < 4; ++i) {
-    const TileCost& t = TILES[i];
-    const int64_t tiles = ceil_div(na, t.a) * ceil_div(nb, t.b);
-    const double time = static_cast<double>(ceil_div(tiles, t.slots)) *
-                        (static_cast<double>(K) / 64.0 * (2 * tiles <= t.slots ? t.half : t.full) + t.end);
+    const double time = tile_time(TILES[i], a1 - a0, b1 - b0, K);
     if (i == 0 || time < least) {
-      best = i;
+      p = {i, a0, a1, b0, b1};
       least = time;
     }
   }
-  return best;
+  return least;
+}
+// One launch, or two where a last round would leave most CUs idle: whole rounds
+// of one tile first, then the rest with the tile that suits it.  5000 x 5000 x
+// 5000 forward 547 -> 483 us, dw of 8000 x 1000 x 10000 512 -> 429, of 1030 x 1024
+// x 4100, where the estimate misses, 42 -> 45.
+constexpr double LAUNCH = 4.0;            // us
+int plan(int64_t na, int64_t nb, int64_t K, Part (&parts)[2]) {
+  double least = best_tile(0, na, 0, nb, K, parts[0]);
+  int n = 1;
+  for (int i = 0; i < 4; ++i) {
+    const TileCost& t = TILES[i];
+    const int64_t ta = ceil_div(na, t.a), tb = ceil_div(nb, t.b), whole = ta * tb / t.slots * t.slots;
+    for (int by_b = 0; by_b < 2; ++by_b) {
+      const int64_t cut = whole / (by_b ? ta : tb);           // columns (rows) of tiles in whole rounds
+      if (cut < 1 || cut >= (by_b ? tb : ta)) continue;
+      const int64_t a1 = by_b ? na : cut * t.a, b1 = by_b ? cut * t.b : nb;
+      Part rest{};
+      const double time = LAUNCH + tile_time(t, a1, b1, K) + best_tile(by_b ? 0 : a1, na, by_b ? b1 : 0, nb, K, rest);
+      if (time < least) {
+        least = time;
+        parts[0] = {i, 0, a1, 0, b1};
+        parts[1] = rest;
+        n = 2;
+      }
+    }
+  }
+  return n;
+}
+
+template <bool GATED, bool A_BY_K, bool B_BY_K, int WA, int WB, int FA, int FB, int KS, int BUFS, bool SPREAD>
+void launch_tiles(MmArgs a, const Part& p, hipStream_t s) {
+  constexpr int halves = GATED ? 2 : 1;
+  a.begin_a = p.a0 / halves;
+  a.begin_b = p.b0;
+  a.tiles_a = ceil_div(p.a1 - p.a0, WA * FA * 16);
+  a.tiles_b = ceil_div(p.b1 - p.b0, WB * FB * 16);
+  hipLaunchKernelGGL((k_mm<GATED, A_BY_K, B_BY_K, WA, WB, FA, FB, KS, BUFS, SPREAD>), dim3(static_cast<unsigned>(a.tiles_a * a.tiles_b)),
+                     dim3(64 * WA * WB), 0, s, a);
 }
 
 // By row 64 k to a stage (whole lines of memory), its reads before its MFMAs;
 // by k 32 and 64, spread: 8192 x 4096 x 11008 forward 1187 us so, 1204 spread,
 // 1306 with 32; dx and its dg and du 1287 against 1387 and 1362, dw 1349 against 1500.
 template <bool GATED, bool A_BY_K, bool B_BY_K>
-void launch_mm(const MmArgs& a, hipStream_t s) {
-  switch (tile_choice(a.A.n * (GATED ? 2 : 1), a.B.n, a.K)) {
+void launch_part(const MmArgs& a, const Part& p, hipStream_t s) {
+  switch (p.tile) {
     case 0:
-      if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 64, 5, false>(a, s);
-      else if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 2, 1, 64, 5, true>(a, s);
-      else launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 32, 5, true>(a, s);
+      if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 64, 5, false>(a, p, s);
+      else if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 2, 1, 64, 5, true>(a, p, s);
+      else launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 32, 5, true>(a, p, s);
       break;
     case 1:
-      if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 2, 64, 5, true>(a, s);
-      else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 2, 4, 4, 32, 5, true>(a, s);
+      if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 2, 64, 5, true>(a, p, s);
+      else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 2, 4, 4, 32, 5, true>(a, p, s);
       break;
     case 2:
-      if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 64, 3, !GATED>(a, s);
-      else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 32, 5, true>(a, s);
+      if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 64, 3, !GATED>(a, p, s);
+      else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 32, 5, true>(a, p, s);
       break;
     default:
-      if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 64, 2, false>(a, s);
-      else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 32, 5, true>(a, s);
+      if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 64, 2, false>(a, p, s);
+      else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 32, 5, true>(a, p, s);
   }
+}
+template <bool GATED, bool A_BY_K, bool B_BY_K>
+void launch_mm(const MmArgs& a, hipStream_t s) {
+  Part parts[2];
+  const int n = plan(a.A.n * (GATED ? 2 : 1), a.B.n, a.K, parts);
+  for (int i = 0; i < n; ++i) launch_part<GATED, A_BY_K, B_BY_K>(a, parts[i], s);
 }
 
 unsigned blocks_for(int64_t threads) { return static_cast<unsigned>(ceil_div(threads, 256)); }
