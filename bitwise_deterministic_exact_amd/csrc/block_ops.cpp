@@ -45,7 +45,7 @@ Tensor wide_rows(const Tensor& t) {
   const Tensor r = rows(t);
   if (r.size(1) % 64 != 0) return r;
   const bool fits = reinterpret_cast<uintptr_t>(r.const_data_ptr()) % 16 == 0 && r.stride(0) % 8 == 0 &&
-                    r.stride(0) >= r.size(1) && r.stride(0) <= (int64_t{1} << 22);
+                    r.stride(0) >= r.size(1) && r.stride(0) <= (int64_t{1} << 21);
   return fits || r.size(0) == 0 ? r : r.clone(at::MemoryFormat::Contiguous);
 }
 

@@ -26,7 +26,6 @@ using namespace rowops;
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
-using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------- activations
 
@@ -49,8 +48,8 @@ __device__ __forceinline__ Act act_of(float g) {
     const Sigmoid s = sigmoid(g);
     return {g * s.s, s.s * fmaf(g, s.rest, 1.0f)};
   } else if constexpr (ACT == DET_ACT_GELU_TANH) {
-    // 0.5 g (1 + tanh t) = g sigmoid(2 t)
-    const float g2 = g * g, in = g * fmaf(0.0713548163f, g2, 1.59576912f);
+    // 0.5 g (1 + tanh t) = g sigmoid(2 t); from 1e4 on g^2 no longer matters, and inf would
+    const float g2 = fminf(g * g, 1.0e4f), in = g * fmaf(0.0713548163f, g2, 1.59576912f);
     const Sigmoid s = sigmoid(in);
     const float slope = s.s * s.rest * fmaf(0.214064449f, g2, 1.59576912f);
     return {g * s.s, fmaf(g, slope, s.s)};
@@ -154,7 +153,7 @@ struct Tile {
     return T >= 128 ? s : ((k >> 1) & 1) | ((k >> 2) & 2);
   }
   // by row: what a row's pieces are swapped with
-  static __device__ __forceinline__ int swap_row(int r) { return KS == 64 ? r & 7 : (r >> 2) & 3; }
+  static __device__ __forceinline__ int swap_row(int r) { return KS == 64 ? r & 7 : ((r >> 1) ^ (r >> 3)) & 3; }
   int64_t stride;                         // bytes
   __amdgpu_buffer_rsrc_t buf;             // by row: of the tile
   int at;                                 // by row: bytes of k before the next stage
@@ -190,7 +189,8 @@ struct Tile {
   // takes, get the next rows' elements or 0.
   __device__ __forceinline__ void copy(char* to, int wave) {
     if constexpr (BY_K) {
-      // no branch: one would keep the copies from going between the MFMAs
+      // No branch: one would keep the copies from going between the MFMAs.  Without
+      // rows, down to -BUFS KS of them, the bytes are at most cols - stride <= 0.
       const __amdgpu_buffer_rsrc_t b = buffer_of(next, max(0, (min(left, KS) - 1) * static_cast<int>(stride) + cols));
 #pragma unroll
       for (int j = 0; j < COPIES; ++j)
@@ -224,7 +224,7 @@ struct Tile {
 #endif
 
 template <bool GATED, bool A_BY_K, bool B_BY_K, int WA, int WB, int FA, int FB, int KS, int BUFS, bool SPREAD>
-__global__ __launch_bounds__(64 * WA * WB, FA * FB > 32 ? 1 : 2) void k_mm(MmArgs a) {
+__global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int NW = WA * WB, TA = WA * FA * 16, TB = WB * FB * 16, TH = GATED ? TA / 2 : TA;
   using TileA = Tile<A_BY_K, TA, NW, KS>;
@@ -317,9 +317,7 @@ __global__ __launch_bounds__(64 * WA * WB, FA * FB > 32 ? 1 : 2) void k_mm(MmArg
       }
     } else {
       __builtin_amdgcn_sched_barrier(0);
-      //PRIO1
       multiply(now);
-      //PRIO0
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -620,7 +618,7 @@ __global__ __launch_bounds__(256) void k_clear(uint16_t* p, int64_t n) {
 // be copied first.  64 x 4096 x 11008: 94 us against 45 with tiles, 48 x 2048 x
 // 5461 22 against 10.5, with rows of 2047 22 against 30; one token 34 us.
 constexpr int64_t FEW = 16, FEW_COPIED = 64;
-constexpr int64_t STRIDE_MAX = 1 << 22;   // 256 rows lie within 2^31 bytes: offsets fit a buffer's 32 bits
+constexpr int64_t STRIDE_MAX = 1 << 21;   // 383 rows before and after an operand's end lie within 2^31 bytes
 
 int64_t up_to(int64_t v, int64_t m) { return ceil_div(v, m) * m; }
 int64_t room(int64_t bytes) { return up_to(bytes, 256); }
@@ -634,10 +632,10 @@ bool direct(const void* p, int64_t stride, int64_t K) {
 // fewer bytes per product, small ones fill the chip.  The rule takes the least of
 // what each would take, rounds (stages t + end), from what was measured (us per
 // stage of 64 k where up to half the CUs have a tile and where all have, a last
-// round in between, and for a tile's end; 64 x 64 fits twice on a CU).  4096 features of either weight, k
-// 4096, by tokens: 256: 17 us (28, 52, 87 for the larger tiles), 512: 28 28 52
-// 87, 1024: 53 35 52 88, 2048: 103 69 65 89, 4096: 202 135 124 106.  The result's
-// bits are the same for all.
+// round in between, and for a tile's end; 64 x 64 fits twice on a CU).  4096
+// features of gate and up together, k 4096, by tokens: 256: 17 us (28, 52, 87 for
+// the larger tiles), 512: 28 28 52 87, 1024: 53 35 52 88, 2048: 103 69 65 89,
+// 4096: 202 135 124 106.  The result's bits are the same for all.
 struct TileCost {
   int a, b, slots;
   double half, full, end;

@@ -574,7 +574,7 @@ typedef enum { DET_SAVE_NONE = 0, DET_SAVE_HALF = 1, DET_SAVE_INT8 = 2 } det_sav
  *   workspace         det_gated_linear_workspace_bytes(N, C, F, save, aligned),
  *                     256-byte aligned; `aligned`: x and both weights start at
  *                     multiples of 16 bytes and their strides are multiples of
- *                     8 in [C, 2^22]
+ *                     8 in [C, 2^21]
  * g and u are fp32 sums over k in one fixed order (matrix-core products of 32 k
  * each, ascending), h is rounded once; values that are not finite take part as
  * IEEE arithmetic has it.  N <= 2^22, C and F <= 65536.

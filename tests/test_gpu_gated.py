@@ -379,6 +379,40 @@ def test_frozen_weights_keep_nothing_of_x(ck):
         assert torch.equal(g, det.gated_linear_backward(dh, kx, wg, wu, s, need_dx=False)[i])
 
 
+@pytest.mark.parametrize("N,F", [(70, 40), (300, 130)])
+def test_rows_far_apart(N, F):
+    # strides up to the largest that is read in place (2^21 elements), and above it
+    C = 64
+    x, wg, wu = operands(18, N, C, F)
+    dh = torch.randn(N, F, device=DEV).to(BF16)
+    h, s = det.gated_linear_forward(x, wg, wu)
+    want = det.gated_linear_backward(dh, x, wg, wu, s)
+    for stride in (1 << 21, (1 << 21) + 8, 1 << 22):
+        room = torch.empty(max(N, F) * stride, dtype=BF16, device=DEV)
+        far = lambda t: room.as_strided(t.shape, (stride, 1)).copy_(t)
+        for i in range(3):
+            v = [far(t) if j == i else t for j, t in enumerate((x, wg, wu))]
+            h2, s2 = det.gated_linear_forward(*v)
+            assert torch.equal(h2, h)
+            assert all(torch.equal(a, b) for a, b in zip(det.gated_linear_backward(dh, *v, s2), want))
+        del room
+
+
+def test_activations_far_out():
+    # their limits' slopes, 1 and 0, as far as fp32 goes
+    one = torch.ones(70, 1, device=DEV, dtype=BF16)
+    for act in ACTS:
+        for size in (1e3, 1e10, 1e20, 1e30):
+            for sign in (1.0, -1.0):
+                wg, wu = torch.full((8, 1), sign * size, device=DEV, dtype=BF16), torch.full((8, 1), 2.0 ** -60, device=DEV, dtype=BF16)
+                h, s = det.gated_linear_forward(one, wg, wu, activation=act)
+                dx, dwg, dwu = det.gated_linear_backward(torch.ones(70, 8, device=DEV, dtype=BF16), one, wg, wu, s, activation=act)
+                assert torch.isfinite(dx).all()
+                g, u = wg[0, 0].item(), 2.0 ** -60
+                assert dwg[0, 0].item() == (70 * u if sign > 0 else 0)
+                assert abs(dwu[0, 0].item() - (70 * g if sign > 0 else 0)) <= 2 * U[BF16] * abs(70 * g)
+
+
 def test_rows_past_32_bits():
     # h, what is kept and dg and du pass 2^32 bytes; the last rows are those of a small batch
     N, C, F = 560000, 64, 4160
