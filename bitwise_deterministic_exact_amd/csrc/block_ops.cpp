@@ -108,12 +108,14 @@ GatedGrads gated_backward(const Tensor& dh, const Tensor& x, const OptTensor& x_
     refuse(what, ": dh must be float32 or bfloat16 of shape ", hs, " on the weights' device");
   const bool int8 = kept.gate.scalar_type() == at::kChar;
   for (const Tensor* t : {&kept.gate, &kept.up})
-    if (!has(*t, int8 ? at::kChar : at::kHalf, hs)) refuse(what, ": gate and up must be as gated_linear_forward gives them");
+    if (!has(*t, int8 ? at::kChar : at::kHalf, hs))
+      refuse(what, ": gate and up must be as gated_linear_forward gives them");
   for (const Tensor* t : {&kept.gate_exp, &kept.up_exp})
     if (!has(*t, at::kChar, blocks)) refuse(what, ": gate and up must be as gated_linear_forward gives them");
   if (x_exp && (!has(x, at::kChar, xs) || !has(*x_exp, at::kChar, with_last(lead, (C + 31) / 32))))
     refuse(what, ": a packed x needs int8 codes of shape ", xs, " and one int8 exponent for each 32 of them");
-  if (!x_exp && x.defined() && !has(x, at::kBFloat16, xs)) refuse(what, ": x must be of shape ", xs, " on the weights' device");
+  if (!x_exp && x.defined() && !has(x, at::kBFloat16, xs))
+    refuse(what, ": x must be of shape ", xs, " on the weights' device");
   if (need_dw && !x.defined()) refuse(what, ": the weights' gradients need x");
   on_gpu(wg, what, "w_gate");
   const c10::DeviceGuard guard(wg.device());
@@ -129,8 +131,8 @@ GatedGrads gated_backward(const Tensor& dh, const Tensor& x, const OptTensor& x_
   const Tensor ge = kept.gate_exp.contiguous(), ue = kept.up_exp.contiguous();
   Tensor g2 = wide_rows(wg), u2 = wide_rows(wu), kg = rows(kept.gate), ku = rows(kept.up);
   if (g2.stride(0) != u2.stride(0)) {     // dx runs over both with one stride
-    g2 = g2.contiguous();
-    u2 = u2.contiguous();
+    g2 = g2.clone(at::MemoryFormat::Contiguous);              // contiguous() would keep a single row's stride
+    u2 = u2.clone(at::MemoryFormat::Contiguous);
   }
   if (kg.stride(0) != ku.stride(0)) {
     kg = kg.contiguous();
@@ -214,7 +216,8 @@ struct GatedFn : torch::autograd::Function<GatedFn> {
                          static_cast<det_activation>(ctx->saved_data["act"].toInt()), ctx->needs_input_grad(0),
                          ctx->needs_input_grad(1) || ctx->needs_input_grad(2));
     }
-    variable_list r = once_at_node({g.dx, ctx->needs_input_grad(1) ? g.dwg : Tensor(), ctx->needs_input_grad(2) ? g.dwu : Tensor()},
+    variable_list r = once_at_node({g.dx, ctx->needs_input_grad(1) ? g.dwg : Tensor(),
+                                    ctx->needs_input_grad(2) ? g.dwu : Tensor()},
                                    grads, "gated_linear");
     r.resize(6);
     return r;
@@ -249,7 +252,8 @@ void bind_block(py::module_& m) {
         [](const Tensor& dh, const OptTensor& x, const OptTensor& x_exp, const Tensor& wg, const Tensor& wu,
            const Tensor& gate, const Tensor& up, const Tensor& gate_exp, const Tensor& up_exp,
            const std::string& activation, bool need_dx, bool need_dw) {
-          const GatedGrads g = gated_backward(dh, x.value_or(Tensor()), x_exp, wg, wu, {gate, up, gate_exp, up_exp}, act_of(activation, "gated_linear_backward"), need_dx, need_dw);
+          const GatedGrads g = gated_backward(dh, x.value_or(Tensor()), x_exp, wg, wu, {gate, up, gate_exp, up_exp},
+                                              act_of(activation, "gated_linear_backward"), need_dx, need_dw);
           return std::make_tuple(opt(g.dx), opt(g.dwg), opt(g.dwu));
         }, release());
   m.def("pack_int8", &pack_int8, release());

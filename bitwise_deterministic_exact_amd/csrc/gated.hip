@@ -167,7 +167,8 @@ struct Tile {
   int left, cols;                         // by k: rows from there on, bytes of a row
   int from[COPIES];                       // by row: rows past the end are the last one again
   // `limit` of its a or b from `first` on are the tile's
-  __device__ __forceinline__ void init(const Operand& o, int64_t first, int limit, int64_t K, int64_t rows, int wave, int lane) {
+  __device__ __forceinline__ void init(const Operand& o, int64_t first, int limit, int64_t K, int64_t rows, int wave,
+                                       int lane) {
     stride = o.stride * 2;
     const int n = static_cast<int>(min<int64_t>(limit, o.n - first));
     if constexpr (BY_K) {
@@ -178,7 +179,8 @@ struct Tile {
       for (int j = 0; j < COPIES; ++j) {
         const int at = (wave * COPIES + j) * 64 + lane, k = at / LINE, slot = at % LINE;
         const int piece = (((slot >> 1) ^ swap(k)) << 1) | (slot & 1);
-        from[j] = k * static_cast<int>(stride) + min(piece, cols / 16 - 1) * 16;         // columns past the end: the last ones
+        // columns past the end: the last ones
+        from[j] = k * static_cast<int>(stride) + min(piece, cols / 16 - 1) * 16;
       }
     } else {
       buf = buffer_of(static_cast<const char*>(o.p) + first * stride, (n - 1) * stride + K * 2);
@@ -218,7 +220,8 @@ struct Tile {
   }
   static __device__ __forceinline__ bf16x8 fragment(const char* __restrict__ tile, int at, int f, int half) {
     if constexpr (BY_K) {
-      const char* const p = tile + half * 32 * T * 2 + (at ^ (f * 32));     // a row of k is a power of two: the bits do not meet
+      // a row of k is a power of two: the bits do not meet
+      const char* const p = tile + half * 32 * T * 2 + (at ^ (f * 32));
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * T * 2));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -295,7 +298,8 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
 #pragma unroll
     for (int i = 0; i < FA; ++i)
 #pragma unroll
-      for (int j = 0; j < FB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.fa[i], f.fb[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < FB; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.fa[i], f.fb[j], acc[i][j], 0, 0, 0);
   };
 
   Frags f0, f1;
@@ -451,7 +455,8 @@ __device__ __forceinline__ bf16x8 fragment(const char* row, int i, int C) {
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (i + e < C) v[e / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(row + (i + e) * 2)) << (16 * (e & 1));
+      if (i + e < C)
+        v[e / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(row + (i + e) * 2)) << (16 * (e & 1));
   }
   return __builtin_bit_cast(bf16x8, v);
 }
@@ -493,7 +498,8 @@ __global__ __launch_bounds__(64, 2) void k_few(FewArgs a) {
       if (s0 + s < whole) {               // uniform
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-          step(__builtin_bit_cast(bf16x8, b.g[s]), __builtin_bit_cast(bf16x8, b.u[s]), j, __builtin_bit_cast(bf16x8, b.x[j][s]));
+          step(__builtin_bit_cast(bf16x8, b.g[s]), __builtin_bit_cast(bf16x8, b.u[s]), j,
+               __builtin_bit_cast(bf16x8, b.x[j][s]));
       }
   };
   if (whole > 0) {
@@ -596,8 +602,8 @@ __global__ __launch_bounds__(256) void k_pad(PadArgs a) {
 }
 
 // the same from codes
-__global__ __launch_bounds__(256) void k_unpack_pad(const int8_t* src, int64_t s_src, const int8_t* exps, int64_t R, int64_t C,
-                                                    int64_t Cp, void* dst) {
+__global__ __launch_bounds__(256) void k_unpack_pad(const int8_t* src, int64_t s_src, const int8_t* exps, int64_t R,
+                                                    int64_t C, int64_t Cp, void* dst) {
   const int64_t per = Cp / 8, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= R * per) return;
   const int64_t r = row_of(i, per);
@@ -616,8 +622,8 @@ __global__ __launch_bounds__(256) void k_unpack_pad(const int8_t* src, int64_t s
 }
 
 __global__ __launch_bounds__(256) void k_clear(uint16_t* p, int64_t n) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i < n) p[i] = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) p[i] = 0;
 }
 
 // ---------------------------------------------------------------- host side
@@ -633,7 +639,8 @@ int64_t room(int64_t bytes) { return up_to(bytes, 256); }
 
 // whether the copies of the matrix product can take rows of K elements as they lie
 bool direct(const void* p, int64_t stride, int64_t K) {
-  return K % 64 == 0 && stride % 8 == 0 && stride >= K && stride <= STRIDE_MAX && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+  return K % 64 == 0 && stride % 8 == 0 && stride >= K && stride <= STRIDE_MAX &&
+         (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
 // Tiles of 64 x 64, 128 x 128, 128 x 256 or 256 x 256 (A x B): large ones move
@@ -648,8 +655,8 @@ struct TileCost {
   int a, b, slots;
   double half, full, end;
 };
-constexpr TileCost TILES[4] = {{64, 64, 512, 0.30, 0.50, 1.0}, {128, 128, 256, 0.50, 0.55, 2.0}, {128, 256, 256, 0.82, 0.95, 4.0},
-                               {256, 256, 256, 1.3, 1.6, 8.0}};
+constexpr TileCost TILES[4] = {{64, 64, 512, 0.30, 0.50, 1.0}, {128, 128, 256, 0.50, 0.55, 2.0},
+                               {128, 256, 256, 0.82, 0.95, 4.0}, {256, 256, 256, 1.3, 1.6, 8.0}};
 double tile_time(const TileCost& t, int64_t na, int64_t nb, int64_t K) {
   const int64_t tiles = ceil_div(na, t.a) * ceil_div(nb, t.b), whole = tiles / t.slots, last = tiles % t.slots;
   const double stages = static_cast<double>(K) / 64.0, share = static_cast<double>(last) / t.slots;
@@ -706,8 +713,8 @@ void launch_tiles(MmArgs a, const Part& p, hipStream_t s) {
   a.begin_b = p.b0;
   a.tiles_a = ceil_div(p.a1 - p.a0, WA * FA * 16);
   a.tiles_b = ceil_div(p.b1 - p.b0, WB * FB * 16);
-  hipLaunchKernelGGL((k_mm<GATED, A_BY_K, B_BY_K, WA, WB, FA, FB, KS, BUFS, SPREAD>), dim3(static_cast<unsigned>(a.tiles_a * a.tiles_b)),
-                     dim3(64 * WA * WB), 0, s, a);
+  hipLaunchKernelGGL((k_mm<GATED, A_BY_K, B_BY_K, WA, WB, FA, FB, KS, BUFS, SPREAD>),
+                     dim3(static_cast<unsigned>(a.tiles_a * a.tiles_b)), dim3(64 * WA * WB), 0, s, a);
 }
 
 // By row 64 k to a stage (whole lines of memory), its reads before its MFMAs;
@@ -774,10 +781,15 @@ bool known_save(int save) { return save == DET_SAVE_NONE || save == DET_SAVE_HAL
 det_status check_sizes(int64_t N, int64_t C, int64_t F, int act, int save) {
   if (!known_act(act)) return fail(DET_EINVAL, "unknown activation %d", act);
   if (!known_save(save)) return fail(DET_EINVAL, "unknown kind of checkpoint %d", save);
-  if (N < 0 || C < 1 || F < 1) return fail(DET_EINVAL, "bad size: N=%lld C=%lld F=%lld", (long long)N, (long long)C, (long long)F);
+  if (N < 0 || C < 1 || F < 1)
+    return fail(DET_EINVAL, "bad size: N=%lld C=%lld F=%lld", (long long)N, (long long)C, (long long)F);
   if (N > DET_ROWS_MAX) return fail(DET_EINVAL, "N = %lld exceeds the limit 2^22 rows per call", (long long)N);
   if (C > DET_GATED_MAX || F > DET_GATED_MAX)
     return fail(DET_EINVAL, "C = %lld and F = %lld must not exceed 65536", (long long)C, (long long)F);
+  // a thread takes 8 elements where rows are copied, and a launch has fewer than 2^32
+  if (N * std::max(C, F) > int64_t{1} << 34)
+    return fail(DET_EINVAL, "more than 2^34 elements of x or h in one call: N=%lld C=%lld F=%lld", (long long)N,
+                (long long)C, (long long)F);
   return DET_OK;
 }
 det_status check_operand(const void* p, int64_t stride, const char* name) {
@@ -813,9 +825,11 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
   if ((st = check_operand(x, s_x, "x")) != DET_OK || (st = check_operand(w_gate, s_gate, "w_gate")) != DET_OK ||
       (st = check_operand(w_up, s_up, "w_up")) != DET_OK)
     return st;
-  if (h == nullptr || (save != DET_SAVE_NONE && (gate == nullptr || up == nullptr || gate_exp == nullptr || up_exp == nullptr)))
+  if (h == nullptr ||
+      (save != DET_SAVE_NONE && (gate == nullptr || up == nullptr || gate_exp == nullptr || up_exp == nullptr)))
     return fail(DET_EINVAL, "null output");
-  if (save != DET_SAVE_NONE && s_kept < F) return fail(DET_EINVAL, "rows of gate and up overlap: stride %lld", (long long)s_kept);
+  if (save != DET_SAVE_NONE && s_kept < F)
+    return fail(DET_EINVAL, "rows of gate and up overlap: stride %lld", (long long)s_kept);
   if (!aligned_for(h, h_dt) || (save == DET_SAVE_HALF && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
     return fail(DET_EINVAL, "outputs must be aligned to their element size");
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -849,7 +863,9 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
 
 int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, int need_dx, int need_dw, int aligned,
                                               int packed) {
-  if (N <= 0 || C <= 0 || F <= 0 || N > DET_ROWS_MAX || C > DET_GATED_MAX || F > DET_GATED_MAX || (!need_dx && !need_dw)) return 0;
+  if (N <= 0 || C <= 0 || F <= 0 || N > DET_ROWS_MAX || C > DET_GATED_MAX || F > DET_GATED_MAX ||
+      (!need_dx && !need_dw))
+    return 0;
   const int64_t Cp = up_to(C, 64);
   const bool as_is = C % 64 == 0 && aligned;
   return room(N * 2 * up_to(F, 64) * 2) + (need_dx && !as_is ? 2 * room(F * Cp * 2) : 0) +
@@ -865,25 +881,30 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
   if (!known_dtype(dh_dt)) return fail(DET_EDTYPE, "unknown dtype %d", dh_dt);
   det_status st = check_sizes(N, C, F, act, save);
   if (st != DET_OK) return st;
-  if (save == DET_SAVE_NONE) return fail(DET_EINVAL, "the gradient needs both projections: save them in the forward call");
+  if (save == DET_SAVE_NONE)
+    return fail(DET_EINVAL, "the gradient needs both projections: save them in the forward call");
   const bool need_dx = dx != nullptr, need_dw = dw_gate != nullptr || dw_up != nullptr;
-  if (need_dw && (dw_gate == nullptr || dw_up == nullptr)) return fail(DET_EINVAL, "dw_gate and dw_up are formed together");
+  if (need_dw && (dw_gate == nullptr || dw_up == nullptr))
+    return fail(DET_EINVAL, "dw_gate and dw_up are formed together");
   if (!aligned_for(dx, DET_BF16) || !aligned_for(dw_gate, DET_BF16) || !aligned_for(dw_up, DET_BF16))
     return fail(DET_EINVAL, "outputs must be aligned to their element size");
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (N == 0) {
     if (need_dw)
       for (void* p : {dw_gate, dw_up})
-        hipLaunchKernelGGL(k_clear, dim3(static_cast<unsigned>(ceil_div(F * C, 256))), dim3(256), 0, s, static_cast<uint16_t*>(p), F * C);
+        hipLaunchKernelGGL(k_clear, dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(F * C, 256), 1 << 16))),
+                           dim3(256), 0, s, static_cast<uint16_t*>(p), F * C);
     return need_dw ? hip_check(hipGetLastError(), "clearing launch") : DET_OK;
   }
   if (!need_dx && !need_dw) return DET_OK;
   if (dh == nullptr || gate == nullptr || up == nullptr || gate_exp == nullptr || up_exp == nullptr)
     return fail(DET_EINVAL, "null pointer");
   if (s_dh < 0 || s_kept < 0) return fail(DET_EINVAL, "negative stride");
-  if (!aligned_for(dh, dh_dt) || (save == DET_SAVE_HALF && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
+  if (!aligned_for(dh, dh_dt) ||
+      (save == DET_SAVE_HALF && (!aligned_for(gate, DET_BF16) || !aligned_for(up, DET_BF16))))
     return fail(DET_EINVAL, "operands must be aligned to their element size");
-  if (need_dx && ((st = check_operand(w_gate, s_gate, "w_gate")) != DET_OK || (st = check_operand(w_up, s_up, "w_up")) != DET_OK))
+  if (need_dx && ((st = check_operand(w_gate, s_gate, "w_gate")) != DET_OK ||
+                  (st = check_operand(w_up, s_up, "w_up")) != DET_OK))
     return st;
   if (need_dw) {
     if (x == nullptr || s_x < 0) return fail(DET_EINVAL, "null x or negative stride");
@@ -912,8 +933,8 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
     pads.copy(ups.p, ups.stride, F);
   }
   if (need_dw && codes) {
-    hipLaunchKernelGGL(k_unpack_pad, dim3(blocks_for(N * (Cp / 8))), dim3(256), 0, s, static_cast<const int8_t*>(x), s_x, x_exp, N,
-                       C, Cp, static_cast<void*>(pads.ws));
+    hipLaunchKernelGGL(k_unpack_pad, dim3(blocks_for(N * (Cp / 8))), dim3(256), 0, s, static_cast<const int8_t*>(x),
+                       s_x, x_exp, N, C, Cp, static_cast<void*>(pads.ws));
     xs = {pads.ws, Cp, C};
   } else if (need_dw && !direct(x, s_x, C)) {
     pads.copy(xs.p, xs.stride, N);

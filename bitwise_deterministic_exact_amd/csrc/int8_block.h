@@ -33,9 +33,12 @@ __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(st
 
 // the largest of 8 adjacent lanes
 __device__ __forceinline__ uint32_t top_of_8(uint32_t m) {
-  m = max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(m), 0xB1, 0xF, 0xF, false)));   // lane ^ 1
-  m = max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(m), 0x4E, 0xF, 0xF, false)));   // lane ^ 2
-  return max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(m), 0x141, 0xF, 0xF, false)));  // mirrored in 8
+  // lane ^ 1
+  m = max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(m), 0xB1, 0xF, 0xF, false)));
+  // lane ^ 2
+  m = max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(m), 0x4E, 0xF, 0xF, false)));
+  // mirrored in 8
+  return max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(m), 0x141, 0xF, 0xF, false)));
 }
 
 // four values as codes of the unit 1 / inv, in one word (bad: a block that is not finite)

@@ -141,7 +141,7 @@ det_status check_block_rows(int dt, int64_t s, int64_t N, int64_t C) {
   return DET_OK;
 }
 
-// one long row where there is no gap and no ragged block; false: too many for one launch
+// one long row where there is no gap and no ragged block; false: more threads than one launch takes (2^32)
 bool lay_out(PackArgs& a) {
   if (a.s_x == a.C && a.C % INT8_BLOCK == 0) {
     a.C *= a.N;
@@ -150,7 +150,7 @@ bool lay_out(PackArgs& a) {
   }
   a.per_row = ceil_div(a.C, INT8_BLOCK) * (INT8_BLOCK / PER);
   a.total = a.N * a.per_row;
-  return ceil_div(a.total, 256 * UNITS) < (int64_t{1} << 31);
+  return a.total <= int64_t{1} << 33;
 }
 
 }  // namespace
@@ -165,7 +165,7 @@ det_status det_int8_pack(det_dtype dt, const void* x, int64_t s_x, int64_t N, in
   if (!aligned_for(x, dt)) return fail(DET_EINVAL, "x must be aligned to its element size");
   PackArgs a{};
   a.x = x; a.s_x = s_x; a.N = N; a.C = C; a.codes = codes; a.exps = exps;
-  if (!lay_out(a)) return fail(DET_EINVAL, "more than 2^44 elements in one call");
+  if (!lay_out(a)) return fail(DET_EINVAL, "more than 2^36 elements in one call");
   a.status = det_device_status_word();
   if (a.status == nullptr) return DET_EHIP;
   const dim3 grid(static_cast<unsigned>(ceil_div(a.total, 256 * UNITS)));
@@ -183,7 +183,7 @@ det_status det_int8_unpack(const int8_t* codes, int64_t s_codes, const int8_t* e
   if (!aligned_for(y, dt)) return fail(DET_EINVAL, "y must be aligned to its element size");
   PackArgs a{};
   a.x = codes; a.s_x = s_codes; a.N = N; a.C = C; a.exps = const_cast<int8_t*>(exps); a.y = y;
-  if (!lay_out(a)) return fail(DET_EINVAL, "more than 2^44 elements in one call");
+  if (!lay_out(a)) return fail(DET_EINVAL, "more than 2^36 elements in one call");
   const dim3 grid(static_cast<unsigned>(ceil_div(a.total, 256 * UNITS)));
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dt == DET_F32) hipLaunchKernelGGL(k_int8_unpack<DET_F32>, grid, dim3(256), 0, s, a);

@@ -269,7 +269,8 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_policy_join(PolicyArgs a) {
     int64_t clipped = 0, count = 0;
     const int stride = serial ? 1 : 64;
     for (int64_t p0 = serial ? 0 : lane; p0 < a.pieces; p0 += AHEAD * stride) {
-      double2 v[AHEAD];                   // all in flight before the first is added; past the end: row b's first, not added
+      // all in flight before the first is added; past the end: row b's first, not added
+      double2 v[AHEAD];
       int2 n[AHEAD];
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
@@ -484,7 +485,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_preference(PreferenceArgs a) {
   double loss, slope;                     // slope: d loss / d (s_chosen - s_rejected)
   if (a.kind == DET_PREFER_SIGMOID) {
     const double e = exp(-fabs(z)), soft = log1p(e), small = e / (1.0 + e), large = 1.0 / (1.0 + e);
-    const double away = z > 0.0 ? soft : soft - z, toward = z > 0.0 ? soft + z : soft;     // -ln sigmoid(z), -ln sigmoid(-z)
+    // -ln sigmoid(z), -ln sigmoid(-z)
+    const double away = z > 0.0 ? soft : soft - z, toward = z > 0.0 ? soft + z : soft;
     loss = a.smooth == 0.0 ? away : (1.0 - a.smooth) * away + a.smooth * toward;
     slope = a.beta * (a.smooth - (z > 0.0 ? small : large));
     if (z != z) loss = slope = z;
@@ -529,7 +531,9 @@ constexpr int64_t T_MAX = int64_t{1} << 24;
 
 int64_t parts_of(int64_t T) { return ceil_div(T, PART); }
 int64_t pieces_of(int64_t T) { return T <= PART ? std::min<int64_t>(T, 1) : ceil_div(T, PIECE); }
-unsigned policy_blocks(int64_t B, int64_t T) { return static_cast<unsigned>(T <= PART ? ceil_div(B, 4) : B * pieces_of(T)); }
+unsigned policy_blocks(int64_t B, int64_t T) {
+  return static_cast<unsigned>(T <= PART ? ceil_div(B, 4) : B * pieces_of(T));
+}
 // workgroups that join rows: one up to 2^13 pieces of rows (up to 8 to a thread of its 1024)
 int groups_of(int64_t B, int64_t pieces) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, ceil_div(B * pieces, 1 << 13))));
@@ -553,7 +557,8 @@ det_status check_tokens(int64_t B, int64_t T, std::initializer_list<int64_t> str
   if (B < 0 || T < 0) return fail(DET_EINVAL, "bad size: %lld rows of %lld tokens", (long long)B, (long long)T);
   if (B > DET_ROWS_MAX || T > T_MAX) return fail(DET_EINVAL, "%lld rows of %lld tokens exceed the limits 2^22 and 2^24",
                                                  (long long)B, (long long)T);
-  if (B * T > int64_t{1} << 40) return fail(DET_EINVAL, "more than 2^40 tokens in one call");
+  // a launch has fewer than 2^32 threads
+  if (B * T > int64_t{1} << 32) return fail(DET_EINVAL, "more than 2^32 tokens in one call");
   for (int64_t s : strides)
     if (s < 0) return fail(DET_EINVAL, "negative stride");
   return DET_OK;
@@ -568,8 +573,10 @@ det_status check_policy(const PolicyArgs& a, double low, double high, double kl_
   if (a.adv_t != 0 && a.adv_t != 1) return fail(DET_EINVAL, "the advantage's tokens are adjacent (1) or one value (0)");
   if (a.reduction != DET_REDUCE_NONE && a.reduction != DET_REDUCE_TOKENS && a.reduction != DET_REDUCE_SEQUENCES)
     return fail(DET_EINVAL, "unknown reduction %d", a.reduction);
-  if (kl_weight > 0.0 && a.ref == nullptr && a.B * a.T > 0) return fail(DET_EINVAL, "a KL term needs the reference's log probabilities");
-  if (a.B * a.T > 0 && (a.lp == nullptr || a.old == nullptr || a.adv == nullptr)) return fail(DET_EINVAL, "null pointer");
+  if (kl_weight > 0.0 && a.ref == nullptr && a.B * a.T > 0)
+    return fail(DET_EINVAL, "a KL term needs the reference's log probabilities");
+  if (a.B * a.T > 0 && (a.lp == nullptr || a.old == nullptr || a.adv == nullptr))
+    return fail(DET_EINVAL, "null pointer");
   if (!aligned4(a.lp) || !aligned4(a.old) || !aligned4(a.adv) || !aligned4(a.ref))
     return fail(DET_EINVAL, "operands must be aligned to their element size");
   return DET_OK;
@@ -612,11 +619,13 @@ det_status det_policy_loss(const float* logprob, int64_t s_logprob, const float*
   if (st != DET_OK) return st;
   const bool none = reduction == DET_REDUCE_NONE;
   if (none && B * T == 0) return DET_OK;
-  if (loss == nullptr || kl == nullptr || clipped == nullptr || (!none && count == nullptr)) return fail(DET_EINVAL, "null output");
+  if (loss == nullptr || kl == nullptr || clipped == nullptr || (!none && count == nullptr))
+    return fail(DET_EINVAL, "null output");
   if (!aligned4(loss) || !aligned4(kl) || !aligned4(clipped) || !aligned8(count))
     return fail(DET_EINVAL, "outputs must be aligned to their element size");
   const int64_t need = det_policy_loss_workspace_bytes(B, T, reduction);
-  if (need > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < static_cast<size_t>(need)))
+  if (need > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) ||
+                   workspace_bytes < static_cast<size_t>(need)))
     return fail(DET_EINVAL, "workspace: %lld bytes, 16-byte aligned, are needed", (long long)need);
   a.loss = loss; a.kl = kl; a.clipped = clipped; a.count = count;
   a.status = det_device_status_word();
@@ -651,8 +660,10 @@ det_status det_policy_loss_grad(const float* logprob, int64_t s_logprob, const f
   if (st != DET_OK) return st;
   if (s_g < 0 || s_g_t < 0) return fail(DET_EINVAL, "negative stride");
   if (B * T == 0) return DET_OK;
-  if (g == nullptr || dlogprob == nullptr || (reduction != DET_REDUCE_NONE && count == nullptr)) return fail(DET_EINVAL, "null pointer");
-  if (!aligned4(g) || !aligned4(dlogprob) || !aligned8(count)) return fail(DET_EINVAL, "operands must be aligned to their element size");
+  if (g == nullptr || dlogprob == nullptr || (reduction != DET_REDUCE_NONE && count == nullptr))
+    return fail(DET_EINVAL, "null pointer");
+  if (!aligned4(g) || !aligned4(dlogprob) || !aligned8(count))
+    return fail(DET_EINVAL, "operands must be aligned to their element size");
   a.count = const_cast<int64_t*>(count);
   a.g = g; a.s_g = s_g; a.s_g_t = s_g_t; a.dlp = dlogprob;
   hipLaunchKernelGGL(k_policy_grad, dim3(policy_blocks(B, T)), dim3(256), 0,
@@ -667,12 +678,14 @@ det_status det_preference_loss(const float* chosen, int64_t s_chosen, const floa
                                int64_t T_rejected, int64_t P, det_preference kind, double beta, double margin,
                                double label_smoothing, int by_length, float* loss, float* chosen_reward,
                                float* rejected_reward, float* slope, void* stream) {
-  det_status st = check_tokens(P, std::max(T_chosen, T_rejected), {s_chosen, s_ref_chosen, s_chosen_mask, s_rejected, s_ref_rejected, s_rejected_mask});
+  det_status st = check_tokens(P, std::max(T_chosen, T_rejected),
+                               {s_chosen, s_ref_chosen, s_chosen_mask, s_rejected, s_ref_rejected, s_rejected_mask});
   if (st != DET_OK) return st;
   if (T_chosen < 0 || T_rejected < 0) return fail(DET_EINVAL, "negative length");
   if (!known_kind(kind)) return fail(DET_EINVAL, "unknown kind of preference loss %d", kind);
   if (!(beta > 0.0) || !(beta < 1e6)) return fail(DET_EINVAL, "beta must lie in (0, 1e6)");
-  if (!(fabs(margin) < 1e6) || (margin != 0.0 && kind == DET_PREFER_IPO)) return fail(DET_EINVAL, "margin must be finite, and 0 for ipo");
+  if (!(fabs(margin) < 1e6) || (margin != 0.0 && kind == DET_PREFER_IPO))
+    return fail(DET_EINVAL, "margin must be finite, and 0 for ipo");
   if (!(label_smoothing >= 0.0) || !(label_smoothing <= 0.5) || (label_smoothing != 0.0 && kind != DET_PREFER_SIGMOID))
     return fail(DET_EINVAL, "label_smoothing must lie in [0, 0.5], and be 0 unless sigmoid");
   if ((ref_chosen == nullptr) != (ref_rejected == nullptr) && T_chosen > 0 && T_rejected > 0)
@@ -681,20 +694,24 @@ det_status det_preference_loss(const float* chosen, int64_t s_chosen, const floa
   if ((T_chosen > 0 && chosen == nullptr) || (T_rejected > 0 && rejected == nullptr) || loss == nullptr ||
       chosen_reward == nullptr || rejected_reward == nullptr || slope == nullptr)
     return fail(DET_EINVAL, "null pointer");
-  for (const void* p : {static_cast<const void*>(chosen), static_cast<const void*>(rejected), static_cast<const void*>(ref_chosen),
-                        static_cast<const void*>(ref_rejected), static_cast<const void*>(loss), static_cast<const void*>(chosen_reward),
+  for (const void* p : {static_cast<const void*>(chosen), static_cast<const void*>(rejected),
+                        static_cast<const void*>(ref_chosen), static_cast<const void*>(ref_rejected),
+                        static_cast<const void*>(loss), static_cast<const void*>(chosen_reward),
                         static_cast<const void*>(rejected_reward), static_cast<const void*>(slope)})
     if (!aligned4(p)) return fail(DET_EINVAL, "operands must be aligned to their element size");
   PreferenceArgs a{};
-  a.side[0] = {chosen, s_chosen, ref_chosen, s_ref_chosen, chosen_mask, s_chosen_mask, T_chosen, chosen_reward, nullptr};
-  a.side[1] = {rejected, s_rejected, ref_rejected, s_ref_rejected, rejected_mask, s_rejected_mask, T_rejected, rejected_reward, nullptr};
+  a.side[0] = {chosen, s_chosen, ref_chosen, s_ref_chosen, chosen_mask, s_chosen_mask, T_chosen, chosen_reward,
+               nullptr};
+  a.side[1] = {rejected, s_rejected, ref_rejected, s_ref_rejected, rejected_mask, s_rejected_mask, T_rejected,
+               rejected_reward, nullptr};
   a.P = P; a.beta = beta; a.margin = margin; a.smooth = label_smoothing; a.kind = kind; a.by_length = by_length != 0;
   a.loss = loss; a.slope = slope;
   a.status = det_device_status_word();
   if (a.status == nullptr) return DET_EHIP;
   hipStream_t s = static_cast<hipStream_t>(stream);
   // the lengths alone decide, for the sums' order follows
-  if (std::max(T_chosen, T_rejected) <= 4 * PART) hipLaunchKernelGGL(k_preference<4>, dim3(static_cast<unsigned>(P)), dim3(256), 0, s, a);
+  if (std::max(T_chosen, T_rejected) <= 4 * PART)
+    hipLaunchKernelGGL(k_preference<4>, dim3(static_cast<unsigned>(P)), dim3(256), 0, s, a);
   else hipLaunchKernelGGL(k_preference<16>, dim3(static_cast<unsigned>(P)), dim3(1024), 0, s, a);
   return hip_check(hipGetLastError(), "preference loss launch");
 }
@@ -707,7 +724,8 @@ det_status det_preference_loss_grad(const uint8_t* chosen_mask, int64_t s_chosen
   if (st != DET_OK) return st;
   if (T_chosen < 0 || T_rejected < 0) return fail(DET_EINVAL, "negative length");
   // a side whose gradient is not needed has no parts
-  const int64_t parts0 = dchosen == nullptr ? 0 : parts_of(T_chosen), parts1 = drejected == nullptr ? 0 : parts_of(T_rejected);
+  const int64_t parts0 = dchosen == nullptr ? 0 : parts_of(T_chosen);
+  const int64_t parts1 = drejected == nullptr ? 0 : parts_of(T_rejected);
   if (P * (parts0 + parts1) == 0) return DET_OK;
   if (slope == nullptr || g == nullptr) return fail(DET_EINVAL, "null pointer");
   if (!aligned4(slope) || !aligned4(g) || !aligned4(dchosen) || !aligned4(drejected))

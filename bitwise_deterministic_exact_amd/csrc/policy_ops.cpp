@@ -56,14 +56,16 @@ PolicyRows policy_rows(const Tensor& lp, const Tensor& old, const Tensor& adv, c
   if (lp.scalar_type() != at::kFloat || lp.dim() < 1)
     refuse(what, ": logprob must be float32 [..., T] (got ", lp.scalar_type(), " ", lp.sizes(), ")");
   check_logprob(old, lp.sizes(), lp, "old_logprob", what);
-  if (adv.sizes() != lp.sizes()) check_logprob(adv, lead_of(lp), lp, "advantage (one to a row, or one to a token)", what);
+  if (adv.sizes() != lp.sizes())
+    check_logprob(adv, lead_of(lp), lp, "advantage (one to a row, or one to a token)", what);
   else check_logprob(adv, lp.sizes(), lp, "advantage", what);
   if (ref) check_logprob(*ref, lp.sizes(), lp, "ref_logprob", what);
   else if (o.kl_weight != 0.0) refuse(what, ": a KL term needs ref_logprob");
   check_mask(mask, lp.sizes(), lp, "mask", what);
   if (!(o.low >= 0.0) || !(o.low <= 1.0)) refuse(what, ": clip_low must lie in [0, 1] (got ", o.low, ")");
   if (!(o.high >= 0.0) || !(o.high < 1e6)) refuse(what, ": clip_high must lie in [0, 1e6) (got ", o.high, ")");
-  if (!(o.kl_weight >= 0.0) || !(o.kl_weight < 1e6)) refuse(what, ": kl_weight must lie in [0, 1e6) (got ", o.kl_weight, ")");
+  if (!(o.kl_weight >= 0.0) || !(o.kl_weight < 1e6))
+    refuse(what, ": kl_weight must lie in [0, 1e6) (got ", o.kl_weight, ")");
   on_gpu(lp, what, "logprob");
   PolicyRows r;
   r.lp = token_rows(lp);
@@ -93,9 +95,9 @@ Policy policy_forward(const Tensor& lp, const Tensor& old, const Tensor& adv, co
   if (!none) p.count = at::empty({r.B + 1}, lp.options().dtype(at::kLong));
   const int64_t bytes = det_policy_loss_workspace_bytes(r.B, r.T, o.reduction);
   const Tensor ws = bytes > 0 ? at::empty({bytes}, lp.options().dtype(at::kByte)) : Tensor();
-  ok(det_policy_loss(ptr<float>(r.lp), r.lp.stride(0), ptr<float>(r.old), r.old.stride(0), ptr<float>(r.adv), r.adv.stride(0),
-                     r.adv_t, ptr<uint8_t>(r.mask), stride_of(r.mask), ptr<float>(r.ref), stride_of(r.ref), r.B, r.T, o.low,
-                     o.high, o.kl_weight, o.reduction, out<float>(p.loss), out<float>(p.kl), out<float>(p.clipped),
+  ok(det_policy_loss(ptr<float>(r.lp), r.lp.stride(0), ptr<float>(r.old), r.old.stride(0), ptr<float>(r.adv),
+                     r.adv.stride(0), r.adv_t, ptr<uint8_t>(r.mask), stride_of(r.mask), ptr<float>(r.ref),
+                     stride_of(r.ref), r.B, r.T, o.low, o.high, o.kl_weight, o.reduction, out<float>(p.loss), out<float>(p.kl), out<float>(p.clipped),
                      out<int64_t>(p.count), out<void>(ws), static_cast<size_t>(bytes), stream_of(lp)));
   return p;
 }
@@ -196,8 +198,10 @@ Preference preference_forward(const Tensor& chosen, const Tensor& rejected, cons
     if (t->scalar_type() != at::kFloat || t->dim() < 1)
       refuse(what, ": ", name, " must be float32 [..., T] (got ", t->scalar_type(), " ", t->sizes(), ")");
   if (lead_of(chosen) != lead_of(rejected) || chosen.device() != rejected.device())
-    refuse(what, ": both sides must have one leading shape, on one device (got ", chosen.sizes(), " and ", rejected.sizes(), ")");
-  if (ref_chosen.has_value() != ref_rejected.has_value()) refuse(what, ": reference log probabilities are given for both sides or for none");
+    refuse(what, ": both sides must have one leading shape, on one device (got ", chosen.sizes(), " and ",
+           rejected.sizes(), ")");
+  if (ref_chosen.has_value() != ref_rejected.has_value())
+    refuse(what, ": reference log probabilities are given for both sides or for none");
   if (ref_chosen) {
     check_logprob(*ref_chosen, chosen.sizes(), chosen, "ref_chosen_logprob", what);
     check_logprob(*ref_rejected, rejected.sizes(), chosen, "ref_rejected_logprob", what);
@@ -207,7 +211,8 @@ Preference preference_forward(const Tensor& chosen, const Tensor& rejected, cons
   if (!(o.beta > 0.0) || !(o.beta < 1e6)) refuse(what, ": beta must lie in (0, 1e6) (got ", o.beta, ")");
   if (!(std::abs(o.margin) < 1e6)) refuse(what, ": margin must be finite (got ", o.margin, ")");
   if (o.margin != 0.0 && o.kind == DET_PREFER_IPO) refuse(what, ": ipo takes no margin");
-  if (!(o.smooth >= 0.0) || !(o.smooth <= 0.5)) refuse(what, ": label_smoothing must lie in [0, 0.5] (got ", o.smooth, ")");
+  if (!(o.smooth >= 0.0) || !(o.smooth <= 0.5))
+    refuse(what, ": label_smoothing must lie in [0, 0.5] (got ", o.smooth, ")");
   if (o.smooth != 0.0 && o.kind != DET_PREFER_SIGMOID) refuse(what, ": label_smoothing is the sigmoid loss's");
   on_gpu(chosen, what, "chosen_logprob");
   const c10::DeviceGuard guard(chosen.device());
@@ -217,9 +222,9 @@ Preference preference_forward(const Tensor& chosen, const Tensor& rejected, cons
   const at::IntArrayRef lead = lead_of(chosen);
   Preference p{at::empty(lead, chosen.options()), at::empty(lead, chosen.options()), at::empty(lead, chosen.options()),
                at::empty({P, 2}, chosen.options())};
-  ok(det_preference_loss(ptr<float>(c), c.stride(0), ptr<float>(rc), stride_of(rc), ptr<uint8_t>(mc), stride_of(mc), c.size(1),
-                         ptr<float>(r), r.stride(0), ptr<float>(rr), stride_of(rr), ptr<uint8_t>(mr), stride_of(mr), r.size(1),
-                         P, o.kind, o.beta, o.margin, o.smooth, o.by_length, out<float>(p.loss), out<float>(p.chosen),
+  ok(det_preference_loss(ptr<float>(c), c.stride(0), ptr<float>(rc), stride_of(rc), ptr<uint8_t>(mc), stride_of(mc),
+                         c.size(1), ptr<float>(r), r.stride(0), ptr<float>(rr), stride_of(rr), ptr<uint8_t>(mr),
+                         stride_of(mr), r.size(1), P, o.kind, o.beta, o.margin, o.smooth, o.by_length, out<float>(p.loss), out<float>(p.chosen),
                          out<float>(p.rejected), out<float>(p.slope), stream_of(chosen)));
   return p;
 }
@@ -229,7 +234,8 @@ std::tuple<Tensor, Tensor> preference_backward(const Tensor& g, const Tensor& sl
                                                const OptTensor& mask_rejected, bool need_chosen, bool need_rejected) {
   const char* const what = "preference_loss_backward";
   not_traced(what);
-  if (chosen.empty() || rejected.empty() || chosen.slice(0, chosen.size() - 1) != rejected.slice(0, rejected.size() - 1))
+  if (chosen.empty() || rejected.empty() ||
+      chosen.slice(0, chosen.size() - 1) != rejected.slice(0, rejected.size() - 1))
     refuse(what, ": both sides must have one leading shape");
   const at::IntArrayRef lead = chosen.slice(0, chosen.size() - 1);
   const int64_t P = c10::multiply_integers(lead);
@@ -245,9 +251,9 @@ std::tuple<Tensor, Tensor> preference_backward(const Tensor& g, const Tensor& sl
   if (need_rejected) dr = at::empty(rejected, slope.options());
   const Tensor s = slope.contiguous(), mc = token_rows(mask_chosen), mr = token_rows(mask_rejected);
   const Tensor g1 = g.reshape({P});
-  ok(det_preference_loss_grad(ptr<uint8_t>(mc), stride_of(mc), chosen.back(), ptr<uint8_t>(mr), stride_of(mr), rejected.back(),
-                              P, ptr<float>(s), ptr<float>(g1), g1.stride(0), out<float>(dc), out<float>(dr),
-                              stream_of(slope)));
+  ok(det_preference_loss_grad(ptr<uint8_t>(mc), stride_of(mc), chosen.back(), ptr<uint8_t>(mr), stride_of(mr),
+                              rejected.back(), P, ptr<float>(s), ptr<float>(g1), g1.stride(0), out<float>(dc),
+                              out<float>(dr), stream_of(slope)));
   return {dc, dr};
 }
 
@@ -259,7 +265,8 @@ struct PreferenceFn : torch::autograd::Function<PreferenceFn> {
     const Preference p = preference_forward(chosen, rejected, ref_chosen, ref_rejected, mask_chosen, mask_rejected,
                                             {static_cast<det_preference>(kind), beta, margin, smooth, by_length});
     // the slopes are what the gradient needs; the log probabilities stand for the shapes and the graph
-    ctx->save_for_backward({chosen, rejected, p.slope, mask_chosen.value_or(Tensor()), mask_rejected.value_or(Tensor())});
+    ctx->save_for_backward({chosen, rejected, p.slope, mask_chosen.value_or(Tensor()),
+                            mask_rejected.value_or(Tensor())});
     ctx->set_materialize_grads(false);
     ctx->mark_non_differentiable({p.chosen, p.rejected});
     return {p.loss, p.chosen, p.rejected};
@@ -284,11 +291,13 @@ std::tuple<Tensor, Tensor, Tensor> preference_loss(const Tensor& chosen, const T
                                                    const OptTensor& mask_chosen, const OptTensor& mask_rejected,
                                                    const std::string& kind, double beta, double margin, double smooth,
                                                    bool by_length) {
-  for (const OptTensor& t : {OptTensor(chosen), OptTensor(rejected), ref_chosen, ref_rejected}) no_tangent(t, "preference_loss");
+  for (const OptTensor& t : {OptTensor(chosen), OptTensor(rejected), ref_chosen, ref_rejected})
+    no_tangent(t, "preference_loss");
   const det_preference k = kind_of(kind, "preference_loss");
   if (at::GradMode::is_enabled() && (wants_grad(chosen) || wants_grad(rejected))) {
-    const variable_list v = PreferenceFn::apply(chosen, rejected, constant(ref_chosen), constant(ref_rejected), mask_chosen,
-                                                mask_rejected, static_cast<int64_t>(k), beta, margin, smooth, by_length);
+    const variable_list v = PreferenceFn::apply(chosen, rejected, constant(ref_chosen), constant(ref_rejected),
+                                                mask_chosen, mask_rejected, static_cast<int64_t>(k), beta, margin, smooth,
+                                                by_length);
     return {v[0], v[1], v[2]};
   }
   const Preference p = preference_forward(chosen, rejected, ref_chosen, ref_rejected, mask_chosen, mask_rejected,
@@ -309,13 +318,15 @@ void bind_policy(py::module_& m) {
   m.def("policy_loss_backward", [](const Tensor& g, const Tensor& lp, const Tensor& old, const Tensor& adv,
                                    const OptTensor& mask, const OptTensor& ref, const OptTensor& count, double low,
                                    double high, double kl_weight, const std::string& red) {
-    return policy_backward(g, lp, old, adv, mask, ref, count, {low, high, kl_weight, reduction_of(red, "policy_loss_backward")});
+    return policy_backward(g, lp, old, adv, mask, ref, count,
+                           {low, high, kl_weight, reduction_of(red, "policy_loss_backward")});
   }, release());
   m.def("preference_loss", &preference_loss, release());
   m.def("preference_loss_forward", [](const Tensor& c, const Tensor& r, const OptTensor& rc, const OptTensor& rr,
                                       const OptTensor& mc, const OptTensor& mr, const std::string& kind, double beta,
                                       double margin, double smooth, bool by_length) {
-    const Preference p = preference_forward(c, r, rc, rr, mc, mr, {kind_of(kind, "preference_loss"), beta, margin, smooth, by_length});
+    const Preference p = preference_forward(c, r, rc, rr, mc, mr,
+                                            {kind_of(kind, "preference_loss"), beta, margin, smooth, by_length});
     return std::make_tuple(p.loss, p.chosen, p.rejected, p.slope);
   }, release());
   m.def("preference_loss_backward", [](const Tensor& g, const Tensor& slope, const std::vector<int64_t>& chosen,

@@ -568,16 +568,16 @@ typedef enum { DET_SAVE_NONE = 0, DET_SAVE_HALF = 1, DET_SAVE_INT8 = 2 } det_sav
  *                     0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
  *   h                 [N][F] contiguous of type h_dt
  *   save              what gate and up ([N] rows of F, s_kept >= F apart; a
- *                     multiple of 4 is faster) get: nothing (null pointers), or g and u as fp16 elements or int8 codes, whose
- *                     blocks' exponents go to gate_exp and up_exp
- *                     [N][ceil(F / 32)]
+ *                     multiple of 4 is faster) get: nothing (null pointers), or
+ *                     g and u as fp16 elements or int8 codes, whose blocks'
+ *                     exponents go to gate_exp and up_exp [N][ceil(F / 32)]
  *   workspace         det_gated_linear_workspace_bytes(N, C, F, save, aligned),
  *                     256-byte aligned; `aligned`: x and both weights start at
  *                     multiples of 16 bytes and their strides are multiples of
  *                     8 in [C, 2^21]
  * g and u are fp32 sums over k in one fixed order (matrix-core products of 32 k
  * each, ascending), h is rounded once; values that are not finite take part as
- * IEEE arithmetic has it.  N <= 2^22, C and F <= 65536.
+ * IEEE arithmetic has it.  N <= 2^22, C and F <= 65536, N C and N F <= 2^34.
  * Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
  */
 int64_t det_gated_linear_workspace_bytes(int64_t N, int64_t C, int64_t F, det_save save, int aligned);
@@ -612,8 +612,9 @@ int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, i
 det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, const void* x, int64_t s_x,
                                  const int8_t* x_exp, const void* w_gate, int64_t s_gate, const void* w_up,
                                  int64_t s_up, det_save save, const void* gate, const void* up, int64_t s_kept,
-                                 const int8_t* gate_exp, const int8_t* up_exp, int64_t N, int64_t C, int64_t F, det_activation act, void* dx,
-                                 void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes, void* stream);
+                                 const int8_t* gate_exp, const int8_t* up_exp, int64_t N, int64_t C, int64_t F,
+                                 det_activation act, void* dx, void* dw_gate, void* dw_up, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 /*
  * det_int8_pack -- rows in 8 bits: 32 consecutive elements of a row (the last
@@ -628,7 +629,8 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
  * det_int8_unpack -- y = code 2^e, exact in fp32 and in bf16; NaN throughout a
  * block of exponent DET_INT8_NAN.
  *   codes             [N] rows of C, s_codes apart; y [N][C] of type dt
- * N <= 2^31, C <= 2^24.  Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
+ * N <= 2^31, C <= 2^24, at most 2^36 elements with each row's last block counted
+ * whole.  Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
  */
 det_status det_int8_pack(det_dtype dt, const void* x, int64_t s_x, int64_t N, int64_t C, int8_t* codes, int8_t* exps,
                          void* stream);
@@ -666,7 +668,7 @@ typedef enum { DET_PREFER_SIGMOID = 0, DET_PREFER_HINGE = 1, DET_PREFER_IPO = 2 
  * and rounded once, then divided: the results do not depend on the order of the
  * rows.  A token that counts and whose l is not finite is noted in the
  * device status ("non-finite"); the sums follow IEEE arithmetic (NaN, or both
- * infinities: NaN).  B <= 2^22, T <= 2^24, B T <= 2^40.
+ * infinities: NaN).  B <= 2^22, T <= 2^24, B T <= 2^32.
  * Returns DET_OK, DET_EINVAL or DET_EHIP.
  */
 int64_t det_policy_loss_workspace_bytes(int64_t B, int64_t T, det_reduction reduction);
@@ -710,7 +712,7 @@ det_status det_policy_loss_grad(const float* logprob, int64_t s_logprob, const f
  *                     loss in each token that counts of its two sides
  * Sums and the loss are formed in 64 bits, in an order that the two lengths
  * alone decide.  A loss that is not finite is noted in the device status
- * ("non-finite").  P <= 2^22, lengths <= 2^24, P times a length <= 2^40.
+ * ("non-finite").  P <= 2^22, lengths <= 2^24, P times a length <= 2^32.
  * Returns DET_OK, DET_EINVAL or DET_EHIP.
  */
 det_status det_preference_loss(const float* chosen, int64_t s_chosen, const float* ref_chosen, int64_t s_ref_chosen,

@@ -72,6 +72,15 @@ def test_c_entry_points_refuse(call, want):
     assert _lib.last_error()
 
 
+def test_what_no_launch_could_hold_is_refused():
+    for call in (lambda: _gated(N=1 << 22, F=4097), lambda: _gated(N=1 << 22, C=4160, s_x=4160, s_g=4160, s_u=4160),
+                 lambda: _grad(N=1 << 22, F=4097, s_dh=4097, s_k=4128), lambda: _pack(N=(1 << 31) - 1, C=33, s=33),
+                 lambda: _unpack(N=1 << 24, C=(1 << 12) + 1, s=4097), lambda: _policy(Bn=1 << 22, T=1025),
+                 lambda: _policy_grad(Bn=1 << 12, T=(1 << 20) + 1), lambda: _prefer(Pn=1 << 22, Tr=1025),
+                 lambda: _prefer_grad(Pn=1 << 22, Tc=1025)):
+        assert call() == EINVAL and "in one call" in _lib.last_error()
+
+
 def test_empty_problems_are_no_ops():
     assert _gated(N=0, x=NULL, h=NULL) == _lib.DET_OK
     assert _grad(N=0, dwg=None, dwu=None) == _lib.DET_OK

@@ -239,6 +239,20 @@ def test_layouts(N, C):
     assert torch.equal(gx.reshape(N, C), det.gated_linear_backward(torch.ones_like(h), x, wg, wu, s, need_dw=False)[0])
 
 
+def test_one_feature_of_wider_weights():
+    """Weights of one row each, whose strides are whatever their slices left."""
+    x, wg, wu = operands(18, 70, 64, 8)
+    ones = wg[::8], wu[:1]
+    assert ones[0].stride(0) != ones[1].stride(0) and all(w.is_contiguous() for w in ones)
+    h, s = det.gated_linear_forward(x, *ones)
+    want_h, want_s = det.gated_linear_forward(x, wg[:1].clone(), wu[:1].clone())
+    dh = torch.ones_like(h)
+    assert torch.equal(h, want_h)
+    for a, b in zip(det.gated_linear_backward(dh, x, *ones, s),
+                    det.gated_linear_backward(dh, x, wg[:1].clone(), wu[:1].clone(), want_s)):
+        assert torch.equal(a, b)
+
+
 def test_no_rows():
     x, wg, wu = operands(11, 4, 40, 24)
     x = x[:0].requires_grad_(True)
