@@ -149,6 +149,7 @@ using lds_s16x4 = __attribute__((address_space(3))) s16x4;
 // fragments of 16.
 template <bool BY_K, int T, int NW, int KS>
 struct Tile {
+  static_assert(T * KS % (512 * NW) == 0, "every wave copies as much");
   static constexpr int COPIES = T * KS / 512 / NW;            // of 1 KiB, per wave and stage
   static constexpr int BYTES = T * KS * 2;
   static constexpr int ROWS = 512 / KS, PIECES = KS / 8;      // by row: rows of a copy, pieces of 16 bytes in one
@@ -643,34 +644,46 @@ bool direct(const void* p, int64_t stride, int64_t K) {
          (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-// Tiles of 64 x 64, 128 x 128, 128 x 256 or 256 x 256 (A x B): large ones move
+// Tiles of 64 x 64, 128 x 128, 128 x 256 or 256 x 256 (A x B; dx: or 128 x 64): large ones move
 // fewer bytes per product, small ones fill the chip.  The rule takes the least of
 // what each would take, rounds (stages t + end), from what was measured (us per
 // stage of 64 k where up to half the CUs have a tile and where all have, a last
 // round in between, and for a tile's end; 64 x 64 fits twice on a CU).  4096
 // features of gate and up together, k 4096, by tokens: 256: 17 us (28, 52, 87 for
 // the larger tiles), 512: 28 28 52 87, 1024: 53 35 52 88, 2048: 103 69 65 89,
-// 4096: 202 135 124 106.  The result's bits are the same for all.
+// 4096: 202 135 124 106.  dx, whose A takes twice the LDS reads, is slower where
+// two small tiles share a CU, and has 128 x 64 for what is too little for 128 x
+// 128: 512 x 4096 x 4096 54 us, 63 with 64 x 64; 1100 x 1024 x 2816 40, 47; 1000 x
+// 1024 x 1024 20, 18.  The result's bits are the same for all.
 struct TileCost {
   int a, b, slots;
-  double half, full, end;
+  double half, more, full, end;           // `more`: just past half
 };
-constexpr TileCost TILES[4] = {{64, 64, 512, 0.30, 0.50, 1.0}, {128, 128, 256, 0.50, 0.55, 2.0},
-                               {128, 256, 256, 0.82, 0.95, 4.0}, {256, 256, 256, 1.3, 1.6, 8.0}};
+constexpr TileCost TILES[4] = {{64, 64, 512, 0.30, 0.30, 0.50, 1.0},
+                               {128, 128, 256, 0.50, 0.50, 0.55, 2.0},
+                               {128, 256, 256, 0.82, 0.82, 0.95, 4.0},
+                               {256, 256, 256, 1.3, 1.3, 1.6, 8.0}};
+constexpr TileCost DX_TILES[5] = {{64, 64, 512, 0.30, 0.42, 0.50, 1.0},
+                                  TILES[1], TILES[2], TILES[3],
+                                  {128, 64, 256, 0.36, 0.36, 0.41, 2.0}};
+struct Tiles {
+  const TileCost* of;
+  int n;
+};
 double tile_time(const TileCost& t, int64_t na, int64_t nb, int64_t K) {
   const int64_t tiles = ceil_div(na, t.a) * ceil_div(nb, t.b), whole = tiles / t.slots, last = tiles % t.slots;
   const double stages = static_cast<double>(K) / 64.0, share = static_cast<double>(last) / t.slots;
-  const double partly = t.half + (t.full - t.half) * std::max(0.0, 2.0 * share - 1.0);
+  const double partly = share <= 0.5 ? t.half : t.more + (t.full - t.more) * (2.0 * share - 1.0);
   return static_cast<double>(whole) * (stages * t.full + t.end) + (last > 0 ? stages * partly + t.end : 0.0);
 }
 struct Part {
   int tile;
   int64_t a0, a1, b0, b1;                 // of A (gated: of both halves together) and B
 };
-double best_tile(int64_t a0, int64_t a1, int64_t b0, int64_t b1, int64_t K, Part& p) {
+double best_tile(const Tiles& tiles, int64_t a0, int64_t a1, int64_t b0, int64_t b1, int64_t K, Part& p) {
   double least = 0.0;
-  for (int i = 0; i < 4; ++i) {
-    const double time = tile_time(TILES[i], a1 - a0, b1 - b0, K);
+  for (int i = 0; i < tiles.n; ++i) {
+    const double time = tile_time(tiles.of[i], a1 - a0, b1 - b0, K);
     if (i == 0 || time < least) {
       p = {i, a0, a1, b0, b1};
       least = time;
@@ -683,18 +696,19 @@ double best_tile(int64_t a0, int64_t a1, int64_t b0, int64_t b1, int64_t K, Part
 // 5000 forward 547 -> 483 us, dw of 8000 x 1000 x 10000 512 -> 429, of 1030 x 1024
 // x 4100, where the estimate misses, 42 -> 45.
 constexpr double LAUNCH = 4.0;            // us
-int plan(int64_t na, int64_t nb, int64_t K, Part (&parts)[2]) {
-  double least = best_tile(0, na, 0, nb, K, parts[0]);
+int plan(const Tiles& tiles, int64_t na, int64_t nb, int64_t K, Part (&parts)[2]) {
+  double least = best_tile(tiles, 0, na, 0, nb, K, parts[0]);
   int n = 1;
-  for (int i = 0; i < 4; ++i) {
-    const TileCost& t = TILES[i];
+  for (int i = 0; i < tiles.n; ++i) {
+    const TileCost& t = tiles.of[i];
     const int64_t ta = ceil_div(na, t.a), tb = ceil_div(nb, t.b), whole = ta * tb / t.slots * t.slots;
     for (int by_b = 0; by_b < 2; ++by_b) {
       const int64_t cut = whole / (by_b ? ta : tb);           // columns (rows) of tiles in whole rounds
       if (cut < 1 || cut >= (by_b ? tb : ta)) continue;
       const int64_t a1 = by_b ? na : cut * t.a, b1 = by_b ? cut * t.b : nb;
       Part rest{};
-      const double time = LAUNCH + tile_time(t, a1, b1, K) + best_tile(by_b ? 0 : a1, na, by_b ? b1 : 0, nb, K, rest);
+      const double time =
+          LAUNCH + tile_time(t, a1, b1, K) + best_tile(tiles, by_b ? 0 : a1, na, by_b ? b1 : 0, nb, K, rest);
       if (time < least) {
         least = time;
         parts[0] = {i, 0, a1, 0, b1};
@@ -736,6 +750,9 @@ void launch_part(const MmArgs& a, const Part& p, hipStream_t s) {
       if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 64, 3, !GATED>(a, p, s);
       else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 32, 5, true>(a, p, s);
       break;
+    case 4:
+      if constexpr (A_BY_K && !B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 4, 2, 2, 2, 64, 4, true>(a, p, s);
+      break;
     default:
       if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 64, 2, false>(a, p, s);
       else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 32, 5, true>(a, p, s);
@@ -744,7 +761,8 @@ void launch_part(const MmArgs& a, const Part& p, hipStream_t s) {
 template <bool GATED, bool A_BY_K, bool B_BY_K>
 void launch_mm(const MmArgs& a, hipStream_t s) {
   Part parts[2];
-  const int n = plan(a.A.n * (GATED ? 2 : 1), a.B.n, a.K, parts);
+  const Tiles tiles = A_BY_K && !B_BY_K ? Tiles{DX_TILES, 5} : Tiles{TILES, 4};
+  const int n = plan(tiles, a.A.n * (GATED ? 2 : 1), a.B.n, a.K, parts);
   for (int i = 0; i < n; ++i) launch_part<GATED, A_BY_K, B_BY_K>(a, parts[i], s);
 }
 

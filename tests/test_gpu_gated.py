@@ -212,6 +212,18 @@ def test_a_token_is_the_same_in_any_batch(C, F):
         assert torch.equal(det.gated_linear_backward(dh[a:b], x[a:b], wg, wu, t, need_dw=False)[0], dx[a:b])
 
 
+@pytest.mark.parametrize("N,C,F", [(1100, 1024, 700), (1021, 1537, 900), (520, 4100, 640)])
+def test_dx_of_a_token_with_the_tiles_between(N, C, F):
+    """Batches whose dx is too little for large tiles and too much for the smallest."""
+    x, wg, wu = operands(19, N, C, F)
+    _, s = det.gated_linear_forward(x, wg, wu)
+    dh = torch.randn(N, F, device=DEV).to(BF16)
+    dx = det.gated_linear_backward(dh, x, wg, wu, s, need_dw=False)[0]
+    for a, b in ((0, 1), (N - 67, N), (100, 400)):
+        cut = det.GatedState(*(type(p)(p[0][a:b], p[1][a:b]) for p in s))
+        assert torch.equal(det.gated_linear_backward(dh[a:b], None, wg, wu, cut, need_dw=False)[0], dx[a:b])
+
+
 @pytest.mark.parametrize("N", [3, 70, 300])
 @pytest.mark.parametrize("C", [64, 100, 128])
 def test_layouts(N, C):
