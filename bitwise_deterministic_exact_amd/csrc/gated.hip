@@ -80,9 +80,10 @@ __device__ __forceinline__ void act_times(int act, const float (&g)[4], const fl
 // x, the weights, dg and du as they lie, with no transposed copy.
 //
 // A workgroup of WA x WB waves owns TA x TB outputs, a wave FA x FB blocks of 16
-// x 16.  A ring of BUFS stages of KS k (32 or 64) in LDS is filled with 16-byte
-// copies that need no registers, BUFS - 1 stages ahead; while the MFMAs of 32 k
-// run (one per block), the next 32's fragments are read.  One barrier per stage.
+// x 16.  A ring of BUFS stages of KS k (32, 64 or 128) in LDS is filled with
+// 16-byte copies that need no registers, BUFS - 1 stages ahead; while the MFMAs of
+// 32 k run (128 where KS is; one per block and 32), the next ones' fragments are
+// read.  One barrier per stage.
 //
 // By row: KS k per row, whose 16-byte pieces lie in the order piece ^ swap_row(row).
 // A fragment is one 16-byte read; the 16 lanes that the LDS serves at once (0-3,
@@ -105,7 +106,7 @@ struct MmArgs {
   // a second operand A1 of the same size: the gate's rows are A's, the up
   // projection's A1's (gated); or k goes over A and then, from `turn` on, over A1
   Operand A, A1, B;
-  int64_t K;                              // a multiple of 64: what lies past the rows of k is 0
+  int64_t K;                              // a multiple of 64 (dx: 256): what lies past the rows of k is 0
   int64_t ka, kb, turn;                   // by k: rows of k of A (and of A1), of B
   int64_t begin_a, begin_b, tiles_a, tiles_b;                // this launch's tiles
   // gated: h [n of B][n of A]; else D, rows [0, split0) in out, [split1, split1 + split0) in out1
@@ -160,12 +161,11 @@ struct Tile {
     return T >= 128 ? s : ((k >> 1) & 1) | ((k >> 2) & 2);
   }
   // by row: what a row's pieces are swapped with
-  static __device__ __forceinline__ int swap_row(int r) { return KS == 64 ? r & 7 : -(r >> 2) & 3; }
+  static __device__ __forceinline__ int swap_row(int r) { return KS >= 64 ? r & (PIECES - 1) : -(r >> 2) & 3; }
   int64_t stride;                         // bytes
-  __amdgpu_buffer_rsrc_t buf;             // by row: of the tile
-  int at;                                 // by row: bytes of k before the next stage
-  const char* next;                       // by k: the next stage's first row
-  int left, cols;                         // by k: rows from there on, bytes of a row
+  const char* next;                       // by row: the tile; by k: the next stage's first row
+  int at, end, bytes;                     // by row: bytes of k before the next stage, of a row, of the tile
+  int left, cols;                         // by k: rows from `next` on, bytes of a row
   int from[COPIES];                       // by row: rows past the end are the last one again
   // `limit` of its a or b from `first` on are the tile's
   __device__ __forceinline__ void init(const Operand& o, int64_t first, int limit, int64_t K, int64_t rows, int wave,
@@ -184,22 +184,25 @@ struct Tile {
         from[j] = k * static_cast<int>(stride) + min(piece, cols / 16 - 1) * 16;
       }
     } else {
-      buf = buffer_of(static_cast<const char*>(o.p) + first * stride, (n - 1) * stride + K * 2);
+      next = static_cast<const char*>(o.p) + first * stride;
       at = 0;
+      end = static_cast<int>(K * 2);
+      bytes = (n - 1) * static_cast<int>(stride) + end;
 #pragma unroll
       for (int j = 0; j < COPIES; ++j) {
         const int r = (wave * COPIES + j) * ROWS + lane / PIECES;
-        from[j] = min(r, n - 1) * static_cast<int>(stride) + (((lane % PIECES) ^ swap_row(lane / PIECES)) * 16);
+        from[j] = min(r, n - 1) * static_cast<int>(stride) + (((lane % PIECES) ^ swap_row(r)) * 16);
       }
     }
   }
-  // The next stage into LDS at `to`.  By k: rows past the end lie past the end of
-  // the buffer and come as 0.  By row: K is whole; stages past it, which no MFMA
-  // takes, get the next rows' elements or 0.
+  // The next stage into LDS at `to`; stages past the last one, which no MFMA
+  // takes, read nothing and get 0.  By k: rows past the end lie past the end of the
+  // buffer and come as 0.
   __device__ __forceinline__ void copy(char* to, int wave) {
     if constexpr (BY_K) {
       // No branch: one would keep the copies from going between the MFMAs.  Without
-      // rows, down to -BUFS KS of them, the bytes are at most cols - stride <= 0.
+      // rows, down to 127 + (BUFS - 1) KS <= 511 past the end, the bytes are at most
+      // cols - stride <= 0.
       const __amdgpu_buffer_rsrc_t b = buffer_of(next, max(0, (min(left, KS) - 1) * static_cast<int>(stride) + cols));
 #pragma unroll
       for (int j = 0; j < COPIES; ++j)
@@ -207,9 +210,10 @@ struct Tile {
       next += KS * stride;
       left -= KS;
     } else {
+      const __amdgpu_buffer_rsrc_t b = buffer_of(next, at < end ? bytes : 0);
 #pragma unroll
       for (int j = 0; j < COPIES; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, to + (wave * COPIES + j) * 1024, 16, from[j], at, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b, to + (wave * COPIES + j) * 1024, 16, from[j], at, 0, 0);
       at += KS * 2;
     }
   }
@@ -280,15 +284,20 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
     else return (wa * FA + i) * 16;
   };
   const int at_a = TileA::lane_at(lane), at_b = TileB::lane_at(lane);
+  // fragments of SET x 32 k: of a whole stage, or of one of its halves
+  constexpr int SET = KS == 64 ? 1 : KS / 32;
   struct Frags {
-    bf16x8 fa[FA], fb[FB];
+    bf16x8 fa[SET][FA], fb[SET][FB];
   };
   auto read = [&](Frags& f, int buf, int half) {
     const char* const tile = lds + buf * BUF;
 #pragma unroll
-    for (int j = 0; j < FB; ++j) f.fb[j] = TileB::fragment(tile + TileA::BYTES, at_b, wb * FB + j, half);
+    for (int h = 0; h < SET; ++h) {
 #pragma unroll
-    for (int i = 0; i < FA; ++i) f.fa[i] = TileA::fragment(tile, at_a, frag_row(i) / 16, half);
+      for (int j = 0; j < FB; ++j) f.fb[h][j] = TileB::fragment(tile + TileA::BYTES, at_b, wb * FB + j, half + h);
+#pragma unroll
+      for (int i = 0; i < FA; ++i) f.fa[h][i] = TileA::fragment(tile, at_a, frag_row(i) / 16, half + h);
+    }
   };
   f32x4 acc[FA][FB];
 #pragma unroll
@@ -297,10 +306,12 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
     for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   auto multiply = [&](const Frags& f) {
 #pragma unroll
-    for (int i = 0; i < FA; ++i)
+    for (int h = 0; h < SET; ++h)
 #pragma unroll
-      for (int j = 0; j < FB; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.fa[i], f.fb[j], acc[i][j], 0, 0, 0);
+      for (int i = 0; i < FA; ++i)
+#pragma unroll
+        for (int j = 0; j < FB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.fa[h][i], f.fb[h][j], acc[i][j], 0, 0, 0);
   };
 
   Frags f0, f1;
@@ -311,7 +322,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
   read(f0, 0, 0);
   // SPREAD: the reads and copies go between the MFMAs.  Else they go before them:
   // then one of a SIMD's two waves reads while the other multiplies.
-  constexpr int MFMAS = FA * FB, READS = FA * (A_BY_K ? 2 : 1) + FB * (B_BY_K ? 2 : 1);
+  constexpr int MFMAS = SET * FA * FB, READS = SET * (FA * (A_BY_K ? 2 : 1) + FB * (B_BY_K ? 2 : 1));
   auto run = [&](const Frags& now, auto copies) {
     if constexpr (SPREAD) {
       constexpr int C = decltype(copies)::value, PER = MFMAS - C > READS ? (MFMAS - C) / READS : 1;
@@ -345,8 +356,8 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
     run(now, std::integral_constant<int, COPIES>{});
     buf = next;
   };
-  if constexpr (KS == 32) {
-    for (int s = 0; s < stages; s += 2) { // K is a multiple of 64
+  if constexpr (SET == KS / 32) {
+    for (int s = 0; s < stages; s += 2) { // K is a multiple of two stages
       turn(f0, f1);
       turn(f1, f0);
     }
@@ -633,7 +644,7 @@ __global__ __launch_bounds__(256) void k_clear(uint16_t* p, int64_t n) {
 // be copied first.  64 x 4096 x 11008: 94 us against 45 with tiles, 48 x 2048 x
 // 5461 22 against 10.5, with rows of 2047 22 against 30; one token 34 us.
 constexpr int64_t FEW = 16, FEW_COPIED = 64;
-constexpr int64_t STRIDE_MAX = 1 << 21;   // 383 rows before and after an operand's end lie within 2^31 bytes
+constexpr int64_t STRIDE_MAX = 1 << 21;   // elements: 512 rows before and after an operand's end lie within 2^31 bytes
 
 int64_t up_to(int64_t v, int64_t m) { return ceil_div(v, m) * m; }
 int64_t room(int64_t bytes) { return up_to(bytes, 256); }
@@ -644,32 +655,39 @@ bool direct(const void* p, int64_t stride, int64_t K) {
          (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-// Tiles of 64 x 64, 128 x 128, 128 x 256 or 256 x 256 (A x B; dx: or 128 x 64): large ones move
-// fewer bytes per product, small ones fill the chip.  The rule takes the least of
-// what each would take, rounds (stages t + end), from what was measured (us per
-// stage of 64 k where up to half the CUs have a tile and where all have, a last
-// round in between, and for a tile's end; 64 x 64 fits twice on a CU).  4096
-// features of gate and up together, k 4096, by tokens: 256: 17 us (28, 52, 87 for
-// the larger tiles), 512: 28 28 52 87, 1024: 53 35 52 88, 2048: 103 69 65 89,
-// 4096: 202 135 124 106.  dx, whose A takes twice the LDS reads, is slower where
-// two small tiles share a CU, and has 128 x 64 for what is too little for 128 x
-// 128: 512 x 4096 x 4096 54 us, 63 with 64 x 64; 1100 x 1024 x 2816 40, 47; 1000 x
-// 1024 x 1024 20, 18.  The result's bits are the same for all.
+// Tiles (A x B): large ones move fewer bytes per product, small ones fill the
+// chip.  The rule takes the least of what each would take, rounds (stages t +
+// end), from what was measured: us per stage of 64 k where up to half the CUs have
+// a tile, where a few more have and where all have, and for a tile's end.  The
+// forward pass, 4096 features of gate and up together, k 4096, by tokens, with 64
+// x 64 (which fits twice on a CU), 128 x 128, 128 x 256 and 256 x 256: 256: 17 us
+// 28 52 87, 512: 28 28 52 87, 1024: 53 35 52 88, 2048: 103 69 65 89, 4096: 202 135
+// 124 106.  The gradients have small tiles with 128 k to a stage, alone on their
+// CU, where the chain of stages bounds them: fewer barriers and waits for the LDS
+// (dw of 8192 x 64 x 64 45 -> 33 us, dx of 200 x 4096 x 4096 40 -> 31; the forward
+// pass gains nothing, 16.2 -> 15.6 at best).  A CU gets at most 55 to 90 GB/s into
+// its LDS, so dx has 64 x 32 for few tokens (64 x 4160 x 11008: 110 -> 86) and 128
+// x 64 (1021 x 1537 x 4099: 73 -> 58).  The result's bits are the same for all.
+enum TileKind { T64_TWICE, T128, T128x256, T256, T64, T128x64, T64x32 };
 struct TileCost {
+  TileKind kind;
   int a, b, slots;
   double half, more, full, end;           // `more`: just past half
 };
-constexpr TileCost TILES[4] = {{64, 64, 512, 0.30, 0.30, 0.50, 1.0},
-                               {128, 128, 256, 0.50, 0.50, 0.55, 2.0},
-                               {128, 256, 256, 0.82, 0.82, 0.95, 4.0},
-                               {256, 256, 256, 1.3, 1.3, 1.6, 8.0}};
-constexpr TileCost DX_TILES[5] = {{64, 64, 512, 0.30, 0.42, 0.50, 1.0},
-                                  TILES[1], TILES[2], TILES[3],
-                                  {128, 64, 256, 0.36, 0.36, 0.41, 2.0}};
 struct Tiles {
   const TileCost* of;
   int n;
 };
+constexpr TileCost TWICE = {T64_TWICE, 64, 64, 512, 0.30, 0.30, 0.50, 1.0};
+constexpr TileCost MID = {T128, 128, 128, 256, 0.50, 0.50, 0.55, 2.0};
+constexpr TileCost WIDE = {T128x256, 128, 256, 256, 0.82, 0.82, 0.95, 4.0};
+constexpr TileCost LARGE = {T256, 256, 256, 256, 1.3, 1.3, 1.6, 8.0};
+constexpr TileCost FORWARD[4] = {TWICE, MID, WIDE, LARGE};
+constexpr TileCost DW[5] = {TWICE, MID, WIDE, LARGE, {T64, 64, 64, 256, 0.22, 0.28, 0.30, 2.0}};
+constexpr TileCost DX[6] = {{T64x32, 64, 32, 256, 0.15, 0.17, 0.20, 1.5},
+                            {T64, 64, 64, 256, 0.21, 0.21, 0.21, 2.0},
+                            {T128x64, 128, 64, 256, 0.35, 0.36, 0.38, 2.0},
+                            MID, WIDE, LARGE};
 double tile_time(const TileCost& t, int64_t na, int64_t nb, int64_t K) {
   const int64_t tiles = ceil_div(na, t.a) * ceil_div(nb, t.b), whole = tiles / t.slots, last = tiles % t.slots;
   const double stages = static_cast<double>(K) / 64.0, share = static_cast<double>(last) / t.slots;
@@ -677,7 +695,7 @@ double tile_time(const TileCost& t, int64_t na, int64_t nb, int64_t K) {
   return static_cast<double>(whole) * (stages * t.full + t.end) + (last > 0 ? stages * partly + t.end : 0.0);
 }
 struct Part {
-  int tile;
+  TileKind tile;
   int64_t a0, a1, b0, b1;                 // of A (gated: of both halves together) and B
 };
 double best_tile(const Tiles& tiles, int64_t a0, int64_t a1, int64_t b0, int64_t b1, int64_t K, Part& p) {
@@ -685,7 +703,7 @@ double best_tile(const Tiles& tiles, int64_t a0, int64_t a1, int64_t b0, int64_t
   for (int i = 0; i < tiles.n; ++i) {
     const double time = tile_time(tiles.of[i], a1 - a0, b1 - b0, K);
     if (i == 0 || time < least) {
-      p = {i, a0, a1, b0, b1};
+      p = {tiles.of[i].kind, a0, a1, b0, b1};
       least = time;
     }
   }
@@ -711,7 +729,7 @@ int plan(const Tiles& tiles, int64_t na, int64_t nb, int64_t K, Part (&parts)[2]
           LAUNCH + tile_time(t, a1, b1, K) + best_tile(tiles, by_b ? 0 : a1, na, by_b ? b1 : 0, nb, K, rest);
       if (time < least) {
         least = time;
-        parts[0] = {i, 0, a1, 0, b1};
+        parts[0] = {t.kind, 0, a1, 0, b1};
         parts[1] = rest;
         n = 2;
       }
@@ -727,41 +745,49 @@ void launch_tiles(MmArgs a, const Part& p, hipStream_t s) {
   a.begin_b = p.b0;
   a.tiles_a = ceil_div(p.a1 - p.a0, WA * FA * 16);
   a.tiles_b = ceil_div(p.b1 - p.b0, WB * FB * 16);
+  if constexpr (B_BY_K && KS == 128) a.K = a.turn = up_to(a.K, 2 * KS);      // rows past the end are 0
   hipLaunchKernelGGL((k_mm<GATED, A_BY_K, B_BY_K, WA, WB, FA, FB, KS, BUFS, SPREAD>),
                      dim3(static_cast<unsigned>(a.tiles_a * a.tiles_b)), dim3(64 * WA * WB), 0, s, a);
 }
 
-// By row 64 k to a stage (whole lines of memory), its reads before its MFMAs;
-// by k 32 and 64, spread: 8192 x 4096 x 11008 forward 1187 us so, 1204 spread,
-// 1306 with 32; dx and its dg and du 1287 against 1387 and 1362, dw 1349 against 1500.
+// Large tiles: by row 64 k to a stage (whole lines of memory), its reads before
+// its MFMAs; by k 32 and 64, spread: 8192 x 4096 x 11008 forward 1187 us so, 1204
+// spread, 1306 with 32; dx and its dg and du 1287 against 1387 and 1362, dw 1349
+// against 1500.
 template <bool GATED, bool A_BY_K, bool B_BY_K>
 void launch_part(const MmArgs& a, const Part& p, hipStream_t s) {
   switch (p.tile) {
-    case 0:
+    case T64_TWICE:
       if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 64, 5, false>(a, p, s);
-      else if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 2, 1, 64, 5, true>(a, p, s);
-      else launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 32, 5, true>(a, p, s);
+      else if constexpr (B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 1, 4, 4, 1, 32, 5, true>(a, p, s);
       break;
-    case 1:
+    case T128:
       if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 2, 64, 5, true>(a, p, s);
       else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 2, 4, 4, 32, 5, true>(a, p, s);
       break;
-    case 2:
+    case T128x256:
       if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 64, 3, !GATED>(a, p, s);
       else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 32, 5, true>(a, p, s);
       break;
-    case 4:
-      if constexpr (A_BY_K && !B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 4, 2, 2, 2, 64, 4, true>(a, p, s);
-      break;
-    default:
+    case T256:
       if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 64, 2, false>(a, p, s);
       else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 8, 4, 32, 5, true>(a, p, s);
+      break;
+    case T64:
+      if constexpr (!GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 4, 2, 1, 2, 128, 4, true>(a, p, s);
+      break;
+    case T128x64:
+      if constexpr (!GATED && !B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 8, 2, 1, 2, 128, 3, true>(a, p, s);
+      break;
+    case T64x32:
+      if constexpr (!GATED && !B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 4, 2, 1, 1, 128, 4, true>(a, p, s);
+      break;
   }
 }
 template <bool GATED, bool A_BY_K, bool B_BY_K>
 void launch_mm(const MmArgs& a, hipStream_t s) {
   Part parts[2];
-  const Tiles tiles = A_BY_K && !B_BY_K ? Tiles{DX_TILES, 5} : Tiles{TILES, 4};
+  const Tiles tiles = GATED ? Tiles{FORWARD, 4} : B_BY_K ? Tiles{DW, 5} : Tiles{DX, 6};
   const int n = plan(tiles, a.A.n * (GATED ? 2 : 1), a.B.n, a.K, parts);
   for (int i = 0; i < n; ++i) launch_part<GATED, A_BY_K, B_BY_K>(a, parts[i], s);
 }
@@ -886,7 +912,7 @@ int64_t det_gated_linear_grad_workspace_bytes(int64_t N, int64_t C, int64_t F, i
     return 0;
   const int64_t Cp = up_to(C, 64);
   const bool as_is = C % 64 == 0 && aligned;
-  return room(N * 2 * up_to(F, 64) * 2) + (need_dx && !as_is ? 2 * room(F * Cp * 2) : 0) +
+  return room(N * 2 * up_to(F, 128) * 2) + (need_dx && !as_is ? 2 * room(F * Cp * 2) : 0) +
          (need_dw && (packed || !as_is) ? room(N * Cp * 2) : 0);
 }
 
@@ -928,7 +954,7 @@ det_status det_gated_linear_grad(det_dtype dh_dt, const void* dh, int64_t s_dh, 
     if (x == nullptr || s_x < 0) return fail(DET_EINVAL, "null x or negative stride");
     if (x_exp == nullptr && !aligned_for(x, DET_BF16)) return fail(DET_EINVAL, "x must be aligned to its element size");
   }
-  const int64_t Cp = up_to(C, 64), Fp = up_to(F, 64), rows = room(N * 2 * Fp * 2);
+  const int64_t Cp = up_to(C, 64), Fp = up_to(F, 128), rows = room(N * 2 * Fp * 2);
   const bool codes = need_dw && x_exp != nullptr;
   // k runs over both weights with one stride
   const bool copy_w = !direct(w_gate, s_gate, C) || !direct(w_up, s_up, C) || s_gate != s_up;

@@ -212,7 +212,7 @@ def test_a_token_is_the_same_in_any_batch(C, F):
         assert torch.equal(det.gated_linear_backward(dh[a:b], x[a:b], wg, wu, t, need_dw=False)[0], dx[a:b])
 
 
-@pytest.mark.parametrize("N,C,F", [(1100, 1024, 700), (1021, 1537, 900), (520, 4100, 640)])
+@pytest.mark.parametrize("N,C,F", [(1100, 1024, 700), (1021, 1537, 900), (520, 4100, 640), (90, 200, 129), (3000, 70, 65)])
 def test_dx_of_a_token_with_the_tiles_between(N, C, F):
     """Batches whose dx is too little for large tiles and too much for the smallest."""
     x, wg, wu = operands(19, N, C, F)
@@ -274,6 +274,28 @@ def test_no_rows():
         assert h.shape == (0, 24)
         gx, gw = torch.autograd.grad(h, (x, w), torch.empty_like(h))
         assert gx.shape == (0, 40) and torch.equal(gw, torch.zeros_like(w))
+
+
+@pytest.mark.parametrize("N", [63, 129, 1000, 4097])
+@pytest.mark.parametrize("C,F", [(64, 30), (100, 300), (130, 1000)])
+def test_weight_gradients_over_long_batches_of_narrow_layers(N, C, F):
+    """Few tiles and a long chain.  Integers: all sums are exact, whatever lies past the last row."""
+    g = torch.Generator(device=DEV).manual_seed(20)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g, device=DEV).to(BF16)
+    x = ints(N + 300, C)
+    x[N:] = float("inf")                                # rows of the batch that this call is not given
+    x = x[:N]
+    wg, wu = torch.zeros(2, F, C, device=DEV, dtype=BF16)
+    wg[:, 0] = wu[:, 0] = 1.0
+    _, s = det.gated_linear_forward(x, wg, wu)
+    dh = ints(N, F)
+    gates = det.GatedState(det.ScaledHalf(torch.zeros_like(s.gate[0]), s.gate[1]), s.up)
+    # g = 0: silu is 0 and its slope 1/2, so dg = dh u / 2 and du = 0
+    _, dwg, dwu = det.gated_linear_backward(dh, x, wg, wu, gates, need_dx=False)
+    dg = (dh.double() * x[:, :1].double() / 2).to(BF16).double()
+    want = dg.t() @ x.double()
+    assert want.abs().max() < 2 ** 24 and torch.equal(dwg, want.to(torch.float32).to(BF16))
+    assert torch.equal(dwu, torch.zeros_like(dwu))
 
 
 def test_rows_that_are_not_finite_stay_by_themselves():
