@@ -376,6 +376,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
   // by itself, so that a row is written in whole lines.  Lane l holds features
   // 4 (l / 16) .. + 3 of a block, of row l % 16.
   constexpr int ROW = FA * 16 + 4;        // floats; 4 more, or all rows would start in one bank
+  static_assert(NW * 16 * ROW * 4 <= BUFS * BUF, "the rows lie in the ring's room");
   float* const own = reinterpret_cast<float*>(lds) + wave * 16 * ROW;
 #pragma unroll
   for (int j = 0; j < FB; ++j) {
@@ -657,38 +658,55 @@ bool direct(const void* p, int64_t stride, int64_t K) {
 
 // Tiles (A x B): large ones move fewer bytes per product, small ones fill the
 // chip.  The rule takes the least of what each would take, rounds (stages t +
-// end), from what was measured: us per stage of 64 k where up to half the CUs have
-// a tile, where a few more have and where all have, and for a tile's end.  The
-// forward pass, 4096 features of gate and up together, k 4096, by tokens, with 64
-// x 64 (which fits twice on a CU), 128 x 128, 128 x 256 and 256 x 256: 256: 17 us
-// 28 52 87, 512: 28 28 52 87, 1024: 53 35 52 88, 2048: 103 69 65 89, 4096: 202 135
-// 124 106.  The gradients have small tiles with 128 k to a stage, alone on their
-// CU, where the chain of stages bounds them: fewer barriers and waits for the LDS
-// (dw of 8192 x 64 x 64 45 -> 33 us, dx of 200 x 4096 x 4096 40 -> 31; the forward
-// pass gains nothing, 16.2 -> 15.6 at best).  A CU gets at most 55 to 90 GB/s into
-// its LDS, so dx has 64 x 32 for few tokens (64 x 4160 x 11008: 110 -> 86) and 128
-// x 64 (1021 x 1537 x 4099: 73 -> 58).  The result's bits are the same for all.
-enum TileKind { T64_TWICE, T128, T128x256, T256, T64, T128x64, T64x32 };
+// end), from what was measured: us per stage of 64 k where up to half the slots
+// have a tile, where a few more have and where all have, and for a round's start
+// and end.  The forward pass, 4096 features of gate and up together, k 4096, by
+// tokens, with 64 x 64 (which fits twice on a CU), 128 x 128, 128 x 256 and 256 x
+// 256: 256: 17 us 28 52 87, 512: 28 28 52 87, 1024: 53 35 52 88, 2048: 103 69 65 89,
+// 4096: 202 135 124 106.
+// "Twice" has a ring short enough for two workgroups on a CU: one's start and end
+// go beside the other's products, where many tiles have few stages (forward with
+// projections kept, 2000 x 512 x 2816: 35 -> 26 us, 2000 x 1024 x 2816 43 -> 38; dw
+// of 500 x 2048 x 5632 54 -> 45).  It waits for its copies where it is alone (512 x
+// 4096 x 2048 forward 45, 29 with the long ring) or they come from HBM for long
+// (362 x 5824 x 8192 100, 91), so it is left to short k (dw of 2426 x 832 x 3520 57,
+// 54).
+// The gradients have small tiles with 128 k to a stage, alone on their CU, where
+// the chain of stages bounds them: fewer barriers and waits for the LDS (dw of 8192
+// x 64 x 64 45 -> 33 us, dx of 200 x 4096 x 4096 40 -> 31; the forward pass gains
+// nothing, 16.2 -> 15.6 at best).  A CU gets at most 55 to 90 GB/s into its LDS, so
+// dx has 64 x 32 for few tokens (64 x 4160 x 11008: 110 -> 86) and 128 x 64 (1021 x
+// 1537 x 4099: 73 -> 58).  The result's bits are the same for all.
+enum TileKind { T64_TWICE, T128, T128_TWICE, T128x256, T256, T64, T128x64, T64x32 };
 struct TileCost {
   TileKind kind;
   int a, b, slots;
   double half, more, full, end;           // `more`: just past half
+  int64_t longest = int64_t{1} << 32;     // k that it is taken for
 };
 struct Tiles {
   const TileCost* of;
   int n;
 };
-constexpr TileCost TWICE = {T64_TWICE, 64, 64, 512, 0.30, 0.30, 0.50, 1.0};
-constexpr TileCost MID = {T128, 128, 128, 256, 0.50, 0.50, 0.55, 2.0};
-constexpr TileCost WIDE = {T128x256, 128, 256, 256, 0.82, 0.82, 0.95, 4.0};
-constexpr TileCost LARGE = {T256, 256, 256, 256, 1.3, 1.3, 1.6, 8.0};
-constexpr TileCost FORWARD[4] = {TWICE, MID, WIDE, LARGE};
-constexpr TileCost DW[5] = {TWICE, MID, WIDE, LARGE, {T64, 64, 64, 256, 0.22, 0.28, 0.30, 2.0}};
+constexpr TileCost FORWARD[5] = {{T64_TWICE, 64, 64, 512, 0.21, 0.30, 0.40, 2.0},
+                                 {T128, 128, 128, 256, 0.44, 0.48, 0.52, 4.0},
+                                 {T128_TWICE, 128, 128, 512, 0.64, 0.70, 0.88, 5.0, 2048},
+                                 {T128x256, 128, 256, 256, 0.72, 0.76, 0.93, 6.3},
+                                 {T256, 256, 256, 256, 1.16, 1.2, 1.52, 12.5}};
 constexpr TileCost DX[6] = {{T64x32, 64, 32, 256, 0.15, 0.17, 0.20, 1.5},
                             {T64, 64, 64, 256, 0.21, 0.21, 0.21, 2.0},
                             {T128x64, 128, 64, 256, 0.35, 0.36, 0.38, 2.0},
-                            MID, WIDE, LARGE};
+                            {T128, 128, 128, 256, 0.50, 0.50, 0.55, 2.0},
+                            {T128x256, 128, 256, 256, 0.82, 0.82, 0.95, 4.0},
+                            {T256, 256, 256, 256, 1.3, 1.3, 1.6, 8.0}};
+constexpr TileCost DW[6] = {{T64, 64, 64, 256, 0.25, 0.36, 0.38, 2.0},
+                            {T64_TWICE, 64, 64, 512, 0.37, 0.42, 0.50, 2.0},
+                            {T128, 128, 128, 256, 0.53, 0.55, 0.55, 3.5},
+                            {T128_TWICE, 128, 128, 512, 0.68, 0.80, 0.99, 6.4, 1024},
+                            {T128x256, 128, 256, 256, 0.75, 0.80, 1.1, 7.3},
+                            {T256, 256, 256, 256, 1.1, 1.3, 1.62, 13.0}};
 double tile_time(const TileCost& t, int64_t na, int64_t nb, int64_t K) {
+  if (K > t.longest) return INFINITY;
   const int64_t tiles = ceil_div(na, t.a) * ceil_div(nb, t.b), whole = tiles / t.slots, last = tiles % t.slots;
   const double stages = static_cast<double>(K) / 64.0, share = static_cast<double>(last) / t.slots;
   const double partly = share <= 0.5 ? t.half : t.more + (t.full - t.more) * (2.0 * share - 1.0);
@@ -765,6 +783,10 @@ void launch_part(const MmArgs& a, const Part& p, hipStream_t s) {
       if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 2, 64, 5, true>(a, p, s);
       else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 2, 4, 4, 32, 5, true>(a, p, s);
       break;
+    case T128_TWICE:
+      if constexpr (GATED) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 2, 64, 2, true>(a, p, s);
+      else if constexpr (B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 2, 4, 4, 32, 3, true>(a, p, s);
+      break;
     case T128x256:
       if constexpr (!B_BY_K) launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 64, 3, !GATED>(a, p, s);
       else launch_tiles<GATED, A_BY_K, B_BY_K, 2, 4, 4, 4, 32, 5, true>(a, p, s);
@@ -787,7 +809,7 @@ void launch_part(const MmArgs& a, const Part& p, hipStream_t s) {
 template <bool GATED, bool A_BY_K, bool B_BY_K>
 void launch_mm(const MmArgs& a, hipStream_t s) {
   Part parts[2];
-  const Tiles tiles = GATED ? Tiles{FORWARD, 4} : B_BY_K ? Tiles{DW, 5} : Tiles{DX, 6};
+  const Tiles tiles = GATED ? Tiles{FORWARD, 5} : B_BY_K ? Tiles{DW, 6} : Tiles{DX, 6};
   const int n = plan(tiles, a.A.n * (GATED ? 2 : 1), a.B.n, a.K, parts);
   for (int i = 0; i < n; ++i) launch_part<GATED, A_BY_K, B_BY_K>(a, parts[i], s);
 }

@@ -160,6 +160,12 @@ def test_gradients_against_64_bits(N, C, F, act, dtype):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("N,C,F", [(1100, 130, 2500), (200, 1000, 2500), (2000, 512, 2816)])
+def test_many_tiles_of_few_stages(N, C, F):
+    test_products_are_exact_on_integers(N, C, F)
+    test_gradients_against_64_bits(N, C, F, "silu", BF16)
+
+
 @pytest.mark.parametrize("N,C,F", [(1, 31, 1), (17, 100, 64), (130, 128, 100), (300, 96, 33), (4100, 64, 2100)])
 def test_int8_checkpoint(N, C, F):
     announce(f"gated int8 {N} {C} {F}")
