@@ -54,8 +54,20 @@ __device__ __forceinline__ Act act_of(float g) {
     const float slope = s.s * s.rest * fmaf(0.214064449f, g2, 1.59576912f);
     return {g * s.s, fmaf(g, slope, s.s)};
   } else {
-    const float p = 0.5f * erfcf(g * -0.707106769f);
-    return {g * p, fmaf(g, 0.398942292f * exp_of(-0.5f * g * g), p)};
+    // Phi(-|g|) = e^(-g^2 / 2) E / 2 with E = erfcx(|g| / sqrt 2) = t p(t), t = 1 / (1 + |g| / sqrt 8):
+    // p of degree 8 is fitted to E / t for |g| up to 14.7, off by 4.3e-8 of it at most; with the roundings
+    // Phi is within 4 units.  The square is carried in two parts, as a rounded one costs g^2 / 2 half
+    // units; from 20 on e^(-g^2 / 2) is 0.  (By erfcf, and e^(-g^2 / 2) beside it, 2048 x 1024 x 2816 forward
+    // took 41 us, 35.5 so, and dx with dg and du 52.5, 46.5.)
+    const float w = fminf(fabsf(g), 20.0f), s = w * w, e0 = exp_of(-0.5f * s);
+    const float e = fmaf(e0, -0.5f * fmaf(w, w, -s), e0), t = __builtin_amdgcn_rcpf(fmaf(w, 0.353553391f, 1.0f));
+    const float c[8] = {0.142540082f, -0.24412401f, 0.139634386f, -0.0137276426f,
+                        0.101519361f, 0.121507309f, 0.141193792f, 0.141042858f};
+    float p = -0.0295861568f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p = fmaf(p, t, c[k]);
+    const float q = t * p * e, cdf = g > 0.0f ? 1.0f - q : q;
+    return {g * cdf, fmaf(g, 0.398942292f * e, cdf)};
   }
 }
 

@@ -452,6 +452,28 @@ def test_rows_far_apart(N, F):
         del room
 
 
+@pytest.mark.parametrize("N", [1, 70])
+def test_gelu_against_64_bits(N):
+    """Any fp32 value as g, from three bf16 parts, times u = 1."""
+    r = 1e-6 * 1.3e7 ** torch.rand(8192, device=DEV, dtype=torch.float64, generator=torch.Generator(device=DEV).manual_seed(21))
+    g = torch.cat([r, -r]).float()
+    hi = g.to(BF16)
+    mid = (g - hi.float()).to(BF16)
+    lo = (g - hi.float() - mid.float()).to(BF16)
+    zero, one = torch.zeros_like(hi), torch.ones_like(hi)
+    wg, wu = torch.stack([hi, mid, lo, zero], 1), torch.stack([one, zero, zero, zero], 1)
+    x = torch.tensor([1, 1, 1, 0], device=DEV, dtype=BF16).expand(N, 4)
+    h = det.gated_linear(x, wg, wu, activation="gelu", out_dtype=F32)
+    G = hi.double() + mid.double() + lo.double()
+    want = G * 0.5 * torch.special.erfc(-G / math.sqrt(2.0))
+    # half steps: 4 of the exponential and 1 of its correction, 3 of the polynomial, 2 of the reciprocal, 1 of the fit,
+    # 5 products and the difference from 1; g itself is a sum of three parts in 32 bits (2, and g Phi(g) changes by up to
+    # (1 + g^2) times as much below 0)
+    bound = (16 + 2 * (1 + G * G)) * U[F32] * want.abs() + 1e-37
+    for row in h:
+        within(row, want, bound, "gelu")
+
+
 def test_activations_far_out():
     # their limits' slopes, 1 and 0, as far as fp32 goes
     one = torch.ones(70, 1, device=DEV, dtype=BF16)
