@@ -72,8 +72,12 @@ Tensor gated_forward(const Tensor& x, const Tensor& wg, const Tensor& wu, det_ac
     const auto o = x.options().dtype(save == DET_SAVE_INT8 ? at::kChar : at::kHalf), e = x.options().dtype(at::kChar);
     // rows of a multiple of 32, so that every row is written and read in aligned words
     const int64_t Fs = (F + 31) / 32 * 32;
-    kept.gate = at::empty(with_last(lead_of(x), Fs), o).narrow(-1, 0, F);
-    kept.up = at::empty(with_last(lead_of(x), Fs), o).narrow(-1, 0, F);
+    kept.gate = at::empty(with_last(lead_of(x), Fs), o);
+    kept.up = at::empty(with_last(lead_of(x), Fs), o);
+    if (Fs != F) {
+      kept.gate = kept.gate.narrow(-1, 0, F);
+      kept.up = kept.up.narrow(-1, 0, F);
+    }
     kept.gate_exp = at::empty(blocks, e);
     kept.up_exp = at::empty(blocks, e);
   }
