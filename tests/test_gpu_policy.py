@@ -154,6 +154,21 @@ def test_the_order_of_the_rows_does_not_matter(B, T, reduction):
                                                 ref_logprob=ref[p], **opts), dlp[p])
 
 
+@pytest.mark.parametrize("T", [1, 5, 300, 512])
+@pytest.mark.parametrize("B", [1, 16, 17, 32])
+def test_a_few_rows_and_the_same_among_others(B, T):
+    """Rows that one launch takes, and in a batch whose other rows do not count: the same sums."""
+    lp, old, adv, mask, ref = answers(22, B, T, masked=False)
+    wide = lambda t, fill: torch.cat([t, torch.full((40, T), fill, device=DEV, dtype=t.dtype)])
+    for reduction in ("tokens", "sequences"):
+        few, count = det.policy_loss_forward(lp, old, adv, None, ref_logprob=ref, kl_weight=0.1, reduction=reduction)
+        all_, many = det.policy_loss_forward(*(wide(t, NAN) for t in (lp, old, adv)),
+                                             wide(torch.ones(B, T, device=DEV, dtype=torch.bool), False),
+                                             ref_logprob=wide(ref, NAN), kl_weight=0.1, reduction=reduction)
+        assert all(torch.equal(a, b) for a, b in zip(few, all_))
+        assert torch.equal(count[:B], many[:B]) and count[B] == many[B + 40] and not many[B:B + 40].any()
+
+
 @pytest.mark.parametrize("reduction", ["tokens", "sequences", "none"])
 def test_nothing_that_counts(reduction):
     lp = torch.full((5, 40), NAN, device=DEV, requires_grad=True)
