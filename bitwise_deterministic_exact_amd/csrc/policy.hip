@@ -233,8 +233,7 @@ __global__ __launch_bounds__(256) void k_policy(PolicyArgs a) {
 }
 
 // Rows joined: a row's pieces are added in 64 bits, in ascending order (up to 16
-// of them) or over the lanes of a wave; the rows' values, to 48 bits, are
-// added exactly.  Three sums (loss, KL, clipped) of NDIG digits, their values
+// of them) or over the lanes of a wave; the rows' values are added exactly.  Three sums (loss, KL, clipped) of NDIG digits, their values
 // that are not finite by kind, and two counts.
 constexpr int SUMS = 3, JOINED = SUMS * NDIG + SUMS + 2, SERIAL = 16, AHEAD = 8, JOIN_THREADS = 1024;
 
@@ -246,17 +245,17 @@ struct JoinTotals {
 
 // the sum of `digits` and the kinds as a value
 template <class D>
-__device__ __forceinline__ float sum_value(D digit, int kinds) {
+__device__ __forceinline__ double sum_value(D digit, int kinds) {
   if (kinds & 1 || kinds == 6) return NAN;
   if (kinds != 0) return kinds == 2 ? INFINITY : -INFINITY;
-  return round_digits(digit, false);
+  return sum_of_digits(digit);
 }
-// the three results from the totals: one more division each, in 64 bits
-template <class Value>
-__device__ __forceinline__ void policy_results(const PolicyArgs& a, int k, Value value, int64_t tokens, int64_t rows) {
+// the three results from the totals, divided in 64 bits (a sum may lie past fp32
+// where its mean does not) and rounded to fp32 once
+__device__ __forceinline__ void policy_results(const PolicyArgs& a, int k, double value, int64_t tokens, int64_t rows) {
   const int64_t n = max<int64_t>(1, a.reduction == DET_REDUCE_TOKENS ? tokens : rows);
   float* const to = k == 0 ? a.loss : k == 1 ? a.kl : a.clipped;
-  *to = static_cast<float>(static_cast<double>(value) / static_cast<double>(n));
+  *to = static_cast<float>(value / static_cast<double>(n));
   if (k == 0) a.count[a.B] = n;
 }
 
@@ -313,15 +312,9 @@ __device__ __forceinline__ void join_rows(const PolicyArgs& a, JoinTotals& s, Ge
 #pragma unroll
     for (int k = 0; k < SUMS; ++k) {
       if (a.reduction == DET_REDUCE_SEQUENCES) sum[k] /= static_cast<double>(max<int64_t>(count, 1));
-      // two fp32 parts, 48 bits: what a row's rounding to one would leave shows where rows cancel
-      const float hi = static_cast<float>(sum[k]), lo = static_cast<float>(sum[k] - static_cast<double>(hi));
       auto add = [&](int j, int64_t x) { atomicAdd(&s.digits[k][j][lane], static_cast<unsigned long long>(x)); };
-      if (!(fabsf(hi) < INFINITY)) {
-        atomicOr(&s.kinds[k], hi != hi ? 1 : hi > 0.0f ? 2 : 4);
-      } else {
-        add_digits(__float_as_uint(hi), add);
-        add_digits(__float_as_uint(lo), add);
-      }
+      if (!(fabs(sum[k]) < INFINITY)) atomicOr(&s.kinds[k], sum[k] != sum[k] ? 1 : sum[k] > 0.0 ? 2 : 4);
+      else add_digits(sum[k], add);
     }
   }
 #pragma unroll

@@ -13,8 +13,8 @@ z = beta (s_chosen - s_rejected) - margin:
   ipo      (s_chosen - s_rejected - 1 / (2 beta))^2
 
 A row's sums are formed in 64 bits in an order that its length alone decides;
-the policy loss adds the rows' values exactly and rounds once (det-train page,
-"Method"), so it does not depend on the order of the rows.  exact_mean averages
+the policy loss adds the rows' values exactly, divides in 64 bits and rounds once
+(det-train page, "Method"), so it does not depend on the order of the rows.  exact_mean averages
 a batch's preference losses the same way.
 
 Tokens that a mask leaves out are not looked at, whatever they hold, and have no

@@ -663,10 +663,10 @@ typedef enum { DET_PREFER_SIGMOID = 0, DET_PREFER_HINGE = 1, DET_PREFER_IPO = 2 
  *                     tokens' or the rows' sum, for the gradient; null with none
  *   workspace         det_policy_loss_workspace_bytes(B, T, reduction), 16-byte
  *                     aligned
- * A row's sums are formed in 64 bits in one order per T and kept to 48 bits (for
- * sequences after the division by its count); the rows' values are added exactly
- * and rounded once, then divided: the results do not depend on the order of the
- * rows.  A token that counts and whose l is not finite is noted in the
+ * A row's sums are formed in 64 bits in one order per T (for sequences divided by
+ * its count there); the rows' values are added exactly, to 2^-170, and the
+ * quotient is rounded to fp32 once: the results do not depend on the order of
+ * the rows.  A token that counts and whose l is not finite is noted in the
  * device status ("non-finite"); the sums follow IEEE arithmetic (NaN, or both
  * infinities: NaN).  B <= 2^22, T <= 2^24, B T <= 2^32.
  * Returns DET_OK, DET_EINVAL or DET_EHIP.

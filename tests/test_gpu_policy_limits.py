@@ -1,0 +1,59 @@
+"""The policy and preference losses where fp32 on the way would show: sums and
+ratios past its range, one rounding of a mean, differences that it does not
+hold, and what a preference loss keeps for its gradient."""
+from fractions import Fraction
+
+import pytest
+import torch
+
+import bitwise_deterministic_exact_amd as det
+from tests.gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24                                      # half a step of fp32
+
+
+def within(got, want, bound, what):
+    assert got.dtype == torch.float32
+    bad = ~((got.double() - want).abs() <= bound)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off: {got[bad][:3]} for {want[bad][:3]}"
+
+
+# one launch of few rows, rows of several workgroups, more pieces than one thread adds, several workgroups that join
+@pytest.mark.parametrize("reduction", ["tokens", "sequences"])
+@pytest.mark.parametrize("B,T", [(1, 4), (20, 300), (40, 7), (3, 5000), (1, 70000), (17000, 3)])
+def test_means_whose_sums_pass_fp32(B, T, reduction):
+    announce(f"policy far sums {B} {T} {reduction}")
+    det.device_status()
+    g = torch.Generator(device=DEV).manual_seed(1)
+    old = -88.0 - 0.7 * torch.rand(B, T, generator=g, device=DEV)
+    lp = torch.zeros(B, T, device=DEV, requires_grad=True)
+    adv = torch.full((B,), -1.0, device=DEV)        # a negative advantage is not clipped above: l = e^d up to 3.3e38
+    ref = -old
+    each, rise = torch.exp(-old.double()), torch.exp(ref.double())
+    r = det.policy_loss(lp, old, adv, ref_logprob=ref, reduction=reduction)
+    # 8 half steps of a token's value, half a step of the mean
+    within(r.loss, each.mean(), 9 * U * each.mean(), "loss")
+    kl = (rise - 1 - ref.double()).mean()
+    within(r.kl, kl, 9 * U * kl, "kl")
+    assert not det.device_status()
+    grad, = torch.autograd.grad(r.loss, lp)
+    within(grad, each / (B * T), 10 * U * each / (B * T), "gradient")
+    # pairs of rows that cancel leave the last one, if any: with r = 1 a token's loss is -A
+    adv = torch.where(torch.arange(B, device=DEV) % 2 == 0, -1.0, 1.0) * 2.0 ** 127
+    want = 2.0 ** 127 / B if B % 2 else 0.0
+    assert det.policy_loss(old, old, adv, reduction=reduction).loss.item() == torch.tensor(want).item()
+
+
+@pytest.mark.parametrize("reduction", ["tokens", "sequences"])
+def test_a_mean_is_rounded_once(reduction):
+    """With r = 1 a token's loss is -A, so a mean is a quotient of exact numbers."""
+    for seed in range(40):
+        g = torch.Generator().manual_seed(seed)
+        B, T = (7, 3) if seed % 2 == 0 else (41, 11)
+        lp, adv = -torch.rand(B, T, generator=g), torch.randn(B, T, generator=g)
+        total = sum(Fraction(v) for v in (-adv.double()).flatten().tolist())
+        want = torch.tensor(float(total / (B * T)), dtype=torch.float64).float()
+        got = det.policy_loss(lp.to(DEV), lp.to(DEV), adv.to(DEV), reduction=reduction).loss
+        assert got.item() == want.item(), seed
