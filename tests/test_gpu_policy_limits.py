@@ -57,3 +57,36 @@ def test_a_mean_is_rounded_once(reduction):
         want = torch.tensor(float(total / (B * T)), dtype=torch.float64).float()
         got = det.policy_loss(lp.to(DEV), lp.to(DEV), adv.to(DEV), reduction=reduction).loss
         assert got.item() == want.item(), seed
+
+
+def test_ratios_past_fp32():
+    """r alone leaves fp32 on either side, r A does not: also where the old policy ruled a token out."""
+    low = torch.finfo(torch.float32).min
+    d, a = [], []
+    for x, y in ((88.9, -1e-10), (100.25, -1e-20), (150.5, -3e-38), (180.125, -2e-45), (-88.5, 1e10), (-100.25, 1e30), (-120.0, 2e38),
+                 (-180.0, 3e38), (80.5, -1.0), (-80.5, 1.0), (85.0, -1e-5), (81.0, -1e-44)):
+        d.append(x)
+        a.append(y)
+    # differences that fp32 holds, and some that it does not
+    for first in (0.0, -0.7331, -13.37):
+        lp = torch.full((len(d),), first, device=DEV, requires_grad=True)
+        old, adv = first - torch.tensor(d, device=DEV), torch.tensor(a, device=DEV)
+        r = det.policy_loss(lp, old, adv, reduction="none")
+        want = -torch.exp(lp.detach().double() - old.double()) * adv.double()
+        # four factors (2 units of the exponential, its low part) and four products; below 2^-126 half a step is 2^-150
+        within(r.loss, want, 24 * U * want.abs() + 2.0 ** -149, "loss")
+        grad, = torch.autograd.grad(r.loss.sum(), lp)
+        within(grad, want, 24 * U * want.abs() + 2.0 ** -149, "gradient")
+    # no advantage: no loss and no gradient, however far the ratio is
+    det.device_status()
+    old = torch.tensor([low, -1e9, -89.0, -1000.0, 0.0, 89.0, 1e9, -low], device=DEV)
+    lp = torch.zeros(8, device=DEV, requires_grad=True)
+    for reduction in ("none", "tokens", "sequences"):
+        r = det.policy_loss(lp, old, torch.zeros(8, device=DEV), reduction=reduction)
+        grad, = torch.autograd.grad(r.loss.sum(), lp)
+        assert (r.loss == 0).all() and (grad == 0).all() and (r.clipped == 0).all()
+    assert not det.device_status()
+    # with one: clipped, or past fp32
+    assert det.policy_loss(lp, old, torch.ones(8, device=DEV), reduction="none").loss.tolist()[:4] == [-torch.tensor(1.2).item()] * 4
+    assert (det.policy_loss(lp, old, -torch.ones(8, device=DEV), reduction="none").loss[:2] == float("inf")).all()
+    det.device_status()
