@@ -131,7 +131,8 @@ __device__ __forceinline__ Token token_of(const PolicyArgs& a, float lp, float o
   t.slope = t.clipped ? 0.0f : -whole;
   t.kl = 0.0f;
   if (a.ref != nullptr) {
-    const float q = static_cast<float>(static_cast<double>(ref) - static_cast<double>(lp));
+    const double dq = static_cast<double>(ref) - static_cast<double>(lp);
+    const float q = static_cast<float>(dq), rest = static_cast<float>(dq - static_cast<double>(q));
     float rise;                           // e^q - 1
     if (fabsf(q) <= 1.0f) {
       // e^q - 1 - q = q^2 (1/2 + q/6 + ...), to q^12: no difference of near values
@@ -143,7 +144,9 @@ __device__ __forceinline__ Token token_of(const PolicyArgs& a, float lp, float o
       t.kl = q * q * s;
       rise = q + t.kl;
     } else {
-      rise = exp_of(q) - 1.0f;
+      // the low part where it is one: without it e^q would be off by |q| half units
+      const float e = exp_of(q);
+      rise = (e < INFINITY && q > -INFINITY ? fmaf(e, rest, e) : e) - 1.0f;
       t.kl = q < INFINITY ? rise - q : q;
       if (q != q) t.kl = rise = q;
     }

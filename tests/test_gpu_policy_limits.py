@@ -90,3 +90,18 @@ def test_ratios_past_fp32():
     assert det.policy_loss(lp, old, torch.ones(8, device=DEV), reduction="none").loss.tolist()[:4] == [-torch.tensor(1.2).item()] * 4
     assert (det.policy_loss(lp, old, -torch.ones(8, device=DEV), reduction="none").loss[:2] == float("inf")).all()
     det.device_status()
+
+
+def test_estimates_of_far_differences():
+    """q = ref - logprob needs more than 32 bits: e^q shows what is missing |q| times over."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    lp = (-85.0 * torch.rand(4, 3000, generator=g, device=DEV)).requires_grad_(True)
+    ref = -85.0 * torch.rand(4, 3000, generator=g, device=DEV)
+    r = det.policy_loss(lp, lp.detach(), torch.zeros(4, device=DEV), ref_logprob=ref, kl_weight=1.0, reduction="none")
+    grad, = torch.autograd.grad(r.loss.sum(), lp)
+    q = ref.double() - lp.detach().double()
+    size = torch.exp(q) + 1 + q.abs()
+    # e^q: 2 units of the exponential, the low part and its product; two differences: 8 half steps in all
+    # (kl: up to |q| = 1 a series, 12 of its own; the gradient's parts there are at most 1)
+    within(r.kl, torch.expm1(q) - q, torch.where(q.abs() <= 1.0, 12 * U * size, 8 * U * size), "kl")
+    within(grad, -torch.expm1(q), torch.where(q.abs() <= 1.0, 12 * U * size, 8 * U * size), "gradient")
