@@ -126,6 +126,7 @@ struct MmArgs {
   // what the gradients read again
   void* gate; void* up; int64_t s_kept;
   int8_t* gate_exp; int8_t* up_exp;
+  int32_t* status;                        // int8: noted where a block is not finite
   int dt, act, save;                      // type of out, activation, what gate and up hold
 };
 
@@ -390,6 +391,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
   constexpr int ROW = FA * 16 + 4;        // floats; 4 more, or all rows would start in one bank
   static_assert(NW * 16 * ROW * 4 <= BUFS * BUF, "the rows lie in the ring's room");
   float* const own = reinterpret_cast<float*>(lds) + wave * 16 * ROW;
+  bool noted = false;                     // a block of codes that is not finite
 #pragma unroll
   for (int j = 0; j < FB; ++j) {
     wave_sync();
@@ -432,6 +434,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
           tg = top_of_8(tg);
           tu = top_of_8(tu);
           const bool bad_g = not_finite(tg), bad_u = not_finite(tu);        // int8 alone
+          noted |= in > 0 && (bad_g || bad_u);
           const int eg = int8 ? block_exponent(tg) : half_exponent(tg), eu = int8 ? block_exponent(tu) : half_exponent(tu);
           const int64_t blocks = (na + 31) / 32, at = b * a.s_kept + c;
           if ((lane & 7) == 0 && in > 0) {
@@ -450,6 +453,8 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
       }
     }
   }
+  if constexpr (GATED)
+    if (noted) a.status[0] = 1;
 #endif
 }
 
@@ -935,6 +940,7 @@ det_status det_gated_linear(const void* x, int64_t s_x, const void* w_gate, int6
   a.K = Cp;
   a.out = h; a.dt = h_dt; a.act = act; a.save = save;
   a.gate = gate; a.up = up; a.s_kept = s_kept; a.gate_exp = gate_exp; a.up_exp = up_exp;
+  if (save == DET_SAVE_INT8 && (a.status = det_device_status_word()) == nullptr) return DET_EHIP;
   launch_mm<true, false, false>(a, s);
   return hip_check(hipGetLastError(), "gated projection launch");
 }

@@ -577,7 +577,8 @@ typedef enum { DET_SAVE_NONE = 0, DET_SAVE_HALF = 1, DET_SAVE_INT8 = 2 } det_sav
  *                     8 in [C, 2^21]
  * g and u are fp32 sums over k in one fixed order (matrix-core products of 32 k
  * each, ascending), h is rounded once; values that are not finite take part as
- * IEEE arithmetic has it.  N <= 2^22, C and F <= 65536, N C and N F <= 2^34.
+ * IEEE arithmetic has it.  An int8 block that is not finite gets the exponent
+ * DET_INT8_NAN and is noted in the device status ("non-finite").  N <= 2^22, C and F <= 65536, N C and N F <= 2^34.
  * Returns DET_OK, DET_EINVAL, DET_EDTYPE or DET_EHIP.
  */
 int64_t det_gated_linear_workspace_bytes(int64_t N, int64_t C, int64_t F, det_save save, int aligned);

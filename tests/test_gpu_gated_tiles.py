@@ -74,3 +74,31 @@ def test_weight_gradients_in_two_launches(N, C, F):
     want = dg.t() @ x.double()
     assert want.abs().max() < 2 ** 24 and torch.equal(dwg, want.to(F32).to(BF16))
     assert torch.equal(dwu, torch.zeros_like(dwu))
+
+
+def test_projections_that_overflow_are_noted():
+    """A block of 8 bits that is not finite spoils the gradients of its 32 features: device_status() says so."""
+    x, wg, wu = base.operands(34, 70, 64, 100)
+    det.device_status()
+    det.gated_linear_forward(x, wg, wu, checkpoint="int8")
+    assert not det.device_status()
+    big = x.clone()
+    big[5] = 1e30                                       # finite, and so are the weights
+    for i in range(2):
+        w = [wg, wu]
+        w[i] = w[i].clone()
+        w[i][40] = 1e30
+        s = det.gated_linear_forward(big, *w, checkpoint="int8")[1]
+        assert s[i].exponents[5, 1] == -128 and (s[i].exponents == -128).sum() == 1
+        assert "nonfinite" in det.device_status()
+        det.gated_linear_forward(big[:5], *w, checkpoint="int8")
+        assert not det.device_status()
+    # in a tile of 256 x 256, too
+    x, wg, wu = base.operands(37, 2000, 1024, 2816)
+    for i in range(2):
+        w = [wg.clone(), wu.clone()]
+        det.gated_linear_forward(x, *w, checkpoint="int8")
+        assert not det.device_status()
+        w[i][2815, 1023] = float("inf")
+        s = det.gated_linear_forward(x, *w, checkpoint="int8")[1]
+        assert (s[i].exponents[:, -1] == -128).all() and "nonfinite" in det.device_status()
