@@ -38,15 +38,16 @@ void check_gated(at::IntArrayRef x, ScalarType xt, const Tensor& like, const Ten
   if (c10::multiply_integers(x) / C > DET_ROWS_MAX) refuse(what, ": more than 2^22 rows in one call");
 }
 
-// rows that the matrix product can copy 16 bytes at a time; other layouts of a
-// width that is a multiple of 64 (narrow slices, odd offsets) are copied here,
-// other widths padded by the library
+// whether the matrix product can copy rows 16 bytes at a time as they lie
+bool wide(const Tensor& r) {
+  return reinterpret_cast<uintptr_t>(r.const_data_ptr()) % 16 == 0 && r.stride(0) % 8 == 0 &&
+         r.stride(0) >= r.size(1) && r.stride(0) <= (int64_t{1} << 21);
+}
+// other layouts of a width that is a multiple of 64 (narrow slices, odd offsets)
+// are copied here, other widths padded by the library
 Tensor wide_rows(const Tensor& t) {
   const Tensor r = rows(t);
-  if (r.size(1) % 64 != 0) return r;
-  const bool fits = reinterpret_cast<uintptr_t>(r.const_data_ptr()) % 16 == 0 && r.stride(0) % 8 == 0 &&
-                    r.stride(0) >= r.size(1) && r.stride(0) <= (int64_t{1} << 21);
-  return fits || r.size(0) == 0 ? r : r.clone(at::MemoryFormat::Contiguous);
+  return r.size(1) % 64 != 0 || r.size(0) == 0 || wide(r) ? r : r.clone(at::MemoryFormat::Contiguous);
 }
 
 // what a forward call keeps of both projections: fp16 elements or int8 codes
@@ -64,8 +65,15 @@ Tensor gated_forward(const Tensor& x, const Tensor& wg, const Tensor& wu, det_ac
   if (!known(ht)) refuse(what, ": out_dtype must be float32 or bfloat16 (got ", ht, ")");
   on_gpu(x, what, "x");
   const c10::DeviceGuard guard(x.device());
-  const Tensor x2 = wide_rows(x), g2 = wide_rows(wg), u2 = wide_rows(wu);
+  Tensor x2 = rows(x), g2 = rows(wg), u2 = rows(wu);
   const int64_t N = x2.size(0), C = x2.size(1), F = wg.size(0);
+  // few tokens of which nothing is kept read the weights at any alignment, and
+  // copying these would move their bytes three times; x alone is little
+  if (!(save == DET_SAVE_NONE && (N <= 16 || (N <= 64 && !(wide(g2) && wide(u2)))))) {
+    x2 = wide_rows(x2);
+    g2 = wide_rows(g2);
+    u2 = wide_rows(u2);
+  }
   const std::vector<int64_t> shape = with_last(lead_of(x), F), blocks = with_last(lead_of(x), (F + 31) / 32);
   Tensor h = at::empty(shape, x.options().dtype(ht));
   if (save != DET_SAVE_NONE) {
@@ -133,10 +141,14 @@ GatedGrads gated_backward(const Tensor& dh, const Tensor& x, const OptTensor& x_
   const Tensor dh2 = rows(dh), x2 = !need_dw ? Tensor() : x_exp ? x.contiguous() : wide_rows(x);
   const Tensor xe = need_dw && x_exp ? x_exp->contiguous() : Tensor();
   const Tensor ge = kept.gate_exp.contiguous(), ue = kept.up_exp.contiguous();
-  Tensor g2 = wide_rows(wg), u2 = wide_rows(wu), kg = rows(kept.gate), ku = rows(kept.up);
-  if (g2.stride(0) != u2.stride(0)) {     // dx runs over both with one stride
-    g2 = g2.clone(at::MemoryFormat::Contiguous);              // contiguous() would keep a single row's stride
-    u2 = u2.clone(at::MemoryFormat::Contiguous);
+  Tensor g2 = wg, u2 = wu, kg = rows(kept.gate), ku = rows(kept.up);
+  if (need_dx) {                          // nothing else reads the weights
+    g2 = wide_rows(wg);
+    u2 = wide_rows(wu);
+    if (g2.stride(0) != u2.stride(0)) {   // dx runs over both with one stride
+      g2 = g2.clone(at::MemoryFormat::Contiguous);            // contiguous() would keep a single row's stride
+      u2 = u2.clone(at::MemoryFormat::Contiguous);
+    }
   }
   if (kg.stride(0) != ku.stride(0)) {
     kg = kg.contiguous();

@@ -102,3 +102,40 @@ def test_projections_that_overflow_are_noted():
         w[i][2815, 1023] = float("inf")
         s = det.gated_linear_forward(x, *w, checkpoint="int8")[1]
         assert (s[i].exponents[:, -1] == -128).all() and "nonfinite" in det.device_status()
+
+
+def bytes_taken(call):
+    call()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    out = call()
+    return torch.cuda.max_memory_allocated() - before, out
+
+
+@pytest.mark.parametrize("N", [1, 16, 17, 64])
+def test_few_tokens_copy_no_weights(N):
+    """Weights that are column slices at odd offsets: 64 tokens at most read them as they lie."""
+    C, F = 1024, 3000
+    x, wg, wu = base.operands(35, N, C, F)
+    want = det.gated_linear(x, wg, wu)
+    odd = lambda t: torch.zeros(F, C + 3, device=DEV, dtype=BF16)[:, 1:C + 1].copy_(t)
+    g, u = odd(wg), odd(wu)
+    for pair in ((g, u), (g, wu), (wg, u)):
+        taken, h = bytes_taken(lambda: det.gated_linear(x, *pair))
+        assert torch.equal(h, want) and taken < F * C
+
+
+@pytest.mark.parametrize("ck", [None, "int8"])
+def test_weight_gradients_copy_no_weights(ck):
+    """The weights' own gradients do not read them: slices and unequal strides stay as they are."""
+    N, C, F = 64, 1024, 3000
+    x, wg, wu = base.operands(36, N, C, F)
+    h, s = det.gated_linear_forward(x, wg, wu, checkpoint=ck)
+    want = det.gated_linear_backward(h, x, wg, wu, s)
+    room = lambda t, off, pad: torch.zeros(F, C + pad, device=DEV, dtype=BF16)[:, off:off + C].copy_(t)
+    outputs = 2 * F * C * 2 + 2 * N * (F + 128) * 2
+    for pair in ((room(wg, 1, 3), room(wu, 2, 5)), (wg, room(wu, 8, 16))):
+        taken, got = bytes_taken(lambda: det.gated_linear_backward(h, x, *pair, s, need_dx=False))
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2]) and taken < outputs + F * C
+        assert torch.equal(det.gated_linear_backward(h, x, *pair, s)[0], want[0])
