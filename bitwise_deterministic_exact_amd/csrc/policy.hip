@@ -484,7 +484,8 @@ __global__ __launch_bounds__(256) void k_policy_grad(PolicyArgs a) {
 //   z = beta (s_chosen - s_rejected) - margin
 //
 // One workgroup to a pair: half of its waves to each side, which take parts of
-// 512 tokens in turn.
+// 512 tokens in turn; two of them where the side has up to 2048 tokens, whatever
+// the other one has: the order of a side's sum is its own length's.
 
 struct Side {
   const float* lp; int64_t s_lp;
@@ -512,9 +513,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_preference(PreferenceArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t p = blockIdx.x;
   const Side& s = a.side[wave < WAVES / 2 ? 0 : 1];
+  const int turns = s.T <= 4 * PART ? 2 : WAVES / 2, turn = wave % (WAVES / 2);
   double sum = 0.0;
   int count = 0;
-  for (int64_t t0 = static_cast<int64_t>(wave % (WAVES / 2)) * PART; t0 < s.T; t0 += PART * (WAVES / 2)) {
+  for (int64_t t0 = turn < turns ? static_cast<int64_t>(turn) * PART : s.T; t0 < s.T; t0 += PART * turns) {
 #pragma unroll
     for (int v = 0; v < VECS; ++v) {
       const int64_t t = t0 + v * 256 + lane * 4;
@@ -785,7 +787,6 @@ det_status det_preference_loss(const float* chosen, int64_t s_chosen, const floa
   a.status = det_device_status_word();
   if (a.status == nullptr) return DET_EHIP;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  // the lengths alone decide, for the sums' order follows
   if (std::max(T_chosen, T_rejected) <= 4 * PART)
     hipLaunchKernelGGL(k_preference<4>, dim3(static_cast<unsigned>(P)), dim3(256), 0, s, a);
   else hipLaunchKernelGGL(k_preference<16>, dim3(static_cast<unsigned>(P)), dim3(1024), 0, s, a);

@@ -711,8 +711,8 @@ det_status det_policy_loss_grad(const float* logprob, int64_t s_logprob, const f
  *   loss, chosen_reward, rejected_reward   [P] fp32; reward = beta s
  *   slope             [P][2] fp32 for the gradient: the derivative of the pair's
  *                     loss in each token that counts of its two sides
- * Sums and the loss are formed in 64 bits, in an order that the two lengths
- * alone decide.  A loss that is not finite is noted in the device status
+ * Sums and the loss are formed in 64 bits, a side's sum in an order that its own
+ * length alone decides.  A loss that is not finite is noted in the device status
  * ("non-finite").  P <= 2^22, lengths <= 2^24, P times a length <= 2^32.
  * Returns DET_OK, DET_EINVAL or DET_EHIP.
  */

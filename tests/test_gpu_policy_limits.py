@@ -105,3 +105,20 @@ def test_estimates_of_far_differences():
     # (kl: up to |q| = 1 a series, 12 of its own; the gradient's parts there are at most 1)
     within(r.kl, torch.expm1(q) - q, torch.where(q.abs() <= 1.0, 12 * U * size, 8 * U * size), "kl")
     within(grad, -torch.expm1(q), torch.where(q.abs() <= 1.0, 12 * U * size, 8 * U * size), "gradient")
+
+
+@pytest.mark.parametrize("T", [4, 600, 1500, 2048, 2050, 9000])
+def test_an_answers_reward_does_not_depend_on_the_other_answer(T):
+    g = torch.Generator(device=DEV).manual_seed(4)
+    # what is left of sums that cancel shows their order
+    x = torch.randn(5, T // 2, generator=g, device=DEV) * torch.exp(20 * torch.randn(5, T // 2, generator=g, device=DEV))
+    x = x.clamp(-1e30, 1e30)
+    x = torch.cat([x, -x], 1)[:, torch.randperm(T, generator=g, device=DEV)]
+    other = -torch.rand(5, 30, generator=g, device=DEV)
+    wide = torch.zeros(5, 7000, device=DEV)
+    wide[:, :30] = other
+    mask = torch.arange(7000, device=DEV).expand(5, 7000) < 30
+    short, long_ = det.preference_loss(x, other), det.preference_loss(x, wide, rejected_mask=mask)
+    assert torch.equal(short.chosen_reward, long_.chosen_reward)
+    assert torch.equal(det.preference_loss(other, x).rejected_reward, short.chosen_reward)
+    assert torch.equal(det.preference_loss(wide, x, chosen_mask=mask).rejected_reward, short.chosen_reward)
