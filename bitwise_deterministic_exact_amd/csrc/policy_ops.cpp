@@ -264,9 +264,10 @@ struct PreferenceFn : torch::autograd::Function<PreferenceFn> {
                                bool by_length) {
     const Preference p = preference_forward(chosen, rejected, ref_chosen, ref_rejected, mask_chosen, mask_rejected,
                                             {static_cast<det_preference>(kind), beta, margin, smooth, by_length});
-    // the slopes are what the gradient needs; the log probabilities stand for the shapes and the graph
-    ctx->save_for_backward({chosen, rejected, p.slope, mask_chosen.value_or(Tensor()),
-                            mask_rejected.value_or(Tensor())});
+    // the slopes and the shapes are what the gradient needs: the log probabilities are not kept
+    ctx->save_for_backward({p.slope, mask_chosen.value_or(Tensor()), mask_rejected.value_or(Tensor())});
+    ctx->saved_data["chosen"] = chosen.sizes().vec();
+    ctx->saved_data["rejected"] = rejected.sizes().vec();
     ctx->set_materialize_grads(false);
     ctx->mark_non_differentiable({p.chosen, p.rejected});
     return {p.loss, p.chosen, p.rejected};
@@ -277,10 +278,11 @@ struct PreferenceFn : torch::autograd::Function<PreferenceFn> {
     Tensor dc, dr;
     if (grads[0].defined()) {
       const at::NoGradGuard no_grad;
-      std::tie(dc, dr) = preference_backward(grads[0], s[2], s[0].sizes(), s[1].sizes(), opt(s[3]), opt(s[4]),
+      std::tie(dc, dr) = preference_backward(grads[0], s[0], ctx->saved_data["chosen"].toIntVector(),
+                                             ctx->saved_data["rejected"].toIntVector(), opt(s[1]), opt(s[2]),
                                              ctx->needs_input_grad(0), ctx->needs_input_grad(1));
     }
-    variable_list r = once({dc, dr}, {s[0], s[1], grads[0]}, "preference_loss");
+    variable_list r = once_at_node({dc, dr}, grads, "preference_loss");
     r.resize(11);
     return r;
   }

@@ -122,3 +122,22 @@ def test_an_answers_reward_does_not_depend_on_the_other_answer(T):
     assert torch.equal(short.chosen_reward, long_.chosen_reward)
     assert torch.equal(det.preference_loss(other, x).rejected_reward, short.chosen_reward)
     assert torch.equal(det.preference_loss(wide, x, chosen_mask=mask).rejected_reward, short.chosen_reward)
+
+
+def test_a_preference_loss_keeps_no_log_probabilities():
+    g = torch.Generator(device=DEV).manual_seed(5)
+    base = [(-torch.rand(6, T, generator=g, device=DEV)).requires_grad_(True) for T in (700, 33)]
+    mask = torch.rand(6, 700, generator=g, device=DEV) < 0.5
+    want = torch.autograd.grad(det.preference_loss(*base, chosen_mask=mask).loss.sum(), base)
+    sizes = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (sizes.append((t.dtype, t.numel())), t)[1], lambda t: t):
+        det.preference_loss(*base, chosen_mask=mask)
+    assert sorted(sizes, key=str) == sorted([(torch.float32, 12), (torch.bool, 6 * 700)], key=str)
+    # the gradient does not need them: they may change in place
+    sides = [t * 1.0 for t in base]
+    loss = det.preference_loss(*sides, chosen_mask=mask).loss.sum()
+    with torch.no_grad():
+        for t in sides:
+            t.add_(1.0)
+    for a, b in zip(torch.autograd.grad(loss, base), want):
+        assert torch.equal(a, b)
