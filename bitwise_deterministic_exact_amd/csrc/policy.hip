@@ -762,7 +762,7 @@ det_status det_preference_loss(const float* chosen, int64_t s_chosen, const floa
   if (T_chosen < 0 || T_rejected < 0) return fail(DET_EINVAL, "negative length");
   if (!known_kind(kind)) return fail(DET_EINVAL, "unknown kind of preference loss %d", kind);
   if (!(beta > 0.0) || !(beta < 1e6)) return fail(DET_EINVAL, "beta must lie in (0, 1e6)");
-  if (!(fabs(margin) < 1e6) || (margin != 0.0 && kind == DET_PREFER_IPO))
+  if (!(fabs(margin) < INFINITY) || (margin != 0.0 && kind == DET_PREFER_IPO))
     return fail(DET_EINVAL, "margin must be finite, and 0 for ipo");
   if (!(label_smoothing >= 0.0) || !(label_smoothing <= 0.5) || (label_smoothing != 0.0 && kind != DET_PREFER_SIGMOID))
     return fail(DET_EINVAL, "label_smoothing must lie in [0, 0.5], and be 0 unless sigmoid");

@@ -3,6 +3,8 @@
 // points of libdetgemm.so (include/detgemm.h).
 #include "ops_common.h"
 
+#include <cmath>
+
 void bind_policy(py::module_& m);
 
 namespace {
@@ -209,7 +211,7 @@ Preference preference_forward(const Tensor& chosen, const Tensor& rejected, cons
   check_mask(mask_chosen, chosen.sizes(), chosen, "chosen_mask", what);
   check_mask(mask_rejected, rejected.sizes(), chosen, "rejected_mask", what);
   if (!(o.beta > 0.0) || !(o.beta < 1e6)) refuse(what, ": beta must lie in (0, 1e6) (got ", o.beta, ")");
-  if (!(std::abs(o.margin) < 1e6)) refuse(what, ": margin must be finite (got ", o.margin, ")");
+  if (!std::isfinite(o.margin)) refuse(what, ": margin must be finite (got ", o.margin, ")");
   if (o.margin != 0.0 && o.kind == DET_PREFER_IPO) refuse(what, ": ipo takes no margin");
   if (!(o.smooth >= 0.0) || !(o.smooth <= 0.5))
     refuse(what, ": label_smoothing must lie in [0, 0.5] (got ", o.smooth, ")");

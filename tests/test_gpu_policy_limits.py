@@ -141,3 +141,14 @@ def test_a_preference_loss_keeps_no_log_probabilities():
             t.add_(1.0)
     for a, b in zip(torch.autograd.grad(loss, base), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge"])
+def test_far_margins(kind):
+    c, r = torch.zeros(3, 4, device=DEV, requires_grad=True), torch.zeros(3, 4, device=DEV)
+    for margin in (1e6, 3e7, -2e9):
+        y = det.preference_loss(c, r, kind=kind, margin=margin)
+        want = max(0.0, margin) if kind == "sigmoid" else max(0.0, 1 + margin)
+        within(y.loss, torch.full((3,), want, dtype=torch.float64, device=DEV), U * want, "loss")
+        grad, = torch.autograd.grad(y.loss.sum(), c)
+        assert (grad == (-torch.tensor(0.1).item() if margin > 0 else 0.0)).all()
