@@ -15,7 +15,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "exact_sum.h"
+#include "rowops.h"
 
 // every fused multiply-add below is written as one: the compiler forms none
 #pragma clang fp contract(off)
@@ -590,11 +590,13 @@ __global__ __launch_bounds__(T, 4) void k_norm_grad_wide(NormGradArgs a) {
 
 // ---------------------------------------------------------------- the exact sum of the chunks
 //
-// A column's digits (exact_sum.h) live in LDS; the waves of a workgroup add
-// into them with 64-bit integer atomics, whose order cannot matter.  512 chunks
-// of 8192 columns take 16 us (2.1 TB/s); sums kept in registers first took 3 us
-// longer.
-constexpr int COL_WAVES = 16, SPLIT_MAX = 64;
+// An fp32 value is sig 2^(e - 150) with e = max(exponent field, 1): it starts
+// at bit o = e + 148 of the accumulator (digit 0 weighs 2^-298) and its 24
+// bits touch digits o/32 and o/32 + 1, 4..13 of the 18.  A column's digits
+// live in LDS; the waves of a workgroup add into them with 64-bit integer
+// atomics, whose order cannot matter.  512 chunks of 8192 columns take 16 us
+// (2.1 TB/s); sums kept in registers first took 3 us longer.
+constexpr int DIG0 = 4, NDIG = 10, COL_WAVES = 16, SPLIT_MAX = 64;
 
 struct ColArgs {
   const float* parts;                     // [chunks][2][C]
@@ -608,11 +610,65 @@ struct ColArgs {
   int32_t* status;
 };
 
+// digits to a value of the gradient's type, rounded once (nearest-even):
+// carries first, then the top 24 bits (bf16: 8) with the rest as a sticky bit.
+// By way of fp32 a bf16 gradient would be rounded twice: 1 + 2^-8 + 2^-30 to 1.
+template <class D>
+__device__ __forceinline__ float round_column(D digit, bool bf16) {
+  uint32_t w[NDIG + 1];
+  int64_t carry = 0;
+#pragma unroll
+  for (int j = 0; j < NDIG; ++j) {
+    const int64_t v = digit(j) + carry;
+    w[j] = static_cast<uint32_t>(v);
+    carry = v >> 32;
+  }
+  const bool neg = carry < 0;
+  w[NDIG] = static_cast<uint32_t>(carry);                     // |carry| < 2^31: the sums stay far below 2^62
+  if (neg) {
+    uint32_t c = 1u;
+#pragma unroll
+    for (int j = 0; j <= NDIG; ++j) {
+      const uint32_t v = ~w[j] + c;
+      c = (c != 0u && v == 0u) ? 1u : 0u;
+      w[j] = v;
+    }
+  }
+  int top = -1;
+  uint32_t hi = 0u, lo = 0u;                                  // the highest nonzero word and the one below it
+#pragma unroll
+  for (int j = 0; j <= NDIG; ++j)
+    if (w[j] != 0u) {
+      top = j;
+      hi = w[j];
+      lo = j > 0 ? w[j > 0 ? j - 1 : 0] : 0u;
+    }
+  bool sticky = false;                                        // any bit below those two
+#pragma unroll
+  for (int j = 0; j <= NDIG; ++j)
+    if (j < top - 1 && w[j] != 0u) sticky = true;
+  if (top < 0) return 0.0f;
+  uint64_t win = (static_cast<uint64_t>(hi) << 32) | lo;      // its bit 0 weighs 2^(32 (DIG0 + top - 1) - 298)
+  int q = 32 * (DIG0 + top - 1) - 298;
+  const int n = 64 - __builtin_clzll(win);                    // n >= 33
+  // the bits below the kept ones; subnormal results keep 2^-149 (bf16: 2^-133)
+  const int cut = bf16 ? max(n - 8, -133 - q) : max(n - 24, -149 - q);
+  if (cut > 64) return neg ? -0.0f : 0.0f;                    // bf16, top = 0: 69, and less than 2^-138
+  if (cut > 0) {
+    const uint64_t rest = win & ((1ull << cut) - 1ull), half = 1ull << (cut - 1);
+    win >>= cut;
+    q += cut;
+    if (rest > half || (rest == half && (sticky || (win & 1ull)))) win += 1ull;
+  }
+  const float mag = ldexpf(static_cast<float>(static_cast<uint32_t>(win)), q);
+  return neg ? -mag : mag;
+}
+
 template <class D>
 __device__ __forceinline__ void write_column(const ColArgs& a, int64_t col, D digit, bool bad) {
   void* const out = col < a.C ? a.dw : a.db;
   if (out != nullptr) {
-    const float v = bad ? NAN : round_digits(digit, a.w_dt == DET_BF16);
+    const float v = bad ? NAN : round_column(digit, a.w_dt == DET_BF16);
     store_elem(a.w_dt, out, col < a.C ? col : col - a.C, v);
   }
   if (a.digits != nullptr) {
@@ -647,8 +703,20 @@ __global__ __launch_bounds__(64 * COL_WAVES) void k_norm_columns(ColArgs a) {
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         const uint32_t u = k0 + i * STEP < end ? __float_as_uint(v[i]) : 0u;
-        if (((u >> 23) & 0xFFu) == 0xFFu) bad[lane] = 1;
-        else add_digits(u, [&](int j, int64_t v) { atomicAdd(&dg[j][lane], static_cast<unsigned long long>(v)); });
+        const uint32_t ef = (u >> 23) & 0xFFu;
+        if (ef == 0xFFu) {
+          bad[lane] = 1;
+        } else if (u << 1) {
+          uint32_t sig = u & 0x7FFFFFu;
+          if (ef != 0u) sig |= 0x800000u;
+          const uint32_t o = max(ef, 1u) + 148u;
+          const uint64_t wide = static_cast<uint64_t>(sig) << (o & 31u);
+          int64_t lo = static_cast<int64_t>(wide & 0xFFFFFFFFull), hi = static_cast<int64_t>(wide >> 32);
+          if (u >> 31) { lo = -lo; hi = -hi; }
+          const int j = static_cast<int>(o >> 5) - DIG0;
+          atomicAdd(&dg[j][lane], static_cast<unsigned long long>(lo));
+          if (hi != 0) atomicAdd(&dg[j + 1][lane], static_cast<unsigned long long>(hi));
+        }
       }
     }
   }
