@@ -390,20 +390,22 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_policy_join(PolicyArgs a) {
   });
 }
 
-// A few short rows in one launch: the same sums, read from the LDS.  8 x 300: 8.6 us,
-// 9.0 and a launch between in two (and 3 us of the host).
-constexpr int FEW_ROWS = 32;
+// A few short rows in one launch, one to a wave: the same sums, read from the LDS.
+// In a graph, us a call in one launch and in two: 8 x 300 9.1 and 9.9, 16 x 512 10.0
+// and 9.4; two rows to a wave 32 x 64 15.8 and 10.2, 32 x 512 14.4 and 9.4.  A launch
+// takes 3 us of the host, which bounds the call outside of graphs.
+constexpr int FEW_ROWS = JOIN_THREADS / 64;
 __global__ __launch_bounds__(JOIN_THREADS) void k_policy_few(PolicyArgs a) {
   __shared__ JoinTotals s;
   __shared__ double2 sums[FEW_ROWS];
   __shared__ int2 counts[FEW_ROWS];
   clear(s);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int64_t b = wave; b < a.B; b += JOIN_THREADS / 64) {
-    const Part p = part_of(a, {b, 0, 0}, lane);
+  if (wave < a.B) {
+    const Part p = part_of(a, {wave, 0, 0}, lane);
     if (lane == 0) {
-      sums[b] = double2{p.loss, p.kl};
-      counts[b] = int2{p.clipped, p.count};
+      sums[wave] = double2{p.loss, p.kl};
+      counts[wave] = int2{p.clipped, p.count};
     }
   }
   __syncthreads();
