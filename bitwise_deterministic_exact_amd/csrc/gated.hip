@@ -55,7 +55,7 @@ __device__ __forceinline__ Act act_of(float g) {
     return {g * s.s, fmaf(g, slope, s.s)};
   } else {
     // Phi(-|g|) = e^(-g^2 / 2) E / 2 with E = erfcx(|g| / sqrt 2) = t p(t), t = 1 / (1 + |g| / sqrt 8):
-    // p of degree 8 is fitted to E / t for |g| up to 14.7, off by 4.3e-8 of it at most; with the roundings
+    // p of degree 8 is fitted to E / t for |g| up to 14.7, off by 5.9e-8 of it at most; with the roundings
     // Phi is within 4 units.  The square is carried in two parts, as a rounded one costs g^2 / 2 half
     // units; from 20 on e^(-g^2 / 2) is 0.  (By erfcf, and e^(-g^2 / 2) beside it, 2048 x 1024 x 2816 forward
     // took 41 us, 35.5 so, and dx with dg and du 52.5, 46.5.)
@@ -214,8 +214,10 @@ struct Tile {
   __device__ __forceinline__ void copy(char* to, int wave) {
     if constexpr (BY_K) {
       // No branch: one would keep the copies from going between the MFMAs.  Without
-      // rows, down to 127 + (BUFS - 1) KS <= 511 past the end, the bytes are at most
-      // cols - stride <= 0.
+      // rows the bytes are at most cols - stride <= 0, and the product fits 32 bits: A is
+      // at most 511 rows past its end (in dx 127 up to Fp and then (BUFS - 1) KS <= 384; in
+      // dw it starts anew at K), of up to 2^22 bytes each; B, dg and du in dw, at most 255
+      // + 384, of 4 Fp <= 2^18 bytes.
       const __amdgpu_buffer_rsrc_t b = buffer_of(next, max(0, (min(left, KS) - 1) * static_cast<int>(stride) + cols));
 #pragma unroll
       for (int j = 0; j < COPIES; ++j)
@@ -256,6 +258,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void k_mm(MmArgs a) {
   constexpr int NW = WA * WB, TA = WA * FA * 16, TB = WB * FB * 16, TH = GATED ? TA / 2 : TA;
   using TileA = Tile<A_BY_K, TA, NW, KS>;
   using TileB = Tile<B_BY_K, TB, NW, KS>;
+  static_assert((BUFS - 1) * KS <= 384, "stages past the last one: how far TileA and TileB run past their rows");
   constexpr int BUF = TileA::BYTES + TileB::BYTES, COPIES = TileA::COPIES + TileB::COPIES;
   __shared__ __attribute__((aligned(1024))) char lds[BUFS * BUF];
   const int lane = threadIdx.x & 63;
@@ -662,7 +665,7 @@ __global__ __launch_bounds__(256) void k_clear(uint16_t* p, int64_t n) {
 // be copied first.  64 x 4096 x 11008: 94 us against 45 with tiles, 48 x 2048 x
 // 5461 22 against 10.5, with rows of 2047 22 against 30; one token 34 us.
 constexpr int64_t FEW = 16, FEW_COPIED = 64;
-constexpr int64_t STRIDE_MAX = 1 << 21;   // elements: 512 rows before and after an operand's end lie within 2^31 bytes
+constexpr int64_t STRIDE_MAX = 1 << 21;   // elements: 512 rows of x or of the weights lie within 2^31 bytes
 
 int64_t up_to(int64_t v, int64_t m) { return ceil_div(v, m) * m; }
 int64_t room(int64_t bytes) { return up_to(bytes, 256); }

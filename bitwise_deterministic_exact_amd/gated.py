@@ -81,7 +81,9 @@ def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, a
 class DetGatedLinear(torch.nn.Module):
     """gated_linear with learned bfloat16 weights [hidden_features,
     in_features]; a DetLinear(hidden_features, in_features) after it completes
-    a feed-forward block."""
+    a feed-forward block.  Unlike DetLinear's its sums are float32: repeatable, a
+    token's the same in any batch, but the weights' gradients depend on how the
+    rows are cut into calls."""
 
     def __init__(self, in_features: int, hidden_features: int, activation: str = "silu", device=None,
                  out_dtype: Optional[torch.dtype] = None, checkpoint: Optional[str] = None):
