@@ -3,12 +3,12 @@
 // with its gradient.
 //
 // One pass over [rows][T] arrays each, bound by HBM on large batches and by the
-// latency of a launch on small ones: 1024 x 8192 tokens with a reference 31 us and
-// 8 to join the rows (143 MB; the exponentials, series and differences in 64 bits
-// take 81 instructions a token, about as long), 30 for the gradient (176 MB, 5.8
-// TB/s); 2 x 2048 x 4096 preference 29 and 13.5 (5.2 and 6.2 TB/s).  A row's sums
-// are formed in 64 bits, in an order that T alone decides; sums over rows are
-// exact (exact_sum.h): any order of the rows gives the same bits.
+// latency of a launch on small ones: 1024 x 8192 tokens with a reference 27 us and
+// 8 to join the rows (143 MB, 5.2 TB/s; the exponentials, series and differences in
+// 64 bits take 79 instructions a token), 29 for the gradient (176 MB, 6.1 TB/s);
+// 2 x 2048 x 4096 preference 29 and 14 (5.2 and 6.0 TB/s).  A row's sums are formed
+// in 64 bits, in an order that T alone decides; sums over rows are exact
+// (exact_sum.h): any order of the rows gives the same bits.
 #include <math.h>
 
 #include <algorithm>
