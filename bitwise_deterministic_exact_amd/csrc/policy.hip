@@ -262,8 +262,9 @@ __global__ __launch_bounds__(256) void k_policy(PolicyArgs a) {
 }
 
 // Rows joined: a row's pieces are added in 64 bits, in ascending order (up to 16
-// of them) or over the lanes of a wave; the rows' values are added exactly.  Three sums (loss, KL, clipped) of NDIG digits, their values
-// that are not finite by kind, and two counts.
+// of them) or over the lanes of a wave; the rows' values are added exactly.  Three
+// sums (loss, KL, clipped) of NDIG digits, their values that are not finite by
+// kind, and two counts.
 constexpr int SUMS = 3, JOINED = SUMS * NDIG + SUMS + 2, SERIAL = 16, AHEAD = 8, JOIN_THREADS = 1024;
 
 struct JoinTotals {
