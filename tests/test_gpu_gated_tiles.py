@@ -1,7 +1,6 @@
 """The gated projection's largest tiles, which carry prompts and large training
 steps: 256 x 256 and 128 x 256 outputs, ragged both ways and on widths that are
-padded, with every kind of kept projections, and weight gradients in two
-launches.  And what a call notes and copies beside its products."""
+padded, with every kind of kept projections, and products in two launches.  And what a call notes and copies beside its products."""
 import pytest
 import torch
 
@@ -14,8 +13,10 @@ DEV = "cuda:0"
 BF16, F32 = torch.bfloat16, torch.float32
 
 # forward in tiles of 256 x 256 and dw of 128 x 256; forward of 128 x 256 and dw of 256 x 256; dx of 128 x 256, forward and dw of
-# 256 x 256; dx of 256 x 256
-SIZES = [(2000, 1023, 2801), (1100, 2100, 2817), (3000, 2112, 2112), (8200, 1030, 260)]
+# 256 x 256; dx of 256 x 256; two launches, the second with smaller tiles: of the forward's features, of its rows, of dx' columns,
+# of its rows
+SIZES = [(2000, 1023, 2801), (1100, 2100, 2817), (3000, 2112, 2112), (8200, 1030, 260), (1021, 1537, 4099), (5000, 1100, 1000),
+         (4100, 2100, 700), (2050, 2111, 1100)]
 
 
 @pytest.mark.parametrize("N,C,F", SIZES)
